@@ -431,6 +431,109 @@ kq_status kq_flipflop(const uint16_t* X, int64_t ldx, const uint16_t* G, int64_t
                       int64_t n, int64_t m, int iters, float* A, float* B, void* ws,
                       size_t ws_bytes, double* phase_ms, void* stream);
 
+/*
+ * Microscaled 4-bit floating point (MXFP4): a second deploy format for processed layers, read
+ * by the matrix instructions as it is held, for any number of tokens.
+ *
+ * A row of n values is held in blocks of 32 (the last may be short).  With a the block's
+ * largest magnitude:
+ *   e = max(floor(log2 a) - 2, -127)        the block's scale 2^e, held as the byte e + 127
+ *   element = x / 2^e, rounded to nearest (ties to the even code) on the E2M1 magnitudes
+ *             {0, 0.5, 1, 1.5, 2, 3, 4, 6}; magnitudes above 6 become 6
+ *             (4 bits: sign, two exponent bits, one mantissa bit)
+ * A block with an infinity or a NaN has the scale byte 255 and zero elements: all its values
+ * are NaN, and so is every output that it enters.
+ *
+ * Layout of `rows` quantised rows, with np = n rounded up to a multiple of 128:
+ *   codes   uint8 [rows][np / 2], contiguous: column 2i in the low, 2i + 1 in the high nibble;
+ *           columns at and past n are zero
+ *   scales  uint8 [np / 128][rows][4], contiguous: the byte of (row r, block b) is at
+ *           ((b / 4) * rows + r) * 4 + b % 4
+ * Both 16-byte aligned.
+ *
+ * Rotated activations: with D = diag(d) and P = blockdiag(Had_b) diag(S) / sqrt(b) as in
+ * kq_biip_rotate, every call below that takes d, sign and had quantises
+ *   x~ = P D^-1 x,
+ * so a weight matrix processed by kq_biip_rotate in mode KQ_BIIP_IN_ONLY (W~ = W D P^T) and
+ * quantised gives y = Q(x~) Q(W~)^T ~ W x with no work on the output side.  In fp32:
+ * f_i = S_i / d_i, x_i f_i, butterflies with ascending strides, times 1 / sqrt(b), each
+ * operation rounded by itself.
+ *   d      device fp32 [n], or NULL for 1;  sign  device int8 +-1 [n], or NULL for +1
+ *   had    Hadamard block: a power of 2 (<= 8192) dividing n; 1: none; 0: the largest power of
+ *          2 dividing n, as kq_biip_rotate (KQ_ENOTIMPL when that exceeds 8192)
+ */
+enum {
+  KQ_F32 = 0,    /* fp32 */
+  KQ_BF16 = 1,   /* bf16 bit patterns */
+  KQ_MXFP4 = 2   /* quantised rows (codes and scales) */
+};
+
+/*
+ * kq_mxfp4_quantize -- rows to MXFP4, with the input side of the incoherence processing.
+ *
+ *   src        device, rows x n of src_type (KQ_F32 or KQ_BF16), leading dim ld >= n, aligned to
+ *              its type (16-byte aligned rows are read faster)
+ *   codes, scales  device, as laid out above
+ *   values_opt device bf16, rows x n (leading dim ldv >= n), or NULL: the values that the codes
+ *              and scales stand for (exact in bf16)
+ * Sizes: 0 <= rows <= 2^30, 1 <= n <= 2^24.  Asynchronous on `stream`.
+ */
+kq_status kq_mxfp4_quantize(const void* src, int src_type, int64_t rows, int64_t n, int64_t ld,
+                            const float* d, const int8_t* sign, int64_t had, uint8_t* codes,
+                            uint8_t* scales, uint16_t* values_opt, int64_t ldv, void* stream);
+
+/*
+ * kq_mxfp4_workspace -- workspace bytes of kq_mxfp4_linear and kq_mxfp4_experts for `rows` rows
+ * of n activations: room for the quantised rows, rows * ceil(n / 128) * 68 (any rows not
+ * quantised yet; quantised ones need none).
+ */
+kq_status kq_mxfp4_workspace(int64_t rows, int64_t n, size_t* bytes);
+
+/*
+ * kq_mxfp4_linear -- a layer held in MXFP4 applied to rows of activations:
+ *   y[t, o] = sum_i Q(x~)[t, i] W[o, i],   sums in fp32, rounded once to y_type.
+ *
+ *   x        device, rows x in of x_type, leading dim ldx.  KQ_F32 and KQ_BF16: activations, which
+ *            the call rotates and quantises (x_scales NULL).  KQ_MXFP4: codes as laid out above
+ *            (ldx = in rounded up to 128), x_scales their scales; d, sign NULL, had 0 or 1
+ *   w_codes, w_scales  device, the layer's out rows of `in` values, as laid out above
+ *   y        device, rows x out of y_type (KQ_F32 or KQ_BF16), leading dim ldy >= out; must not
+ *            overlap the inputs
+ *   ws       device workspace, 16-byte aligned, ws_bytes >= kq_mxfp4_workspace(rows, in) unless
+ *            x_type is KQ_MXFP4 (then it may be NULL)
+ * Sizes: 0 <= rows <= 2^30, 1 <= in, out <= 2^24.  Asynchronous on `stream`; the same inputs
+ * give the same bits.
+ */
+kq_status kq_mxfp4_linear(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                          const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                          const uint8_t* w_codes, const uint8_t* w_scales, int64_t out, void* y,
+                          int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kq_mxfp4_experts -- kq_mxfp4_linear with one of several layers per row (a mixture of experts):
+ * for every slot s in [offsets[e], offsets[e + 1]),
+ *   y[s, o] = sum_i Q(x~)[index[s], i] W_e[o, i].
+ *
+ *   x, ..., had  as for kq_mxfp4_linear (the experts share d, sign and had); quantised once per row
+ *   index    device int32 [slots]: the row of x that a slot reads; one outside [0, rows) reads as
+ *            a row of zeros.  NULL: slot s reads row s (slots <= rows)
+ *   offsets  device int32 [experts + 1], non-decreasing, within [0, slots]: slots sorted by
+ *            expert.  An expert may have none; slots before offsets[0] and from
+ *            offsets[experts] on are not written.  Offsets that leave [0, slots] are cut to it;
+ *            where they decrease, the slots between are unspecified
+ *   w_codes, w_scales  device: experts layers of out rows, one after another (codes
+ *            [experts][out][np / 2], scales [experts][np / 128][out][4])
+ *   y        device, slots x out
+ *   ws       as for kq_mxfp4_linear (by the rows of x, not by slots)
+ * Sizes: as kq_mxfp4_linear, 0 <= slots <= 2^30, 1 <= experts <= 4096.  The offsets stay on the
+ * device: nothing is read back.
+ */
+kq_status kq_mxfp4_experts(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                           const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                           const int32_t* index, int64_t slots, const int32_t* offsets, int experts,
+                           const uint8_t* w_codes, const uint8_t* w_scales, int64_t out, void* y,
+                           int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

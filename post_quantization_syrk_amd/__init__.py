@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(HERE, "libkq.so")
 
 KQ_OK, KQ_EINVAL, KQ_ESHAPE, KQ_ENOTSPD, KQ_EWORKSPACE, KQ_ENOTIMPL, KQ_EHIP = range(7)
 KQ_BIIP_FULL, KQ_BIIP_NO_RESCALE, KQ_BIIP_IN_ONLY, KQ_BIIP_OUT_ONLY = range(4)
+KQ_F32, KQ_BF16, KQ_MXFP4 = range(3)
 STATUS_NAMES = {0: "KQ_OK", 1: "KQ_EINVAL", 2: "KQ_ESHAPE", 3: "KQ_ENOTSPD", 4: "KQ_EWORKSPACE",
                 5: "KQ_ENOTIMPL", 6: "KQ_EHIP"}
 
@@ -28,7 +29,8 @@ EXPORTED = ("kq_version", "kq_last_error", "kq_accumulate_hessian", "kq_sensitiv
             "kq_quantize_layer_noalloc", "kq_quantize_layer_async",
             "kq_allocate_bits", "kq_deploy_linear", "kq_deploy_linear_group",
             "kq_flipflop_workspace", "kq_flipflop", "kq_quantize_two_sided_workspace",
-            "kq_quantize_two_sided", "kq_testing_select")
+            "kq_quantize_two_sided", "kq_mxfp4_quantize", "kq_mxfp4_workspace", "kq_mxfp4_linear",
+            "kq_mxfp4_experts", "kq_testing_select")
 
 
 class KQError(RuntimeError):
@@ -83,6 +85,12 @@ _SIGS = {
                                _sz, _vp, _vp], _int),
     "kq_flipflop": ([_vp, _i64, _vp, _i64, _i64, _i64, _i64, _int, _vp, _vp, _vp, _sz,
                      ctypes.POINTER(ctypes.c_double), _vp], _int),
+    "kq_mxfp4_quantize": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _vp, _vp, _vp, _i64, _vp], _int),
+    "kq_mxfp4_workspace": ([_i64, _i64, ctypes.POINTER(_sz)], _int),
+    "kq_mxfp4_linear": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64, _vp, _int, _i64,
+                         _vp, _sz, _vp], _int),
+    "kq_mxfp4_experts": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp,
+                          _i64, _vp, _int, _i64, _vp, _sz, _vp], _int),
     "kq_testing_select": ([_int, _i64], _int),
 }
 
@@ -416,3 +424,127 @@ def kq_quantize_two_sided(p: QuantParams, W, HX, HG, packed, scales, zeros, ws=N
         _dev_ptr(ws, "ws", (torch.uint8,)), ws.numel(), _dev_ptr(codes, "codes", (torch.uint8,), True),
         _stream(stream))
     _check(st, "kq_quantize_two_sided")
+
+
+def kq_mxfp4_padded(n: int) -> int:
+    """Columns of a quantised row of n values: n rounded up to a multiple of 128."""
+    return -(-n // 128) * 128
+
+
+def kq_mxfp4_empty(rows: int, n: int, experts: int | None = None, device="cuda"):
+    """Uninitialised (codes, scales) for `rows` quantised rows of n values: codes uint8
+    [rows, np / 2], scales uint8 [np / 128, rows, 4], np = kq_mxfp4_padded(n); with `experts`,
+    that many of each, one after another."""
+    torch = _torch()
+    lead = () if experts is None else (experts,)
+    np_ = kq_mxfp4_padded(n)
+    return (torch.empty((*lead, rows, np_ // 2), dtype=torch.uint8, device=device),
+            torch.empty((*lead, np_ // 128, rows, 4), dtype=torch.uint8, device=device))
+
+
+def _mx_type(t, name: str) -> int:
+    torch = _torch()
+    if t.dtype is torch.bfloat16:
+        return KQ_BF16
+    if t.dtype is torch.float32:
+        return KQ_F32
+    raise TypeError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
+
+
+def _mx_vectors(d, sign, n: int):
+    torch = _torch()
+    for v, name in ((d, "d"), (sign, "sign")):
+        if v is not None and (v.numel() != n or not v.is_contiguous()):
+            raise ValueError(f"{name} must hold {n} contiguous entries")
+    return _dev_ptr(d, "d", (torch.float32,), True), _dev_ptr(sign, "sign", (torch.int8,), True)
+
+
+def _mx_check(codes, scales, rows: int, n: int, lead: tuple, name: str):
+    torch = _torch()
+    np_ = kq_mxfp4_padded(n)
+    if tuple(codes.shape) != (*lead, rows, np_ // 2) or not codes.is_contiguous():
+        raise ValueError(f"{name} codes must be contiguous {(*lead, rows, np_ // 2)}")
+    if tuple(scales.shape) != (*lead, np_ // 128, rows, 4) or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be contiguous {(*lead, np_ // 128, rows, 4)}")
+    return _dev_ptr(codes, f"{name} codes", (torch.uint8,)), _dev_ptr(scales, f"{name} scales", (torch.uint8,))
+
+
+def kq_mxfp4_quantize(src, codes, scales, d=None, sign=None, had: int = 1, values=None, stream=None) -> None:
+    """Rows of src (fp32 or bf16, rows x n) to MXFP4 codes and scales (kq_mxfp4_empty) of
+    P D^-1 src; `values` (bf16, rows x n, optional) receives what they stand for."""
+    torch = _torch()
+    lib = load_library()
+    rows, n = src.shape
+    cp, sp = _mx_check(codes, scales, rows, n, (), "output")
+    dp, gp = _mx_vectors(d, sign, n)
+    if values is not None and values.shape != src.shape:
+        raise ValueError("values must have src's shape")
+    st = lib.kq_mxfp4_quantize(
+        _dev_ptr(src, "src"), _mx_type(src, "src"), rows, n, _ld(src, "src"), dp, gp, had, cp, sp,
+        _dev_ptr(values, "values", (torch.bfloat16,), True),
+        0 if values is None else _ld(values, "values"), _stream(stream))
+    _check(st, "kq_mxfp4_quantize")
+
+
+def kq_mxfp4_workspace(rows: int, n: int) -> int:
+    lib = load_library()
+    b = ctypes.c_size_t(0)
+    _check(lib.kq_mxfp4_workspace(rows, n, ctypes.byref(b)), "kq_mxfp4_workspace")
+    return b.value
+
+
+def _mx_rows(x, x_scales, d, sign, n, ws):
+    """(pointer, type, rows, n, ld, scales, d, sign, ws, ws bytes) of the activations."""
+    torch = _torch()
+    if x_scales is not None:
+        if n is None:
+            raise ValueError("quantised rows need n, their number of values")
+        rows = x.shape[0]
+        xp, sp = _mx_check(x, x_scales, rows, n, (), "x")
+        return xp, KQ_MXFP4, rows, n, kq_mxfp4_padded(n), sp, *_mx_vectors(d, sign, n), None, 0
+    rows, cols = x.shape
+    if n is not None and n != cols:
+        raise ValueError(f"x has {cols} columns, not {n}")
+    if ws is None:
+        ws = torch.empty(kq_mxfp4_workspace(rows, cols), dtype=torch.uint8, device=x.device)
+    return (_dev_ptr(x, "x"), _mx_type(x, "x"), rows, cols, _ld(x, "x"), None, *_mx_vectors(d, sign, cols),
+            _dev_ptr(ws, "ws", (torch.uint8,)), ws.numel())
+
+
+def kq_mxfp4_linear(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1, x_scales=None,
+                    n=None, stream=None) -> None:
+    """y = Q(P D^-1 x) W^T for a layer held in MXFP4: x fp32 or bf16 [rows, n] (or codes, with
+    x_scales and n), y fp32 or bf16 [rows, out]."""
+    lib = load_library()
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
+    out = w_codes.shape[0]
+    cp, sp = _mx_check(w_codes, w_scales, out, n, (), "weight")
+    if tuple(y.shape) != (rows, out):
+        raise ValueError(f"y must be {(rows, out)}")
+    st = lib.kq_mxfp4_linear(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, _dev_ptr(y, "y"),
+                             _mx_type(y, "y"), _ld(y, "y"), wp, wb, _stream(stream))
+    _check(st, "kq_mxfp4_linear")
+
+
+def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1,
+                     x_scales=None, n=None, stream=None) -> None:
+    """y[s] = Q(P D^-1 x[index[s]]) W_e^T for the slots s of expert e, [offsets[e], offsets[e + 1]):
+    index int32 [slots] or None, offsets int32 [experts + 1], weights of kq_mxfp4_empty(out, n,
+    experts), y fp32 or bf16 [slots, out].  Offsets and index stay on the device."""
+    torch = _torch()
+    lib = load_library()
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
+    experts, out = w_codes.shape[0], w_codes.shape[1]
+    cp, sp = _mx_check(w_codes, w_scales, out, n, (experts,), "weight")
+    slots = y.shape[0]
+    if tuple(y.shape) != (slots, out):
+        raise ValueError(f"y must have {out} columns")
+    if tuple(offsets.shape) != (experts + 1,) or not offsets.is_contiguous():
+        raise ValueError(f"offsets must hold {experts + 1} contiguous entries")
+    if index is not None and (tuple(index.shape) != (slots,) or not index.is_contiguous()):
+        raise ValueError(f"index must hold {slots} contiguous entries")
+    i32 = (torch.int32,)
+    st = lib.kq_mxfp4_experts(xp, xt, rows, n, ldx, xsp, dp, gp, had, _dev_ptr(index, "index", i32, True), slots,
+                              _dev_ptr(offsets, "offsets", i32), experts, cp, sp, out, _dev_ptr(y, "y"),
+                              _mx_type(y, "y"), _ld(y, "y"), wp, wb, _stream(stream))
+    _check(st, "kq_mxfp4_experts")

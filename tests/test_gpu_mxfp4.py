@@ -1,0 +1,465 @@
+"""GPU parity of the MXFP4 operators against plain 64-bit implementations.
+
+Quantisation is held to equality: with no rotation the elements of a given fp32 or bf16 row
+are determined, and with one the definition fixes every fp32 rounding (butterflies with
+ascending strides), which numpy's fp32 repeats; against the 64-bit rotation they may differ
+only next to a rounding boundary.  Products: a sum of K terms in fp32, in any order, is off by
+at most (K + 2) 2^-24 sum |x w|, and by half an ulp more after the rounding to bf16.
+"""
+import numpy as np
+import pytest
+
+import oracle.mxfp4 as om
+from tests.gpu_util import announce, torch_cuda
+
+pytestmark = pytest.mark.gpu
+
+
+def _kq():
+    import post_quantization_syrk_amd as kq
+    return kq
+
+
+def _rows(rng, rows, n, kind):
+    torch = torch_cuda()
+    x = rng.standard_normal((rows, n)) * np.exp(rng.standard_normal(n))
+    x = torch.from_numpy(x.astype(np.float32))
+    return x.to(torch.bfloat16) if kind == "bf16" else x
+
+
+def _processing(rng, n, rescale, signed):
+    d = np.exp(0.5 * rng.standard_normal(n)).astype(np.float32) if rescale else None
+    s = rng.choice([-1, 1], n).astype(np.int8) if signed else None
+    return d, s
+
+
+def _dev(a):
+    torch = torch_cuda()
+    return None if a is None else torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def _quantize(x, d=None, sign=None, had=1, values=True, stream=None):
+    """(codes, scale bytes, values) of device rows x, unpacked."""
+    torch = torch_cuda()
+    kq = _kq()
+    rows, n = x.shape
+    codes, scales = kq.kq_mxfp4_empty(rows, n)
+    codes.fill_(0xAA)
+    scales.fill_(0xAA)
+    vals = torch.full((rows, n), 7.0, dtype=torch.bfloat16, device="cuda") if values else None
+    kq.kq_mxfp4_quantize(x, codes, scales, d=_dev(d), sign=_dev(sign), had=had, values=vals, stream=stream)
+    torch.cuda.synchronize()
+    return (*om.mx_unpack(codes.cpu().numpy(), scales.cpu().numpy()), vals.float().cpu().numpy() if values else None)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,n", [(1, 1), (2, 31), (3, 32), (1, 33), (5, 100), (4, 128), (3, 129), (2, 1000),
+                                    (1, 4096), (3, 4224), (2, 11008), (70, 515), (1, 8200), (300, 64)])
+def test_quantize_without_rotation(rows, n, kind):
+    announce(f"mxfp4 quantize {rows}x{n} {kind}")
+    rng = np.random.default_rng(rows * 100003 + n)
+    x = _rows(rng, rows, n, kind)
+    code, scale, values = _quantize(x.cuda())
+    ref = x.double().numpy()
+    c, s = om.mx_encode(ref)
+    assert np.array_equal(code & 7, c & 7) and np.array_equal(scale, s)
+    assert np.array_equal(values, om.mx_values(c, s, n))
+    d, sg = _processing(rng, n, True, True)
+    code, scale, values = _quantize(x.cuda(), d, sg)
+    c, s = om.mx_encode(om.mx_rotate_f32(x.float().numpy(), d, sg))
+    assert np.array_equal(code, c) and np.array_equal(scale, s)
+    assert np.array_equal(values, om.mx_values(c, s, n))
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,n,had", [(2, 2, 2), (3, 36, 4), (5, 1000, 8), (2, 48, 16), (3, 96, 32), (2, 192, 64),
+                                        (3, 384, 128), (9, 256, 256), (2, 11008, 256), (3, 1536, 512), (2, 1024, 1024),
+                                        (2, 6144, 2048), (1, 4096, 4096), (33, 4096, 4096), (2, 12288, 4096),
+                                        (1, 8192, 8192), (3, 24576, 8192), (17, 2048, 2048), (2, 8192, 16)])
+def test_quantize_with_rotation(rows, n, had, kind):
+    announce(f"mxfp4 quantize {rows}x{n} block {had} {kind}")
+    rng = np.random.default_rng(rows + 7 * n + had)
+    x = _rows(rng, rows, n, kind)
+    d, sg = _processing(rng, n, True, True)
+    code, scale, values = _quantize(x.cuda(), d, sg, had)
+    xr = om.mx_rotate_f32(x.float().numpy(), d, sg, had)
+    c, s = om.mx_encode(xr)
+    assert np.array_equal(code & 7, c & 7) and np.array_equal(scale, s)
+    assert np.array_equal(values, om.mx_values(c, s, n))
+    # against the rotation in 64 bits: equal but next to a boundary.  Each of log2(had) + 2 stages
+    # rounds by 2^-24 of a partial sum, so an entry is off by at most that times the block's norm
+    exact = om.mx_rotate(x.double().numpy(), d, sg, had)
+    norm = np.sqrt((exact.reshape(rows, -1, had) ** 2).sum(-1, keepdims=True))
+    off = (np.log2(had) + 3) * 2.0 ** -24 * np.broadcast_to(norm, (rows, n // had, had)).reshape(rows, n)
+    rel = np.minimum((off / np.maximum(np.abs(exact), 1e-30)), 0.5)
+    differ = om.mx_round(exact) != values
+    sure = (om.mx_round(exact - off) == om.mx_round(exact + off)) & ~om.mx_near_tie(exact, float(np.median(rel)) * 8)
+    assert not (differ & sure).any()
+    assert differ.mean() <= 1e-3
+
+
+@pytest.mark.parametrize("signed,rescale,had", [(True, False, 1), (False, True, 1), (True, False, 64), (False, True, 64),
+                                                (False, False, 64), (False, False, 0)])
+def test_quantize_parts_of_the_processing(signed, rescale, had):
+    rng = np.random.default_rng(3)
+    x = _rows(rng, 7, 448, "f32")
+    d, sg = _processing(rng, 448, rescale, signed)
+    code, scale, values = _quantize(x.cuda(), d, sg, had)
+    c, s = om.mx_encode(om.mx_rotate_f32(x.numpy(), d, sg, had or 64))
+    assert np.array_equal(code & 7, c & 7) and np.array_equal(scale, s)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("had", [1, 4])
+def test_quantize_edges(kind, had):
+    """Zero blocks, the smallest and the largest numbers, ties, infinities and NaN."""
+    announce(f"mxfp4 quantize edges {kind} block {had}")
+    x = np.zeros((8, 128), np.float32)
+    x[0, :8] = [6, 5, 3.5, 2.5, 1.75, 1.25, 0.75, 0.25]
+    x[0, 32:40] = [-8, -7, -5, -3, -2.5, -1.5, -0.5, 7.96875]
+    x[1, 5], x[1, 40], x[1, 70] = 2.0 ** -149 if kind == "f32" else 2.0 ** -133, 2.0 ** -126, 2.0 ** -127
+    x[2, :4] = [3.3e38, -3.3e38, 1e30, 0] if had == 1 else [1e37, 1e30, 0, 0]
+    x[3, 3], x[3, 64:66] = np.inf, [1, -2]
+    x[4, 127], x[4, 0] = np.nan, 1
+    x[5, 33] = -np.inf
+    x[6] = -0.0
+    x[7] = np.linspace(-7.9, 7.9, 128)
+    torch = torch_cuda()
+    xt = torch.from_numpy(x)
+    xt = xt.to(torch.bfloat16) if kind == "bf16" else xt
+    code, scale, values = _quantize(xt.cuda(), had=had)
+    with np.errstate(invalid="ignore", over="ignore"):
+        r = om.mx_rotate_f32(xt.float().numpy(), had=had)
+    c, s = om.mx_encode(r)
+    assert np.array_equal(scale, s)
+    assert np.array_equal(code & 7, c & 7)
+    assert np.array_equal(values, om.mx_values(c, s, 128), equal_nan=True)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("off,pad,had", [(1, 3, 1), (2, 6, 1), (0, 7, 1), (4, 4, 8), (1, 1, 8), (3, 0, 512), (8, 8, 512)])
+def test_quantize_strides_and_alignment(kind, off, pad, had):
+    """Rows inside a wider buffer, starting at any element; values into a wider buffer."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(off + pad)
+    wide = _rows(rng, 6, off + 1024 + pad, kind).cuda()
+    x = wide[:, off:off + 1024]
+    values = torch.zeros((6, 1040), dtype=torch.bfloat16, device="cuda")
+    codes, scales = kq.kq_mxfp4_empty(6, 1024)
+    kq.kq_mxfp4_quantize(x, codes, scales, had=had, values=values[:, 5:1029])
+    c, s = om.mx_encode(om.mx_rotate_f32(x.float().cpu().numpy(), had=had))
+    v = values.float().cpu().numpy()
+    assert np.array_equal(v[:, 5:1029], om.mx_values(c, s, 1024))
+    assert not v[:, :5].any() and not v[:, 1029:].any()
+    code, scale = om.mx_unpack(codes.cpu().numpy(), scales.cpu().numpy())
+    assert np.array_equal(code & 7, c & 7) and np.array_equal(scale, s)
+
+
+def _layer(rng, out, n, experts=None):
+    """Codes and scales on the device of random weights, and their values [.., out, n]."""
+    torch = torch_cuda()
+    kq = _kq()
+    lead = 1 if experts is None else experts
+    codes, scales = kq.kq_mxfp4_empty(out, n, experts=lead)
+    vals = []
+    for e in range(lead):
+        c, s = om.mx_encode(0.05 * rng.standard_normal((out, n)) * np.exp(0.5 * rng.standard_normal((out, 1))))
+        vals.append(om.mx_values(c, s, n))
+        pc, ps = om.mx_pack(c, s)
+        codes[e].copy_(torch.from_numpy(pc))
+        scales[e].copy_(torch.from_numpy(ps))
+    return (codes[0], scales[0], vals[0]) if experts is None else (codes, scales, np.stack(vals))
+
+
+def _close(y, xq, w, bf16):
+    """y against xq w^T within the bound of an fp32 sum."""
+    ref, mag = xq @ w.T, np.abs(xq) @ np.abs(w.T)
+    bound = (xq.shape[1] + 2) * 2.0 ** -24 * mag
+    if bf16:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(ref)
+    y = y.double().cpu().numpy()
+    assert np.all(np.abs(y - ref) <= bound), float((np.abs(y - ref) - bound).max())
+
+
+def _empty(shape, kind):
+    torch = torch_cuda()
+    return torch.full(shape, 123.0, dtype=torch.bfloat16 if kind == "bf16" else torch.float32, device="cuda")
+
+
+@pytest.mark.parametrize("rows,n,out,had,xk,yk", [
+    (1, 128, 1, 128, "bf16", "f32"), (1, 4096, 4096, 4096, "bf16", "bf16"), (1, 33, 17, 1, "f32", "f32"),
+    (2, 1, 3, 1, "f32", "bf16"), (3, 1000, 4099, 8, "bf16", "f32"), (1, 11008, 100, 256, "f32", "bf16"),
+    (7, 512, 65, 512, "bf16", "bf16"), (16, 2048, 300, 2048, "bf16", "f32"), (17, 640, 128, 128, "f32", "f32"),
+    (31, 192, 1000, 64, "bf16", "bf16"), (32, 256, 256, 256, "bf16", "f32"), (33, 256, 31, 256, "f32", "bf16"),
+    (64, 4096, 96, 4096, "bf16", "f32"), (65, 1024, 130, 1024, "bf16", "bf16"), (100, 96, 1, 32, "f32", "f32"),
+    (128, 384, 515, 128, "bf16", "bf16"), (200, 8192, 257, 8192, "bf16", "f32"), (256, 128, 256, 1, "bf16", "f32"),
+    (257, 512, 700, 512, "f32", "bf16"), (300, 1000, 1001, 8, "bf16", "f32"), (513, 320, 2050, 64, "bf16", "bf16"),
+    (1100, 2048, 600, 2048, "bf16", "f32"),
+])
+def test_linear(rows, n, out, had, xk, yk):
+    announce(f"mxfp4 linear {rows}x{n} -> {out} block {had} {xk} {yk}")
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows + 3 * n + 5 * out)
+    x = _rows(rng, rows, n, xk)
+    if rows > 2:
+        x[rows // 2] = 0
+    d, sg = _processing(rng, n, had > 1, had > 1)
+    wc, ws, wv = _layer(rng, out, n)
+    y = _empty((rows, out), yk)
+    kq.kq_mxfp4_linear(x.cuda(), wc, ws, y, d=_dev(d), sign=_dev(sg), had=had)
+    xq = om.mx_round(om.mx_rotate_f32(x.float().numpy(), d, sg, had))
+    _close(y, xq, wv, yk == "bf16")
+    # activations quantised beforehand give the same bits; so does a second call
+    xc, xs = kq.kq_mxfp4_empty(rows, n)
+    kq.kq_mxfp4_quantize(x.cuda(), xc, xs, d=_dev(d), sign=_dev(sg), had=had)
+    again = _empty((rows, out), yk)
+    kq.kq_mxfp4_linear(xc, wc, ws, again, x_scales=xs, n=n)
+    assert torch.equal(y, again)
+    kq.kq_mxfp4_linear(x.cuda(), wc, ws, again, d=_dev(d), sign=_dev(sg), had=had)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40, 150])
+@pytest.mark.parametrize("off,pad", [(0, 0), (1, 2), (4, 4), (8, 8)])
+def test_linear_strided_output(rows, off, pad):
+    """An output inside a wider buffer, at any element: nothing around it is written."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    x = _rows(rng, rows, 256, "bf16").cuda()
+    wc, ws, wv = _layer(rng, 200, 256)
+    xq = om.mx_round(x.double().cpu().numpy())
+    for kind in ("bf16", "f32"):
+        wide = _empty((rows + 2, off + 200 + pad), kind)
+        kq.kq_mxfp4_linear(x, wc, ws, wide[1:-1, off:off + 200])
+        _close(wide[1:-1, off:off + 200], xq, wv, kind == "bf16")
+        rest = wide.clone()
+        rest[1:-1, off:off + 200] = 123.0
+        assert torch.equal(rest, _empty(tuple(wide.shape), kind))
+
+
+@pytest.mark.parametrize("rows", [1, 20, 130])
+def test_not_finite_values_stay_in_their_rows(rows):
+    """An infinity in an activation makes its own output row NaN; a NaN block in a weight row
+    makes that output column NaN; everything else is untouched."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    x = _rows(rng, rows, 320, "f32")
+    wc, ws, wv = _layer(rng, 150, 320)
+    y0 = _empty((rows, 150), "f32")
+    kq.kq_mxfp4_linear(x.cuda(), wc, ws, y0)
+    x[rows - 1, 300] = np.inf
+    ws2 = ws.clone()
+    ws2[1, 77, 2] = 255
+    y1 = _empty((rows, 150), "f32")
+    kq.kq_mxfp4_linear(x.cuda(), wc, ws2, y1)
+    bad = torch.zeros((rows, 150), dtype=torch.bool, device="cuda")
+    bad[rows - 1] = True
+    bad[:, 77] = True
+    assert torch.equal(torch.isnan(y1), bad)
+    assert torch.equal(y1[~bad], y0[~bad])
+
+
+@pytest.mark.parametrize("rows", [1, 24, 140])
+def test_linear_of_extreme_scales(rows):
+    """Scale bytes from one end of their range to the other, with products inside fp32's."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(5)
+    n, out = 256, 40
+    code, scale = om.mx_encode(rng.standard_normal((rows, n)))
+    wcode, wscale = om.mx_encode(rng.standard_normal((out, n)))
+    for xb, wb in ((0, 127), (0, 240), (252, 10), (252, 100), (60, 80)):
+        scale[:], wscale[:] = xb, wb
+        xc, xs = (torch.from_numpy(a).cuda() for a in om.mx_pack(code, scale))
+        wc, ws = (torch.from_numpy(a).cuda() for a in om.mx_pack(wcode, wscale))
+        y = _empty((rows, out), "f32")
+        kq.kq_mxfp4_linear(xc, wc, ws, y, x_scales=xs, n=n)
+        ref = om.mx_values(code, scale, n) @ om.mx_values(wcode, wscale, n).T
+        tiny = 2.0 ** -126 if xb + wb < 140 else 0.0   # results below fp32's normal range may be flushed
+        assert np.all(np.abs(y.double().cpu().numpy() - ref) <= (n + 2) * 2.0 ** -24 * np.abs(ref).max() + tiny)
+
+
+def _experts_ref(xq, index, offsets, w, slots, rows):
+    want = np.full((slots, w.shape[1]), 123.0)
+    mag = np.zeros_like(want)
+    for e in range(w.shape[0]):
+        lo = min(max(int(offsets[e]), 0), slots)
+        hi = min(max(int(offsets[e + 1]), lo), slots)
+        for s in range(lo, hi):
+            r = s if index is None else int(index[s])
+            x = xq[r] if 0 <= r < rows else np.zeros(xq.shape[1])
+            want[s], mag[s] = w[e] @ x, np.abs(w[e]) @ np.abs(x)
+    return want, mag
+
+
+def _experts_check(y, want, mag, n, bf16):
+    bound = (n + 2) * 2.0 ** -24 * mag
+    if bf16:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * np.abs(want) * (mag > 0)
+    got = y.double().cpu().numpy()
+    assert np.all(np.abs(got - want) <= bound), float((np.abs(got - want) - bound).max())
+
+
+def _sorted_slots(rng, tokens, top, experts, skew):
+    popular = skew * rng.standard_normal(experts)
+    chosen = np.argsort(-(popular + rng.standard_normal((tokens, experts))), axis=1)[:, :top].reshape(-1)
+    order = np.argsort(chosen, kind="stable")
+    offsets = np.concatenate([[0], np.cumsum(np.bincount(chosen, minlength=experts))])
+    return (order // top).astype(np.int32), offsets.astype(np.int32)
+
+
+@pytest.mark.parametrize("tokens,top,experts,n,out,had,xk,yk,skew", [
+    (1, 1, 1, 128, 16, 128, "bf16", "f32", 0.0), (1, 2, 8, 512, 130, 512, "bf16", "bf16", 1.0),
+    (5, 2, 4, 1000, 65, 8, "f32", "f32", 1.0), (33, 4, 16, 256, 200, 256, "bf16", "f32", 2.0),
+    (96, 6, 64, 384, 100, 128, "bf16", "bf16", 1.0), (200, 1, 3, 640, 257, 128, "f32", "bf16", 2.0),
+    (300, 2, 5, 256, 300, 256, "bf16", "f32", 1.0), (64, 8, 128, 128, 33, 128, "bf16", "f32", 0.5),
+    (700, 2, 4, 512, 520, 512, "bf16", "bf16", 1.5), (3, 3, 300, 96, 20, 32, "f32", "f32", 0.0),
+])
+def test_experts(tokens, top, experts, n, out, had, xk, yk, skew):
+    announce(f"mxfp4 experts {tokens}x{top} of {experts} {n} -> {out}")
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(tokens + experts + n)
+    x = _rows(rng, tokens, n, xk)
+    d, sg = _processing(rng, n, True, True)
+    index, offsets = _sorted_slots(rng, tokens, top, experts, skew)
+    wc, ws, wv = _layer(rng, out, n, experts)
+    y = _empty((tokens * top, out), yk)
+    kq.kq_mxfp4_experts(x.cuda(), _dev(index), _dev(offsets), wc, ws, y, d=_dev(d), sign=_dev(sg), had=had)
+    xq = om.mx_round(om.mx_rotate_f32(x.float().numpy(), d, sg, had))
+    want, mag = _experts_ref(xq, index, offsets, wv, tokens * top, tokens)
+    _experts_check(y, want, mag, n, yk == "bf16")
+    again = _empty((tokens * top, out), yk)
+    xc, xs = kq.kq_mxfp4_empty(tokens, n)
+    kq.kq_mxfp4_quantize(x.cuda(), xc, xs, d=_dev(d), sign=_dev(sg), had=had)
+    kq.kq_mxfp4_experts(xc, _dev(index), _dev(offsets), wc, ws, again, x_scales=xs, n=n)
+    assert torch.equal(y, again)
+
+
+@pytest.mark.parametrize("slots,offsets", [
+    (50, [0, 0, 0, 50, 50]),        # everything with one expert
+    (50, [0, 0, 0, 0, 0]),          # nothing with any
+    (50, [10, 20, 20, 30, 41]),     # slots before the first and after the last expert
+    (50, [0, 1, 2, 3, 4]),          # one slot each
+    (50, [-7, 20, 60, 70, 90]),     # offsets that leave the range are cut
+    (50, [0, 30, 20, 25, 50]),      # decreasing: that expert has none
+    (300, [0, 129, 129, 257, 300]),
+])
+@pytest.mark.parametrize("indexed", [True, False])
+def test_experts_ranges(slots, offsets, indexed):
+    """Slots outside every expert keep what y held; an index outside the rows reads zeros."""
+    kq = _kq()
+    rng = np.random.default_rng(slots + offsets[1])
+    n, out = 160, 70
+    rows = 20 if indexed else slots
+    x = _rows(rng, rows, n, "bf16")
+    index = rng.integers(0, rows, slots).astype(np.int32) if indexed else None
+    if indexed:
+        index[[0, 3, slots - 1]] = [-1, rows, 2 ** 31 - 1]
+    wc, ws, wv = _layer(rng, out, n, 4)
+    y = _empty((slots, out), "f32")
+    kq.kq_mxfp4_experts(x.cuda(), _dev(index), _dev(np.int32(offsets)), wc, ws, y)
+    # ranges may overlap where the offsets decrease: a later expert's rows are then any of the two
+    want, mag = _experts_ref(om.mx_round(x.double().numpy()), index, offsets, wv, slots, rows)
+    if offsets != sorted(offsets):
+        want, mag, y = want[30:], mag[30:], y[30:]
+    _experts_check(y, want, mag, n, False)
+
+
+def test_experts_of_no_rows():
+    """No rows of x at all: every index is outside, every reached slot is zero."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(0)
+    wc, ws, _ = _layer(rng, 40, 128, 2)
+    y = _empty((10, 40), "f32")
+    x = torch.empty((0, 128), device="cuda")
+    kq.kq_mxfp4_experts(x, torch.zeros(10, dtype=torch.int32, device="cuda"),
+                        torch.tensor([0, 4, 9], dtype=torch.int32, device="cuda"), wc, ws, y)
+    want = _empty((10, 40), "f32")
+    want[:9] = 0
+    assert torch.equal(y, want)
+
+
+def test_another_stream_and_a_graph():
+    """On a stream of its own, and captured: every replay gives the eager result of its inputs."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(9)
+    d, sg = _processing(rng, 512, True, True)
+    d, sg = _dev(d), _dev(sg)
+    wc, ws, _ = _layer(rng, 200, 512)
+    ec, es, _ = _layer(rng, 96, 512, 4)
+    inputs = [_rows(rng, 40, 512, "bf16").cuda() for _ in range(4)]
+    index, offsets = (_dev(v) for v in _sorted_slots(rng, 40, 2, 4, 1.0))
+    x = inputs[0].clone()
+    work = torch.empty(kq.kq_mxfp4_workspace(40, 512), dtype=torch.uint8, device="cuda")
+    y, z = _empty((40, 200), "f32"), _empty((80, 96), "bf16")
+
+    def both(x, y, z, work=work):
+        kq.kq_mxfp4_linear(x, wc, ws, y, work, d=d, sign=sg, had=512)
+        kq.kq_mxfp4_experts(x, index, offsets, ec, es, z, work, d=d, sign=sg, had=512)
+
+    eager = []
+    for v in inputs:
+        a, b = _empty((40, 200), "f32"), _empty((80, 96), "bf16")
+        both(v, a, b)
+        eager.append((a, b))
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(inputs[1], y, z)
+    side.synchronize()
+    assert torch.equal(y, eager[1][0]) and torch.equal(z, eager[1][1])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(x, y, z)
+    for k in (1, 3, 2, 0, 3):
+        x.copy_(inputs[k])
+        y.fill_(5.0)
+        graph.replay()
+        a, b = _empty((40, 200), "f32"), _empty((80, 96), "bf16")
+        torch.cuda.synchronize()
+        both(inputs[k], a, b, torch.empty_like(work))
+        assert torch.equal(y, eager[k][0]) and torch.equal(z, eager[k][1])
+        assert torch.equal(a, y) and torch.equal(b, z)
+
+
+def test_refusals_of_the_binding():
+    torch = torch_cuda()
+    kq = _kq()
+    x = torch.zeros((4, 128), device="cuda")
+    codes, scales = kq.kq_mxfp4_empty(4, 128)
+    with pytest.raises(TypeError):
+        kq.kq_mxfp4_quantize(x.half(), codes, scales)
+    with pytest.raises(TypeError):
+        kq.kq_mxfp4_quantize(x.cpu(), codes, scales)
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_quantize(x, codes[:3], scales)
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_quantize(x, codes, scales, d=torch.ones(127, device="cuda"))
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_quantize(x.T.contiguous().T, codes, scales)
+    with pytest.raises(kq.KQError) as e:
+        kq.kq_mxfp4_quantize(x, codes, scales, had=256)
+    assert e.value.status == kq.KQ_ESHAPE
+    wc, ws = kq.kq_mxfp4_empty(8, 128)
+    y = torch.zeros((4, 8), device="cuda")
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_linear(x, wc, ws, y[:, :7])
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_linear(codes, wc, ws, y, x_scales=scales)
+    with pytest.raises(kq.KQError) as e:
+        kq.kq_mxfp4_linear(x, wc, ws, y, torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == kq.KQ_EWORKSPACE
+    ec, es = kq.kq_mxfp4_empty(8, 128, experts=2)
+    off = torch.zeros(3, dtype=torch.int32, device="cuda")
+    with pytest.raises(TypeError):
+        kq.kq_mxfp4_experts(x, None, off.long(), ec, es, y)
+    with pytest.raises(ValueError):
+        kq.kq_mxfp4_experts(x, None, off[:2], ec, es, y)
