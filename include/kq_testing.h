@@ -31,7 +31,9 @@ enum {
   KQ_TESTING_FACTOR_SUPERBLOCK = 1,
   /* Longest row (bytes) the quantizer's row kernels stage in LDS (default 65536); 0 forces
    * their direct paths, which longer rows take. */
-  KQ_TESTING_ROW_LDS_BYTES = 2
+  KQ_TESTING_ROW_LDS_BYTES = 2,
+  /* Outputs per workgroup of the MXFP4 products. */
+  KQ_TESTING_MX_TILE = 3
 };
 
 /* Selects `value` for `knob`; value -1 restores the default.  KQ_EINVAL for an unknown knob

@@ -1,0 +1,622 @@
+// Products with layers held in MXFP4: y = Q(x~) W^T for one layer, or for one of several
+// layers per row (a mixture's experts), sums in fp32 on the scaled matrix instructions.
+#include "mxfp4.h"
+
+#include <algorithm>
+
+namespace kq {
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+struct ProductArgs {
+  const uint8_t* xc;       // rows x pitch
+  const uint8_t* xs;
+  int64_t rows;            // rows of x
+  const uint8_t* wc;       // experts x N x pitch
+  const uint8_t* ws;
+  int64_t N;
+  int64_t pitch;           // bytes of a quantised row: Kp / 2
+  int steps;               // Kp / 128
+  const int32_t* index;    // slot -> row of x, or NULL: the slot itself
+  const int32_t* offsets;  // experts + 1 first slots, or NULL: one layer, slots = rows
+  int experts;
+  int64_t slots;
+  void* y;
+  bool y_bf16;
+  bool y_far;              // rows of y too far apart for 32-bit offsets inside a tile
+  int64_t ldy;
+};
+
+// Slots [first, last) of expert e, kept inside [0, slots) whatever the offsets hold.
+__device__ __forceinline__ void expert_range(const ProductArgs& a, int e, int& first, int& last) {
+  const int lo = a.offsets[e], hi = a.offsets[e + 1], n = (int)a.slots;
+  first = min(max(lo, 0), n);
+  last = min(max(hi, first), n);
+}
+
+// Where a tile's rows of x come from: consecutive rows, rows behind an index, or rows behind an
+// index of an x too large for 32-bit offsets.
+enum { X_ROWS, X_INDEX, X_FAR };
+
+// Rows [m0, last) of y with expert e's layer, columns from n0: one tile.
+struct Tile {
+  int e, m0, last, n0;
+};
+
+// Experts whose tiles a kernel finds through its table; more are searched in memory.
+constexpr int TABLE = 1024;
+struct ExpertTable {
+  int before[TABLE];      // row tiles of the experts before this one
+  int first[TABLE + 1];   // its first slot; of the one past the last: the end
+};
+
+// Row tiles of all experts; with at most TABLE experts, the table too (all threads of the
+// workgroup, which a barrier has to follow).
+template <int BM>
+__device__ __forceinline__ int count_tiles(const ProductArgs& a, ExpertTable& tab) {
+  const int lane = threadIdx.x & 63;
+  int tm = 0;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    int c = 0, first = 0, last = 0;
+    if (e0 + lane < a.experts) {
+      expert_range(a, e0 + lane, first, last);
+      c = (last - first + BM - 1) / BM;
+    }
+    int sum = c;   // inclusive sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (a.experts <= TABLE && threadIdx.x < 64 && e0 + lane < a.experts) {
+      tab.before[e0 + lane] = tm + sum - c;
+      tab.first[e0 + lane] = first;
+      if (e0 + lane == a.experts - 1) tab.first[a.experts] = last;
+    }
+    tm += __builtin_amdgcn_readlane(sum, 63);
+  }
+  if (a.experts <= TABLE && threadIdx.x < 64)
+    for (int e = a.experts + lane; e < TABLE; e += 64) tab.before[e] = 0x7fffffff;
+  return __builtin_amdgcn_readfirstlane(tm);
+}
+
+// The expert of row tile mt (< the count) and the tile's rows.
+template <int BM>
+__device__ __forceinline__ void find_rows(const ProductArgs& a, const ExpertTable& tab, int mt, Tile& t) {
+  const int lane = threadIdx.x & 63;
+  if (a.experts <= TABLE) {
+    // the last expert with before <= mt: it has tiles, or the next one would have the same before
+    const int b = 16 * (__popcll(__ballot(tab.before[16 * lane] <= mt)) - 1);
+    const int e = b + __popcll(__ballot(lane < 16 && tab.before[b + (lane & 15)] <= mt)) - 1;
+    t.e = __builtin_amdgcn_readfirstlane(e);
+    t.m0 = __builtin_amdgcn_readfirstlane(tab.first[t.e] + (mt - tab.before[t.e]) * BM);
+    t.last = __builtin_amdgcn_readfirstlane(max(tab.first[t.e + 1], tab.first[t.e]));
+    return;
+  }
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    int c = 0, first = 0, last = 0;
+    if (e0 + lane < a.experts) {
+      expert_range(a, e0 + lane, first, last);
+      c = (last - first + BM - 1) / BM;
+    }
+    int sum = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int all = __builtin_amdgcn_readlane(sum, 63);
+    if (mt < all) {
+      const int src = __ffsll((unsigned long long)__ballot(sum > mt)) - 1;
+      t.e = __builtin_amdgcn_readfirstlane(e0 + src);
+      t.m0 = __builtin_amdgcn_readfirstlane(__shfl(first, src) + (mt - __shfl(sum - c, src)) * BM);
+      t.last = __builtin_amdgcn_readfirstlane(__shfl(last, src));
+      return;
+    }
+    mt -= all;
+  }
+}
+
+// Tile `id` of tm x tn, counted in bands of G row tiles so that neighbours share panels.
+template <int BM, int BN, int G, int ROWS>
+__device__ __forceinline__ Tile tile_at(const ProductArgs& a, const ExpertTable& tab, int64_t id, int tm, int tn) {
+  const int64_t band = (int64_t)G * tn;
+  const int g = (int)(id / band), rem = (int)(id - g * band);
+  const int gs = min(G, tm - g * G), mt = g * G + rem % gs;
+  Tile t;
+  t.n0 = rem / gs * BN;
+  if (ROWS == X_ROWS) {
+    t.e = 0;
+    t.m0 = mt * BM;
+    t.last = (int)a.slots;
+  } else {
+    find_rows<BM>(a, tab, mt, t);
+  }
+  return t;
+}
+
+// Zeros that copies of rows outside x read.
+__device__ __attribute__((aligned(16))) uint32_t g_zeros[4];
+
+// One wave's copy of 64 pieces of SIZE bytes into LDS, piece l to `to` + SIZE l; a lane whose
+// offset lies outside the descriptor copies zeros.
+template <int SIZE>
+__device__ __forceinline__ void copy_lds(__amdgpu_buffer_rsrc_t r, unsigned off, uint8_t* to) {
+  typedef __attribute__((address_space(3))) void lds_void;
+  if constexpr (SIZE == 16)
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 16, (int)off, 0, 0, 0);
+  else
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, (int)off, 0, 0, 0);
+}
+__device__ __forceinline__ void copy_lds(const uint8_t* from, uint8_t* to) {
+  __builtin_amdgcn_global_load_lds((const void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+}
+
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(unsigned, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
+// Stores W values side by side at byte offset `off` (a masked offset stores nothing).
+template <int W>
+__device__ __forceinline__ void store_f32(__amdgpu_buffer_rsrc_t r, int off, const float (&v)[W]) {
+  if constexpr (W == 4)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]),
+                                                 __float_as_uint(v[3])}, r, off, 0, 0);
+  else if constexpr (W == 2)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v[0]), __float_as_uint(v[1])}, r, off, 0, 0);
+  else
+    bstore(v[0], r, off);
+}
+template <int W>
+__device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, const float (&v)[W]) {
+  if constexpr (W == 4)
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])}, r, off, 0, 0);
+  else if constexpr (W == 2)
+    __builtin_amdgcn_raw_buffer_store_b32(pack_bf16(v[0], v[1]), r, off, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v[0]), r, off, 0, 0);
+}
+
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+// Tiles of BM x BN outputs, 128 of K per stage, waves in 2 x WC, each with MT x NT accumulators
+// of 32 x 32.  A workgroup takes tile after tile; the copies of the next tile's first stages
+// follow those of the last stages of the present one, so the ring never runs dry and the stores
+// of one tile go out while the next is multiplied.
+template <int MT, int NT, int WC, int RING, int ROWS>
+__global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
+  constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 64, PANELS = (BM + BN) * 64;
+  constexpr int CA = 2 * MT / WC, CB = NT;            // copies of x and of W per wave and stage
+  constexpr int SI = (BM + BN) / 64, SC = (SI + 2 * WC - 1) / (2 * WC);   // scale copies: all, per wave
+  constexpr int COPIES = CA + CB + SC;
+  constexpr int STAGE = PANELS + (BM + BN) * 4;
+  __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t b1[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t b2[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t b3[RING == 4 ? STAGE : 16];
+  __shared__ ExpertTable tab[1];
+  __shared__ __attribute__((aligned(256))) int next_index[ROWS == X_ROWS ? 64 : BM];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wr = wave / WC, wc = wave % WC, l32 = lane & 31, q = lane >> 5;
+
+  // Workgroup u runs on XCD u mod 8 (a heuristic: any order is right).  Each XCD takes a
+  // contiguous run of tiles, so that those resident on it at a time share panels in its L2.
+  int tm = (int)((a.slots + BM - 1) / BM);
+  if (ROWS != X_ROWS) {
+    tm = count_tiles<BM>(a, *tab);
+    __syncthreads();
+  }
+  const int tn = (int)((a.N + BN - 1) / BN), turns = gridDim.x >> 3;
+  const int64_t total = (int64_t)tm * tn, per = (total + 7) / 8, run = (blockIdx.x & 7) * per;
+  const int64_t end = min(run + per, total);
+  int64_t id = run + (blockIdx.x >> 3);
+  if (id >= end) return;
+  auto at_id = [&](int64_t k) { return tile_at<BM, BN, 4, ROWS>(a, *tab, k, tm, tn); };
+
+  // Copies: descriptors whose base advances a stage at a time, and each lane's offset from it.
+  // Lanes of rows outside x, and past the last column all copies of x, lie outside their
+  // descriptor and put zeros into LDS.
+  constexpr unsigned ALL = 0xfffffff0u;
+  const uint8_t *xc, *xs, *wc_e, *ws_e;
+  unsigned oa[CA], ob[CB], os[SC];
+  const uint8_t* pa[CA];   // X_FAR: x beyond the reach of a 32-bit offset
+  int stepa[CA];
+  int issued;
+  const int slot4 = lane & 3;
+  // Points the copies at tile t; `row` gives the row of x behind a row of the tile.
+  auto aim = [&](const Tile& t, auto row_of_x) {
+    auto x_row = [&](int r) -> int64_t {   // -1: zeros
+      if (ROWS == X_ROWS) return min(r, t.last - 1 - t.m0);
+      const int x = row_of_x(min(r, t.last - 1 - t.m0));
+      return x >= 0 && x < a.rows ? x : -1;
+    };
+    auto w_row = [&](int r) -> unsigned { return (unsigned)min((int64_t)r, a.N - 1 - t.n0); };
+    issued = 0;
+    xc = a.xc + (ROWS == X_ROWS ? t.m0 * a.pitch : 0);
+    xs = a.xs + (ROWS == X_ROWS ? (int64_t)t.m0 * 4 : 0);
+    wc_e = a.wc + ((int64_t)t.e * a.N + t.n0) * a.pitch;
+    ws_e = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
+#pragma unroll
+    for (int r = 0; r < CA; ++r) {
+      const int pos = (wave * CA + r) * 16 + (lane >> 2), p = pos % (32 * MT);
+      const int64_t row = x_row(pos / (32 * MT) * (32 * MT) + (p & 31) * MT + (p >> 5));
+      const int64_t at = row * a.pitch + 16 * (slot4 ^ ((pos >> 2) & 3));
+      oa[r] = row >= 0 ? (unsigned)at : ALL;
+      pa[r] = row >= 0 ? a.xc + at : (const uint8_t*)g_zeros;
+      stepa[r] = row >= 0 ? 64 : 0;
+    }
+#pragma unroll
+    for (int r = 0; r < CB; ++r) {
+      const int pos = (wave * CB + r) * 16 + (lane >> 2), p = pos % (32 * NT);
+      ob[r] = w_row(pos / (32 * NT) * (32 * NT) + (p & 31) * NT + (p >> 5)) * (unsigned)a.pitch +
+              16 * (slot4 ^ ((pos >> 2) & 3));
+    }
+#pragma unroll
+    for (int k = 0; k < SC; ++k) {
+      const int si = min(wave * SC + k, SI - 1);
+      const int64_t row = si < MT ? x_row(64 * si + lane) : w_row(64 * (si - MT) + lane);
+      os[k] = row >= 0 ? (unsigned)row * 4 : ALL;
+    }
+  };
+  auto issue = [&](uint8_t* buf) {
+    const bool live = issued < a.steps;
+    const __amdgpu_buffer_rsrc_t ra = rsrc(xc, live ? (int)ALL : 0), rb = rsrc(wc_e, (int)ALL);
+#pragma unroll
+    for (int r = 0; r < CA; ++r) {
+      uint8_t* to = buf + (wave * CA + r) * 1024;
+      if (ROWS == X_FAR) {
+        copy_lds(live ? pa[r] : (const uint8_t*)g_zeros, to);
+        pa[r] += stepa[r];
+      } else {
+        copy_lds<16>(ra, oa[r], to);
+      }
+    }
+#pragma unroll
+    for (int r = 0; r < CB; ++r) copy_lds<16>(rb, ob[r], buf + PANEL_A + (wave * CB + r) * 1024);
+#pragma unroll
+    for (int k = 0; k < SC; ++k) {
+      const int si = min(wave * SC + k, SI - 1);
+      copy_lds<4>(rsrc(si < MT ? xs : ws_e, (int)ALL), os[k], buf + PANELS + si * 256);
+    }
+    // past the end the last stage's weights and scales are copied again, with zeros for x
+    const int64_t on = ++issued < a.steps;
+    xc += 64 * on;
+    wc_e += 64 * on;
+    xs += 4 * a.rows * on;
+    ws_e += 4 * a.N * on;
+  };
+
+  f32x16 acc[MT][NT];
+
+  const int swz = (l32 >> 2) & 3;
+  const int off0 = (l32 * 4 + (q ^ swz)) * 16, off1 = (l32 * 4 + ((2 + q) ^ swz)) * 16;
+  const int sca = PANELS + (wr * 32 * MT + l32 * MT) * 4, scb = PANELS + BM * 4 + (wc * 32 * NT + l32 * NT) * 4;
+  auto read = [&](const uint8_t* buf, int h, i32x4 (&xa)[MT], i32x4 (&xb)[NT]) {
+    const uint8_t* pA = buf + wr * MT * 2048 + (h ? off1 : off0);
+    const uint8_t* pB = buf + PANEL_A + wc * NT * 2048 + (h ? off1 : off0);
+    xa[0] = *(const i32x4*)pA;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) xb[n] = *(const i32x4*)(pB + n * 2048);
+#pragma unroll
+    for (int m = 1; m < MT; ++m) xa[m] = *(const i32x4*)(pA + m * 2048);
+  };
+  auto read_scales = [&](const uint8_t* buf, int (&sa)[MT], int (&sb)[NT]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sa[m] = *(const int*)(buf + sca + 4 * m) >> (8 * q);
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sb[n] = *(const int*)(buf + scb + 4 * n) >> (8 * q);
+  };
+  auto mma0 = [&](const i32x4 (&xa)[MT], const i32x4 (&xb)[NT], const int (&sa)[MT], const int (&sb)[NT]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
+            widen(xa[m]), widen(xb[n]), acc[m][n], 4, 4, 0, sa[m], 0, sb[n]);
+  };
+  auto mma1 = [&](const i32x4 (&xa)[MT], const i32x4 (&xb)[NT], const int (&sa)[MT], const int (&sb)[NT]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(xa[m]), widen(xb[n]), acc[m][n], 4, 4, 2,
+                                                                   sa[m], 2, sb[n]);
+  };
+
+  Tile t = at_id(id);
+  aim(t, [&](int r) { return a.index ? a.index[t.m0 + r] : t.m0 + r; });
+  i32x4 xa[MT], xb[NT], ya[MT], yb[NT];
+  int sa[MT], sb[NT], ta[MT], tb[NT];
+  issue(b0);
+  issue(b1);
+  issue(b2);
+  if constexpr (RING == 4) issue(b3);
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  lds_barrier();
+  read(b0, 0, xa, xb);
+  read_scales(b0, sa, sb);
+
+// Stage s: read the operands of its second half while multiplying the first; wait for this
+// wave's copies of stage s + 1 (at most WAIT newer ones outstanding) and for every wave's reads
+// of stage s; refill its buffer and read the first half of stage s + 1 while multiplying the
+// second half.
+#define KQ_MX_STEP(CUR, NXT, SA, SB, TA, TB, WAIT)           \
+  {                                                         \
+    read(CUR, 1, ya, yb);                                   \
+    mma0(xa, xb, SA, SB);                                   \
+    _Pragma("unroll") for (int i_ = 0; i_ < MT + NT; ++i_) { \
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    \
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    \
+    }                                                       \
+    __builtin_amdgcn_sched_barrier(0);                      \
+    WAIT;                                                   \
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);                 \
+    lds_barrier();                                          \
+    issue(CUR);                                             \
+    read(NXT, 0, xa, xb);                                   \
+    read_scales(NXT, TA, TB);                               \
+    mma1(ya, yb, SA, SB);                                   \
+    _Pragma("unroll") for (int i_ = 0; i_ < COPIES; ++i_) { \
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);    \
+      __builtin_amdgcn_sched_group_barrier(0x020, 1, 1);    \
+      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);    \
+    }                                                       \
+    __builtin_amdgcn_sched_barrier(0);                      \
+  }
+// A round of the ring, each stage in its buffer
+#define KQ_MX_ROUND()                                                                         \
+  if constexpr (RING == 4) {                                                                  \
+    KQ_MX_STEP(b0, b1, sa, sb, ta, tb, wait_stage(k))                                         \
+    KQ_MX_STEP(b1, b2, ta, tb, sa, sb, wait_stage(k))                                         \
+    KQ_MX_STEP(b2, b3, sa, sb, ta, tb, wait_stage(k))                                         \
+    KQ_MX_STEP(b3, b0, ta, tb, sa, sb, wait_stage(1))                                         \
+  } else {                                                                                    \
+    KQ_MX_STEP(b0, b1, sa, sb, ta, tb, wait_stage(k))                                         \
+    KQ_MX_STEP(b1, b2, ta, tb, sa, sb, wait_stage(k))                                         \
+    KQ_MX_STEP(b2, b0, sa, sb, ta, tb, wait_stage(1))                                         \
+    _Pragma("unroll") for (int m_ = 0; m_ < MT; ++m_) sa[m_] = ta[m_];                        \
+    _Pragma("unroll") for (int n_ = 0; n_ < NT; ++n_) sb[n_] = tb[n_];                        \
+  }
+  // Waits for the next stage's copies.  The 16 MT stores of the tile before are newer than the
+  // copies of this one's first stages: before the last stage of the first round (k = 0) they stay
+  // outstanding (the counter holds 63).  One block of instructions: a branch that the compiler
+  // sees would let it move the matrix instructions across.
+  constexpr int STEADY = (RING - 2) * COPIES, AFTER = STEADY + 16 * MT < 63 ? STEADY + 16 * MT : 63;
+  auto wait_stage = [&](int k) {
+    asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(%2)\n.Lstage%=:"
+                 :: "s"(k), "n"(AFTER), "n"(STEADY) : "scc", "memory");
+  };
+  const int rounds = (a.steps + RING - 1) / RING;   // stages past the end multiply zeros
+  const int size = a.y_bf16 ? 2 : 4;
+
+  for (;;) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int k = 0; k < NT; ++k) acc[m][k] = f32x16{};
+    id += turns;
+    const bool more = id < end;
+    Tile nt = t;
+    if (more) nt = at_id(id);
+    if (ROWS != X_ROWS && more && a.index) {
+      const int r = min(64 * (wave % MT) + lane, nt.last - 1 - nt.m0);
+      copy_lds<4>(rsrc(a.index + nt.m0, (int)ALL), 4 * r, (uint8_t*)(next_index + 64 * (wave % MT)));
+    }
+    // the next tile's copies follow the last ones of this tile: those of its last round
+    auto aim_next = [&]() {
+      if (more) aim(nt, [&](int r) { return a.index ? next_index[r] : nt.m0 + r; });
+    };
+    for (int k = 0; k < rounds; ++k) {
+      if (k == rounds - 1) {
+        if (ROWS != X_ROWS && k == 0) {   // the index's copies have no earlier barrier behind them
+          __builtin_amdgcn_s_waitcnt(wait_vm(0));
+          lds_barrier();
+        }
+        aim_next();
+      }
+      KQ_MX_ROUND()
+    }
+
+    // Lane l32 holds NT neighbouring columns of 16 MT rows.  The descriptor ends with the tile's
+    // last row, so stores of rows past it are dropped, and so are those of lanes whose columns
+    // pass the last one.
+    uint8_t* y0 = (uint8_t*)a.y + ((int64_t)t.m0 * a.ldy + t.n0) * size;
+    const int rows = t.last - t.m0, n = t.n0 + (wc * 32 + l32) * NT;
+    // Row m's sums, held in accumulation registers up to here: read out ahead of the branches
+    // below, all of them at once, they would not fit.
+    auto take = [&](int m, f32x16 (&v)[NT]) {
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        v[k] = acc[m][k];
+        asm volatile("" : "+a"(v[k]));
+      }
+    };
+    if (!a.y_far && (t.n0 + BN <= a.N || a.N % NT == 0)) {
+      const int pitch = (int)a.ldy * size;
+      const __amdgpu_buffer_rsrc_t ry = rsrc(y0, rows < BM ? rows * pitch : OOB);
+      const int first = (wr * 32 * MT + q * 4 * MT) * pitch + (wc * 32 + l32) * NT * size;
+      const int at = n + NT <= a.N ? first : OOB;
+      auto store = [&](auto put) {
+        int lane_at = at;
+        asm volatile("" : "+v"(lane_at));   // offsets of the two types apart: shared ones spill
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x16 sums[NT];
+          take(m, sums);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            float v[NT];
+#pragma unroll
+            for (int k = 0; k < NT; ++k) v[k] = sums[k][j];
+            put(lane_at + (((j >> 2) * 8 + (j & 3)) * MT + m) * pitch, v);
+          }
+        }
+      };
+      if (a.y_bf16)
+        store([&](int off, const float (&v)[NT]) { store_bf16<NT>(ry, off, v); });
+      else
+        store([&](int off, const float (&v)[NT]) { store_f32<NT>(ry, off, v); });
+    } else {
+      // a last column that ends inside a lane's, or rows too far apart for 32-bit offsets
+      int part = q;
+      asm volatile("" : "+v"(part));   // its addresses computed here, not ahead of the loop
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x16 sums[NT];
+        take(m, sums);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int r = wr * 32 * MT + ((j >> 2) * 8 + part * 4 + (j & 3)) * MT + m;
+          const int64_t at = r * a.ldy + n - t.n0;
+          const int cols = r < rows ? (int)min((int64_t)NT, a.N - n) : 0;
+#pragma unroll
+          for (int k = 0; k < NT; ++k)
+            if (k < cols) {
+              if (a.y_bf16)
+                ((uint16_t*)y0)[at + k] = to_bf16(sums[k][j]);
+              else
+                ((float*)y0)[at + k] = sums[k][j];
+            }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));   // fewer stores than the next round's waits count on
+    }
+    if (!more) break;
+    t = nt;
+  }
+#undef KQ_MX_ROUND
+#undef KQ_MX_STEP
+  // the ring's trailing copies must land before its LDS is released
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+}
+
+size_t code_bytes(int64_t rows, int64_t n) { return (size_t)rows * (size_t)(mx_pad(n) / 2); }
+size_t scale_bytes(int64_t rows, int64_t n) { return (size_t)rows * (size_t)(mx_pad(n) / 32); }
+
+// Whether an index can reach past the 32-bit offsets of the copies.
+bool x_far(const ProductArgs& p) { return p.rows * p.pitch >= 0xffff0000ll; }
+
+template <int MT, int NT, int WC, int RING>
+kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
+  constexpr int BM = 64 * MT, BN = 32 * NT * WC;
+  const int64_t tm = ceil_div(p.slots, BM) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
+  // one workgroup for each place on the card, or for each tile if there are fewer
+  constexpr int PLACES = 160 * 1024 / (RING * (BM + BN) * 68 + (1 << 13));
+  const int64_t total = std::min<int64_t>(ceil_div(tm * ceil_div(p.N, BN), 8),
+                                          ceil_div(device_cu_count() * std::min(PLACES, 4), 8)) * 8;
+  const dim3 grid((unsigned)total), block(128 * WC);
+  if (!p.offsets)
+    mx_tile_kernel<MT, NT, WC, RING, X_ROWS><<<grid, block, 0, s>>>(p);
+  else if (!x_far(p))
+    mx_tile_kernel<MT, NT, WC, RING, X_INDEX><<<grid, block, 0, s>>>(p);
+  else if constexpr (MT == 4 && NT == 4)
+    mx_tile_kernel<MT, NT, WC, RING, X_FAR><<<grid, block, 0, s>>>(p);
+  KQ_LAUNCHED("mx_tile_kernel");
+  return KQ_OK;
+}
+
+// Checks and quantises the activations (unless they are quantised already), then the product.
+kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, void* ws, size_t ws_bytes,
+                  hipStream_t s) {
+  int64_t block = 1;
+  if (x.type == KQ_MXFP4) {
+    if (x.rows < 0 || x.rows > MX_MAX_ROWS || x.n < 1 || x.n > MX_MAX_N)
+      return fail(KQ_ESHAPE, "%s: %lld rows of %lld values", fn, (long long)x.rows, (long long)x.n);
+    if (x.ld != mx_pad(x.n)) return fail(KQ_ESHAPE, "%s: quantised rows are contiguous: ldx = %lld", fn, (long long)mx_pad(x.n));
+    if (x.rows > 0 && (!x.x || !x.scales)) return fail(KQ_EINVAL, "%s: NULL quantised rows or scales", fn);
+    if (!aligned16(x.x) || !aligned16(x.scales)) return fail(KQ_EINVAL, "%s: quantised rows must be 16-byte aligned", fn);
+    if (x.d || x.sign || (x.had != 1 && x.had != 0)) return fail(KQ_EINVAL, "%s: quantised rows take no rescale, signs or rotation", fn);
+  } else {
+    KQ_TRY(mx_check_rows(fn, x, &block));
+    if (x.scales) return fail(KQ_EINVAL, "%s: scales go with quantised rows only", fn);
+  }
+  if (y_type != KQ_F32 && y_type != KQ_BF16) return fail(KQ_EINVAL, "%s: output type %d", fn, y_type);
+  if (p.N < 1 || p.N > MX_MAX_N) return fail(KQ_ESHAPE, "%s: %lld output channels", fn, (long long)p.N);
+  if (p.ldy < p.N) return fail(KQ_ESHAPE, "%s: ldy %lld < %lld", fn, (long long)p.ldy, (long long)p.N);
+  if (!p.wc || !p.ws) return fail(KQ_EINVAL, "%s: NULL weights", fn);
+  if (!aligned16(p.wc) || !aligned16(p.ws)) return fail(KQ_EINVAL, "%s: weights must be 16-byte aligned", fn);
+  if (p.slots > 0 && !p.y) return fail(KQ_EINVAL, "%s: NULL output", fn);
+  const int size = y_type == KQ_F32 ? 4 : 2;
+  if ((uintptr_t)p.y & (size - 1)) return fail(KQ_EINVAL, "%s: output not aligned to its type", fn);
+  p.pitch = mx_pad(x.n) / 2;
+  p.steps = (int)(mx_pad(x.n) / MX_GROUP);
+  p.rows = x.rows;
+  p.y_bf16 = y_type == KQ_BF16;
+  p.y_far = p.ldy > (1 << 20);
+  if (x.type == KQ_MXFP4) {
+    p.xc = (const uint8_t*)x.x;
+    p.xs = x.scales;
+  } else {
+    const size_t need = code_bytes(x.rows, x.n) + scale_bytes(x.rows, x.n);
+    if (need > 0 && (!ws || ws_bytes < need || !aligned16(ws)))
+      return fail(KQ_EWORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+    p.xc = (uint8_t*)ws;
+    p.xs = (uint8_t*)ws + code_bytes(x.rows, x.n);
+  }
+  if (p.slots == 0) return KQ_OK;
+  if (x.type != KQ_MXFP4) KQ_TRY(mx_quantize(x, block, (uint8_t*)p.xc, (uint8_t*)p.xs, nullptr, 0, s));
+  switch (p.offsets && x_far(p) ? 44 : testing_value(KQ_TESTING_MX_TILE, 44)) {
+    case 44: return launch_tiles<4, 4, 2, 4>(p, s);
+    case 448: return launch_tiles<4, 2, 4, 4>(p, s);
+    case 243: return launch_tiles<2, 4, 2, 3>(p, s);
+    case 423: return launch_tiles<4, 2, 2, 3>(p, s);
+    case 24: return launch_tiles<2, 4, 2, 4>(p, s);
+    case 42: return launch_tiles<4, 2, 2, 4>(p, s);
+    case 22: return launch_tiles<2, 2, 2, 4>(p, s);
+    case 12: return launch_tiles<1, 2, 2, 4>(p, s);
+    default: return launch_tiles<1, 1, 2, 4>(p, s);
+  }
+}
+
+}  // namespace
+}  // namespace kq
+
+extern "C" kq_status kq_mxfp4_workspace(int64_t rows, int64_t n, size_t* bytes) {
+  using namespace kq;
+  if (!bytes) return fail(KQ_EINVAL, "kq_mxfp4_workspace: NULL argument");
+  if (rows < 0 || rows > MX_MAX_ROWS || n < 1 || n > MX_MAX_N)
+    return fail(KQ_ESHAPE, "kq_mxfp4_workspace: %lld rows of %lld values", (long long)rows, (long long)n);
+  *bytes = code_bytes(rows, n) + scale_bytes(rows, n);
+  return KQ_OK;
+}
+
+extern "C" kq_status kq_mxfp4_linear(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                     const uint8_t* x_scales, const float* d, const int8_t* sign,
+                                     int64_t had, const uint8_t* w_codes, const uint8_t* w_scales,
+                                     int64_t out, void* y, int y_type, int64_t ldy, void* ws,
+                                     size_t ws_bytes, void* stream) {
+  using namespace kq;
+  ProductArgs p{};
+  p.wc = w_codes; p.ws = w_scales; p.N = out; p.experts = 1; p.slots = rows; p.y = y; p.ldy = ldy;
+  return product("kq_mxfp4_linear", MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, p, y_type, ws,
+                 ws_bytes, as_stream(stream));
+}
+
+extern "C" kq_status kq_mxfp4_experts(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                      const uint8_t* x_scales, const float* d, const int8_t* sign,
+                                      int64_t had, const int32_t* index, int64_t slots,
+                                      const int32_t* offsets, int experts, const uint8_t* w_codes,
+                                      const uint8_t* w_scales, int64_t out, void* y, int y_type,
+                                      int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  using namespace kq;
+  const char* fn = "kq_mxfp4_experts";
+  if (experts < 1 || experts > 4096) return fail(KQ_ESHAPE, "%s: %d experts (1 .. 4096)", fn, experts);
+  if (slots < 0 || slots > MX_MAX_ROWS) return fail(KQ_ESHAPE, "%s: %lld slots", fn, (long long)slots);
+  if (!offsets) return fail(KQ_EINVAL, "%s: NULL offsets", fn);
+  if (((uintptr_t)offsets | (uintptr_t)index) & 3) return fail(KQ_EINVAL, "%s: offsets or index not aligned", fn);
+  if (!index && slots > rows)
+    return fail(KQ_ESHAPE, "%s: %lld slots of %lld rows need an index", fn, (long long)slots, (long long)rows);
+  ProductArgs p{};
+  p.wc = w_codes; p.ws = w_scales; p.N = out; p.index = index; p.offsets = offsets; p.experts = experts;
+  p.slots = slots; p.y = y; p.ldy = ldy;
+  return product(fn, MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, p, y_type, ws, ws_bytes,
+                 as_stream(stream));
+}
