@@ -33,7 +33,10 @@ enum {
    * their direct paths, which longer rows take. */
   KQ_TESTING_ROW_LDS_BYTES = 2,
   /* Outputs per workgroup of the MXFP4 products. */
-  KQ_TESTING_MX_TILE = 3
+  KQ_TESTING_MX_TILE = 3,
+  /* Most rows (per expert, on average) of the MXFP4 products' few-row kernel; most activations that it quantises itself. */
+  KQ_TESTING_MX_FEW = 4,
+  KQ_TESTING_MX_FUSED = 5
 };
 
 /* Selects `value` for `knob`; value -1 restores the default.  KQ_EINVAL for an unknown knob

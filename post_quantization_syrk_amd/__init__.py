@@ -96,7 +96,7 @@ _SIGS = {
 
 # include/kq_testing.h: implementation selection for tests
 (KQ_TESTING_SYRK_KERNEL, KQ_TESTING_FACTOR_SUPERBLOCK, KQ_TESTING_ROW_LDS_BYTES,
- KQ_TESTING_MX_TILE) = range(4)
+ KQ_TESTING_MX_TILE, KQ_TESTING_MX_FEW, KQ_TESTING_MX_FUSED) = range(6)
 
 _lib = None
 

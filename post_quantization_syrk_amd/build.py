@@ -20,7 +20,7 @@ LIB = os.path.join(HERE, "libkq.so")
 
 SOURCES = ["common.hip", "syrk.hip", "reduce.hip", "alloc.hip", "fwht.hip", "gemm_f32.hip", "chol.hip",
            "gptq.hip", "deploy.hip", "flipflop.hip", "twosided.hip",
-           "mxfp4_quantize.hip", "mxfp4_product.hip"]
+           "mxfp4_quantize.hip", "mxfp4_product.hip", "mxfp4_few.hip"]
 # host-only arithmetic that must match IEEE operation by operation
 NO_CONTRACT = {"alloc.hip"}
 

@@ -32,8 +32,8 @@ int device_cu_count() {
   return cus;
 }
 
-constexpr int N_TESTING_KNOBS = 4;
-static std::atomic<int64_t> g_testing[N_TESTING_KNOBS] = {{-1}, {-1}, {-1}, {-1}};
+constexpr int N_TESTING_KNOBS = 6;
+static std::atomic<int64_t> g_testing[N_TESTING_KNOBS] = {{-1}, {-1}, {-1}, {-1}, {-1}, {-1}};
 
 int64_t testing_value(int knob, int64_t dflt) {
   if (knob < 0 || knob >= N_TESTING_KNOBS) return dflt;

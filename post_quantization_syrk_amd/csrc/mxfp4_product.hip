@@ -1,52 +1,15 @@
 // Products with layers held in MXFP4: y = Q(x~) W^T for one layer, or for one of several
 // layers per row (a mixture's experts), sums in fp32 on the scaled matrix instructions.
-#include "mxfp4.h"
+#include "mxfp4_tiles.h"
 
 #include <algorithm>
 
 namespace kq {
 namespace {
 
-typedef int i32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-
-struct ProductArgs {
-  const uint8_t* xc;       // rows x pitch
-  const uint8_t* xs;
-  int64_t rows;            // rows of x
-  const uint8_t* wc;       // experts x N x pitch
-  const uint8_t* ws;
-  int64_t N;
-  int64_t pitch;           // bytes of a quantised row: Kp / 2
-  int steps;               // Kp / 128
-  const int32_t* index;    // slot -> row of x, or NULL: the slot itself
-  const int32_t* offsets;  // experts + 1 first slots, or NULL: one layer, slots = rows
-  int experts;
-  int64_t slots;
-  void* y;
-  bool y_bf16;
-  bool y_far;              // rows of y too far apart for 32-bit offsets inside a tile
-  int64_t ldy;
-};
-
-// Slots [first, last) of expert e, kept inside [0, slots) whatever the offsets hold.
-__device__ __forceinline__ void expert_range(const ProductArgs& a, int e, int& first, int& last) {
-  const int lo = a.offsets[e], hi = a.offsets[e + 1], n = (int)a.slots;
-  first = min(max(lo, 0), n);
-  last = min(max(hi, first), n);
-}
-
 // Where a tile's rows of x come from: consecutive rows, rows behind an index, or rows behind an
 // index of an x too large for 32-bit offsets.
 enum { X_ROWS, X_INDEX, X_FAR };
-
-// Rows [m0, last) of y with expert e's layer, columns from n0: one tile.
-struct Tile {
-  int e, m0, last, n0;
-};
 
 // Experts whose tiles a kernel finds through its table; more are searched in memory.
 constexpr int TABLE = 1024;
@@ -98,28 +61,7 @@ __device__ __forceinline__ void find_rows(const ProductArgs& a, const ExpertTabl
     t.last = __builtin_amdgcn_readfirstlane(max(tab.first[t.e + 1], tab.first[t.e]));
     return;
   }
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    int c = 0, first = 0, last = 0;
-    if (e0 + lane < a.experts) {
-      expert_range(a, e0 + lane, first, last);
-      c = (last - first + BM - 1) / BM;
-    }
-    int sum = c;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(sum, o);
-      if (lane >= o) sum += v;
-    }
-    const int all = __builtin_amdgcn_readlane(sum, 63);
-    if (mt < all) {
-      const int src = __ffsll((unsigned long long)__ballot(sum > mt)) - 1;
-      t.e = __builtin_amdgcn_readfirstlane(e0 + src);
-      t.m0 = __builtin_amdgcn_readfirstlane(__shfl(first, src) + (mt - __shfl(sum - c, src)) * BM);
-      t.last = __builtin_amdgcn_readfirstlane(__shfl(last, src));
-      return;
-    }
-    mt -= all;
-  }
+  search_rows<BM>(a, mt, t);
 }
 
 // Tile `id` of tm x tn, counted in bands of G row tiles so that neighbours share panels.
@@ -140,9 +82,6 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const ExpertTable&
   return t;
 }
 
-// Zeros that copies of rows outside x read.
-__device__ __attribute__((aligned(16))) uint32_t g_zeros[4];
-
 // One wave's copy of 64 pieces of SIZE bytes into LDS, piece l to `to` + SIZE l; a lane whose
 // offset lies outside the descriptor copies zeros.
 template <int SIZE>
@@ -155,11 +94,6 @@ __device__ __forceinline__ void copy_lds(__amdgpu_buffer_rsrc_t r, unsigned off,
 }
 __device__ __forceinline__ void copy_lds(const uint8_t* from, uint8_t* to) {
   __builtin_amdgcn_global_load_lds((const void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
-}
-
-__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
-__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
-  return __builtin_bit_cast(unsigned, bf16x2{(__bf16)lo, (__bf16)hi});
 }
 
 // Stores W values side by side at byte offset `off` (a masked offset stores nothing).
@@ -182,8 +116,6 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
   else
     __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v[0]), r, off, 0, 0);
 }
-
-__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
 
 // Tiles of BM x BN outputs, 128 of K per stage, waves in 2 x WC, each with MT x NT accumulators
 // of 32 x 32.  A workgroup takes tile after tile; the copies of the next tile's first stages
@@ -562,8 +494,11 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
     p.xs = (uint8_t*)ws + code_bytes(x.rows, x.n);
   }
   if (p.slots == 0) return KQ_OK;
+  const bool few = mx_few(p);
+  if (few && x.type != KQ_MXFP4 && mx_few_fused(p, x, block)) return mx_few_product(p, x, block, true, s);
   if (x.type != KQ_MXFP4) KQ_TRY(mx_quantize(x, block, (uint8_t*)p.xc, (uint8_t*)p.xs, nullptr, 0, s));
-  switch (p.offsets && x_far(p) ? 44 : testing_value(KQ_TESTING_MX_TILE, 44)) {
+  if (few) return mx_few_product(p, x, block, false, s);
+  switch (p.offsets && x_far(p) ? 44 : testing_value(KQ_TESTING_MX_TILE, 448)) {
     case 44: return launch_tiles<4, 4, 2, 4>(p, s);
     case 448: return launch_tiles<4, 2, 4, 4>(p, s);
     case 243: return launch_tiles<2, 4, 2, 3>(p, s);

@@ -1,0 +1,94 @@
+// Device side that the MXFP4 products share: their arguments, the tiles of y, types.
+#pragma once
+
+#include "mxfp4.h"
+
+namespace kq {
+
+// A product's arguments on the device.
+struct ProductArgs {
+  const uint8_t* xc;       // rows x pitch
+  const uint8_t* xs;
+  int64_t rows;            // rows of x
+  const uint8_t* wc;       // experts x N x pitch
+  const uint8_t* ws;
+  int64_t N;
+  int64_t pitch;           // bytes of a quantised row: Kp / 2
+  int steps;               // Kp / 128
+  const int32_t* index;    // slot -> row of x, or NULL: the slot itself
+  const int32_t* offsets;  // experts + 1 first slots, or NULL: one layer, slots = rows
+  int experts;
+  int64_t slots;
+  void* y;
+  bool y_bf16;
+  bool y_far;              // rows of y too far apart for 32-bit offsets inside a tile
+  int64_t ldy;
+};
+
+// A product with few rows (mxfp4_few.hip): whether it is one, and its launch.  x: the rows to
+// quantise on the way in, at most as many as `mx_few_rows` says, or quantised rows (KQ_MXFP4).
+bool mx_few(const ProductArgs& p);
+bool mx_few_fused(const ProductArgs& p, const MxRows& x, int64_t block);
+kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s);
+
+namespace {
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+
+// Slots [first, last) of expert e, kept inside [0, slots) whatever the offsets hold.
+__device__ __forceinline__ void expert_range(const ProductArgs& a, int e, int& first, int& last) {
+  const int lo = a.offsets[e], hi = a.offsets[e + 1], n = (int)a.slots;
+  first = min(max(lo, 0), n);
+  last = min(max(hi, first), n);
+}
+
+// Rows [m0, last) of y with expert e's layer, columns from n0: one tile.
+struct Tile {
+  int e, m0, last, n0;
+};
+
+// The expert of row tile mt, counted over the experts, and the tile's rows; false past the last.
+template <int BM>
+__device__ __forceinline__ bool search_rows(const ProductArgs& a, int mt, Tile& t) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 < a.experts; e0 += 64) {
+    int c = 0, first = 0, last = 0;
+    if (e0 + lane < a.experts) {
+      expert_range(a, e0 + lane, first, last);
+      c = (last - first + BM - 1) / BM;
+    }
+    int sum = c;   // inclusive sum over the lanes
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    const int all = __builtin_amdgcn_readlane(sum, 63);
+    if (mt < all) {
+      const int src = __ffsll((unsigned long long)__ballot(sum > mt)) - 1;
+      t.e = __builtin_amdgcn_readfirstlane(e0 + src);
+      t.m0 = __builtin_amdgcn_readfirstlane(__shfl(first, src) + (mt - __shfl(sum - c, src)) * BM);
+      t.last = __builtin_amdgcn_readfirstlane(__shfl(last, src));
+      return true;
+    }
+    mt -= all;
+  }
+  return false;
+}
+
+// Zeros that copies of rows outside x read.
+__device__ __attribute__((aligned(16))) uint32_t g_zeros[4];
+
+__device__ __forceinline__ uint16_t to_bf16(float v) { return __builtin_bit_cast(uint16_t, (__bf16)v); }
+__device__ __forceinline__ unsigned pack_bf16(float lo, float hi) {
+  return __builtin_bit_cast(unsigned, bf16x2{(__bf16)lo, (__bf16)hi});
+}
+
+__device__ __forceinline__ i32x8 widen(i32x4 v) { return i32x8{v[0], v[1], v[2], v[3], 0, 0, 0, 0}; }
+
+}  // namespace
+}  // namespace kq

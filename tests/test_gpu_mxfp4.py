@@ -463,3 +463,42 @@ def test_refusals_of_the_binding():
         kq.kq_mxfp4_experts(x, None, off.long(), ec, es, y)
     with pytest.raises(ValueError):
         kq.kq_mxfp4_experts(x, None, off[:2], ec, es, y)
+
+
+def _forced(knobs):
+    """A context in which the implementation paths are chosen by `knobs` (name -> value)."""
+    from contextlib import ExitStack
+    kq = _kq()
+    stack = ExitStack()
+    for name, value in knobs.items():
+        stack.enter_context(kq.testing_select(getattr(kq, name), value))
+    return stack
+
+
+PATHS = [dict(KQ_TESTING_MX_FUSED=0), dict(KQ_TESTING_MX_FUSED=1 << 20),
+         *(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (448, 24, 42, 22, 12))]
+
+
+@pytest.mark.parametrize("path", PATHS, ids=str)
+@pytest.mark.parametrize("rows,n,out,had", [(1, 4096, 300, 4096), (3, 1000, 515, 8), (13, 640, 64, 128), (16, 2048, 96, 2048),
+                                            (2, 8192, 130, 8192), (40, 384, 257, 128), (64, 1536, 300, 512),
+                                            (150, 256, 1000, 256), (700, 1152, 520, 128), (1300, 128, 1100, 128)])
+def test_every_path(rows, n, out, had, path):
+    """Each implementation gives the product within the bound, for a layer and for experts."""
+    announce(f"mxfp4 {rows}x{n} -> {out} {path}")
+    kq = _kq()
+    rng = np.random.default_rng(rows + n)
+    x = _rows(rng, rows, n, "bf16")
+    d, sg = _processing(rng, n, True, True)
+    wc, ws, wv = _layer(rng, out, n)
+    ec, es, ev = _layer(rng, 72, n, 5)
+    index, offsets = _sorted_slots(rng, rows, 2, 5, 1.0)
+    xq = om.mx_round(om.mx_rotate_f32(x.float().numpy(), d, sg, had))
+    want, mag = _experts_ref(xq, index, offsets, ev, 2 * rows, rows)
+    with _forced(path):
+        for kind in ("f32", "bf16"):
+            y, z = _empty((rows, out), kind), _empty((2 * rows, 72), kind)
+            kq.kq_mxfp4_linear(x.cuda(), wc, ws, y, d=_dev(d), sign=_dev(sg), had=had)
+            _close(y, xq, wv, kind == "bf16")
+            kq.kq_mxfp4_experts(x.cuda(), _dev(index), _dev(offsets), ec, es, z, d=_dev(d), sign=_dev(sg), had=had)
+            _experts_check(z, want, mag, n, kind == "bf16")
