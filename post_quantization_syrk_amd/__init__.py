@@ -443,31 +443,51 @@ def kq_mxfp4_empty(rows: int, n: int, experts: int | None = None, device="cuda")
             torch.empty((*lead, np_ // 128, rows, 4), dtype=torch.uint8, device=device))
 
 
+# One token's call takes less time on the GPU than the checks of the functions above take here, so
+# those below read each tensor's properties once and pass plain integers.
 def _mx_type(t, name: str) -> int:
     torch = _torch()
-    if t.dtype is torch.bfloat16:
-        return KQ_BF16
-    if t.dtype is torch.float32:
-        return KQ_F32
-    raise TypeError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
+    if isinstance(t, torch.Tensor):
+        if t.dtype is torch.bfloat16:
+            return KQ_BF16
+        if t.dtype is torch.float32:
+            return KQ_F32
+        raise TypeError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
+    raise TypeError(f"{name} must be a device (cuda/hip) tensor")
 
 
-def _mx_vectors(d, sign, n: int):
+def _mx_ptr(t, name: str, dtype) -> int:
     torch = _torch()
-    for v, name in ((d, "d"), (sign, "sign")):
-        if v is not None and (v.numel() != n or not v.is_contiguous()):
-            raise ValueError(f"{name} must hold {n} contiguous entries")
-    return _dev_ptr(d, "d", (torch.float32,), True), _dev_ptr(sign, "sign", (torch.int8,), True)
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a device (cuda/hip) tensor")
+    if dtype is not None and t.dtype is not dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
+    return t.data_ptr()
 
 
-def _mx_check(codes, scales, rows: int, n: int, lead: tuple, name: str):
+def _mx_stream(stream) -> int:
     torch = _torch()
-    np_ = kq_mxfp4_padded(n)
-    if tuple(codes.shape) != (*lead, rows, np_ // 2) or not codes.is_contiguous():
-        raise ValueError(f"{name} codes must be contiguous {(*lead, rows, np_ // 2)}")
-    if tuple(scales.shape) != (*lead, np_ // 128, rows, 4) or not scales.is_contiguous():
-        raise ValueError(f"{name} scales must be contiguous {(*lead, np_ // 128, rows, 4)}")
-    return _dev_ptr(codes, f"{name} codes", (torch.uint8,)), _dev_ptr(scales, f"{name} scales", (torch.uint8,))
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
+
+
+def _mx_vector(v, name: str, n: int, dtype):
+    if v is None:
+        return None
+    if v.numel() != n or not v.is_contiguous():
+        raise ValueError(f"{name} must hold {n} contiguous entries")
+    return _mx_ptr(v, name, dtype)
+
+
+def _mx_check(codes, scales, shape: tuple, n: int, name: str):
+    torch = _torch()
+    groups = -(-n // 128)
+    if codes.shape != (*shape, 64 * groups) or not codes.is_contiguous():
+        raise ValueError(f"{name} codes must be contiguous {(*shape, 64 * groups)}")
+    if scales.shape != (*shape[:-1], groups, shape[-1], 4) or not scales.is_contiguous():
+        raise ValueError(f"{name} scales must be contiguous {(*shape[:-1], groups, shape[-1], 4)}")
+    return _mx_ptr(codes, f"{name} codes", torch.uint8), _mx_ptr(scales, f"{name} scales", torch.uint8)
 
 
 def kq_mxfp4_quantize(src, codes, scales, d=None, sign=None, had: int = 1, values=None, stream=None) -> None:
@@ -475,19 +495,23 @@ def kq_mxfp4_quantize(src, codes, scales, d=None, sign=None, had: int = 1, value
     P D^-1 src; `values` (bf16, rows x n, optional) receives what they stand for."""
     torch = _torch()
     lib = load_library()
+    xt = _mx_type(src, "src")
     rows, n = src.shape
-    cp, sp = _mx_check(codes, scales, rows, n, (), "output")
-    dp, gp = _mx_vectors(d, sign, n)
-    if values is not None and values.shape != src.shape:
-        raise ValueError("values must have src's shape")
-    st = lib.kq_mxfp4_quantize(
-        _dev_ptr(src, "src"), _mx_type(src, "src"), rows, n, _ld(src, "src"), dp, gp, had, cp, sp,
-        _dev_ptr(values, "values", (torch.bfloat16,), True),
-        0 if values is None else _ld(values, "values"), _stream(stream))
-    _check(st, "kq_mxfp4_quantize")
+    cp, sp = _mx_check(codes, scales, (rows,), n, "output")
+    vp, ldv = None, 0
+    if values is not None:
+        if values.shape != (rows, n):
+            raise ValueError("values must have src's shape")
+        vp, ldv = _mx_ptr(values, "values", torch.bfloat16), _ld(values, "values")
+    st = lib.kq_mxfp4_quantize(_mx_ptr(src, "src", None), xt, rows, n, _ld(src, "src"),
+                               _mx_vector(d, "d", n, torch.float32), _mx_vector(sign, "sign", n, torch.int8), had,
+                               cp, sp, vp, ldv, _mx_stream(stream))
+    if st:
+        _check(st, "kq_mxfp4_quantize")
 
 
 def kq_mxfp4_workspace(rows: int, n: int) -> int:
+    """Workspace bytes of kq_mxfp4_linear and kq_mxfp4_experts for `rows` rows of n activations."""
     lib = load_library()
     b = ctypes.c_size_t(0)
     _check(lib.kq_mxfp4_workspace(rows, n, ctypes.byref(b)), "kq_mxfp4_workspace")
@@ -500,16 +524,19 @@ def _mx_rows(x, x_scales, d, sign, n, ws):
     if x_scales is not None:
         if n is None:
             raise ValueError("quantised rows need n, their number of values")
+        if d is not None or sign is not None:
+            raise ValueError("quantised rows take no rescale and no signs")
         rows = x.shape[0]
-        xp, sp = _mx_check(x, x_scales, rows, n, (), "x")
-        return xp, KQ_MXFP4, rows, n, kq_mxfp4_padded(n), sp, *_mx_vectors(d, sign, n), None, 0
+        xp, sp = _mx_check(x, x_scales, (rows,), n, "x")
+        return xp, KQ_MXFP4, rows, n, kq_mxfp4_padded(n), sp, None, None, None, 0
+    xt = _mx_type(x, "x")
     rows, cols = x.shape
     if n is not None and n != cols:
         raise ValueError(f"x has {cols} columns, not {n}")
     if ws is None:
         ws = torch.empty(kq_mxfp4_workspace(rows, cols), dtype=torch.uint8, device=x.device)
-    return (_dev_ptr(x, "x"), _mx_type(x, "x"), rows, cols, _ld(x, "x"), None, *_mx_vectors(d, sign, cols),
-            _dev_ptr(ws, "ws", (torch.uint8,)), ws.numel())
+    return (_mx_ptr(x, "x", None), xt, rows, cols, _ld(x, "x"), None, _mx_vector(d, "d", cols, torch.float32),
+            _mx_vector(sign, "sign", cols, torch.int8), _mx_ptr(ws, "ws", torch.uint8), ws.numel())
 
 
 def kq_mxfp4_linear(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1, x_scales=None,
@@ -519,12 +546,14 @@ def kq_mxfp4_linear(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: in
     lib = load_library()
     xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
     out = w_codes.shape[0]
-    cp, sp = _mx_check(w_codes, w_scales, out, n, (), "weight")
-    if tuple(y.shape) != (rows, out):
+    cp, sp = _mx_check(w_codes, w_scales, (out,), n, "weight")
+    yt = _mx_type(y, "y")
+    if y.shape != (rows, out):
         raise ValueError(f"y must be {(rows, out)}")
-    st = lib.kq_mxfp4_linear(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, _dev_ptr(y, "y"),
-                             _mx_type(y, "y"), _ld(y, "y"), wp, wb, _stream(stream))
-    _check(st, "kq_mxfp4_linear")
+    st = lib.kq_mxfp4_linear(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, _mx_ptr(y, "y", None), yt,
+                             _ld(y, "y"), wp, wb, _mx_stream(stream))
+    if st:
+        _check(st, "kq_mxfp4_linear")
 
 
 def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1,
@@ -536,16 +565,14 @@ def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, s
     lib = load_library()
     xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
     experts, out = w_codes.shape[0], w_codes.shape[1]
-    cp, sp = _mx_check(w_codes, w_scales, out, n, (experts,), "weight")
-    slots = y.shape[0]
-    if tuple(y.shape) != (slots, out):
+    cp, sp = _mx_check(w_codes, w_scales, (experts, out), n, "weight")
+    yt = _mx_type(y, "y")
+    slots, cols = y.shape
+    if cols != out:
         raise ValueError(f"y must have {out} columns")
-    if tuple(offsets.shape) != (experts + 1,) or not offsets.is_contiguous():
-        raise ValueError(f"offsets must hold {experts + 1} contiguous entries")
-    if index is not None and (tuple(index.shape) != (slots,) or not index.is_contiguous()):
-        raise ValueError(f"index must hold {slots} contiguous entries")
-    i32 = (torch.int32,)
-    st = lib.kq_mxfp4_experts(xp, xt, rows, n, ldx, xsp, dp, gp, had, _dev_ptr(index, "index", i32, True), slots,
-                              _dev_ptr(offsets, "offsets", i32), experts, cp, sp, out, _dev_ptr(y, "y"),
-                              _mx_type(y, "y"), _ld(y, "y"), wp, wb, _stream(stream))
-    _check(st, "kq_mxfp4_experts")
+    st = lib.kq_mxfp4_experts(xp, xt, rows, n, ldx, xsp, dp, gp, had,
+                              _mx_vector(index, "index", slots, torch.int32), slots,
+                              _mx_vector(offsets, "offsets", experts + 1, torch.int32), experts, cp, sp, out,
+                              _mx_ptr(y, "y", None), yt, _ld(y, "y"), wp, wb, _mx_stream(stream))
+    if st:
+        _check(st, "kq_mxfp4_experts")

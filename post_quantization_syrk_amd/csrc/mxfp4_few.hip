@@ -21,11 +21,12 @@ struct RowArgs {
   const int8_t* sign;
   int had;
   float isb;
+  bool wide;
 };
 
 // Rotates and quantises the tile's rows into LDS: codes [rows][pitch], then scale dwords
 // [rows][steps].
-template <typename T, int WAVES, bool LONG>
+template <typename T, int WAVES, bool LONG, bool WIDE>
 __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArgs& x, const Tile& t, float* lds,
                                               uint8_t* codes, int* scales) {
   const int rows = t.last - t.m0, lane = threadIdx.x & 63;
@@ -36,15 +37,20 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
   for (int64_t c0 = 0; c0 < 2 * a.pitch; c0 += SPAN * WAVES) {
     const int64_t c = c0 + 8 * threadIdx.x;
     float f[8], r[8], next[8];
-    const T* p = source(0);
-    load_columns<T, false>(p, c, p ? x.n : 0, r);
+    auto load = [&](int k, float (&v)[8]) {
+      const T* p = source(k);
+      if (p) {
+        load_columns<T, WIDE>(p, c, x.n, v);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = 0.f;
+      }
+    };
+    load(0, r);
     const bool scaled = x.d || x.sign;
     if (scaled) factors(x.d, x.sign, c, x.n, f);
     for (int k = 0; k < rows; ++k) {
-      if (k + 1 < rows) {
-        p = source(k + 1);
-        load_columns<T, false>(p, c, p ? x.n : 0, next);
-      }
+      if (k + 1 < rows) load(k + 1, next);
       rotate<WAVES, LONG>(r, scaled, f, x.had, x.isb, lds);
       float s;
       bool bad;
@@ -60,10 +66,13 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
   }
 }
 
-// 16 MT rows of y by 16 NT columns per workgroup: its waves take K in equal parts, U steps of 128
-// at a time, and add their sums through LDS in wave order.  A lane holds 16 bytes of one row of
-// the layer per step: the first operand of the 16 x 16 x 128 instruction; rows of x are the
-// second, so a lane's four sums are neighbouring columns of one row of y.
+// 16 MT rows of y by 16 NT columns per workgroup: its waves take K in equal parts, U pairs of
+// 128 at a time, and add their sums through LDS in wave order.  Rows of the layer are the first
+// operand of the 16 x 16 x 128 instruction and rows of x the second, so a lane's four sums are
+// neighbouring columns of one row of y.  Which 32 of K a lane's operand holds is free as long as
+// both operands agree: lane group q takes blocks 2 q and 2 q + 1 of a pair's eight, one per
+// instruction, so its two loads are neighbours, a row's line is read whole, and both blocks'
+// scales lie in one dword.
 // T: void for quantised activations, else their type, quantised here (MT = 1).
 template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T>
 __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowArgs x) {
@@ -82,7 +91,8 @@ __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowAr
     t.last = (int)a.slots;
   }
   t.last = min(t.last, t.m0 + BM);
-  const int per = (a.steps + WAVES - 1) / WAVES, s0 = wave * per, s1 = min(s0 + per, a.steps);
+  const int pairs = (a.steps + 1) / 2, per = (pairs + WAVES - 1) / WAVES;
+  const int p0 = wave * per, p1 = min(p0 + per, pairs);
 
   const uint8_t* wc = a.wc + ((int64_t)t.e * a.N + t.n0) * a.pitch;
   const uint8_t* ws = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
@@ -90,63 +100,76 @@ __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowAr
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
     const unsigned r = (unsigned)min((int64_t)16 * n + l16, a.N - 1 - t.n0);
-    ow[n] = r * (unsigned)a.pitch + 16 * q;
+    ow[n] = r * (unsigned)a.pitch + 32 * q;
     os[n] = r * 4;
   }
   // rows of x: quantised ones in memory (zeros for a row outside x), or those quantised below
   const uint8_t* px[MT];
   const uint8_t* ps[MT];
   int64_t stepx[MT], steps[MT];
-  const float* spare = lds + rotate_floats(WAVES);
-  uint8_t* codes = (uint8_t*)spare;
+  uint8_t* codes = (uint8_t*)(lds + rotate_floats(WAVES));
   int* scales = (int*)(codes + (t.last - t.m0) * a.pitch);
 #pragma unroll
   for (int m = 0; m < MT; ++m) {
     const int slot = min(t.m0 + 16 * m + l16, t.last - 1);
     if (FUSED) {
-      px[m] = codes + (slot - t.m0) * a.pitch + 16 * q;
+      px[m] = codes + (slot - t.m0) * a.pitch + 32 * q;
       ps[m] = (const uint8_t*)(scales + (slot - t.m0) * a.steps);
       stepx[m] = 64;
       steps[m] = 4;
     } else {
       const int row = EXPERTS && a.index ? a.index[slot] : slot;
       const bool in = row >= 0 && row < a.rows;
-      px[m] = in ? a.xc + row * a.pitch + 16 * q : (const uint8_t*)g_zeros;
+      px[m] = in ? a.xc + row * a.pitch + 32 * q : (const uint8_t*)g_zeros;
       ps[m] = in ? a.xs + (int64_t)row * 4 : (const uint8_t*)g_zeros;
       stepx[m] = in ? 64 : 0;
       steps[m] = in ? a.rows * 4 : 0;
     }
   }
-  i32x4 wv[U][NT], xv[U][MT];
+  // Pair p of the lane: its first step of 128 is 2 p + q / 2.  The last pair may lack its second
+  // step: lane groups 2 and 3 then read the first one's again and take zeros for x.
+  i32x4 wv[U][NT][2], xv[U][MT][2];
   int sw[U][NT], sx[U][MT];
-  auto load_w = [&](int s) {
+  auto lacks = [&](int p) { return 2 * p + 1 >= a.steps && q >= 2; };
+  auto load_w = [&](int first) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = min(s + u, s1 - 1);
+      const int p = min(first + u, p1 - 1), back = lacks(p);
+      const int64_t k = 2 * p + (q >> 1) - back;
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        wv[u][n] = *(const i32x4*)(wc + 64 * k + ow[n]);
+        const uint8_t* from = wc + 128 * (int64_t)p + (ow[n] - 64 * back);
+        wv[u][n][0] = *(const i32x4*)from;
+        wv[u][n][1] = *(const i32x4*)(from + 16);
         sw[u][n] = *(const int*)(ws + 4 * a.N * k + os[n]);
       }
     }
   };
-  auto load_x = [&](int s) {
+  auto load_x = [&](int first) {
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t k = min(s + u, s1 - 1);
+      const int p = min(first + u, p1 - 1), back = lacks(p);
 #pragma unroll
       for (int m = 0; m < MT; ++m) {
-        xv[u][m] = *(const i32x4*)(px[m] + stepx[m] * k);
-        sx[u][m] = *(const int*)(ps[m] + steps[m] * k);
+        const uint8_t* from = px[m] + stepx[m] * (2 * p - back);
+        xv[u][m][0] = *(const i32x4*)from;
+        xv[u][m][1] = *(const i32x4*)(from + (stepx[m] >> 2));
+        sx[u][m] = *(const int*)(ps[m] + steps[m] * (2 * p + (q >> 1) - back));
+        if (2 * p + 1 >= a.steps) {
+          xv[u][m][0] = back ? i32x4{} : xv[u][m][0];
+          xv[u][m][1] = back ? i32x4{} : xv[u][m][1];
+        }
       }
     }
   };
-  if (s0 < s1) load_w(s0);
+  if (p0 < p1) load_w(p0);
   if constexpr (FUSED) {
-    if (x.had <= SPAN)
-      quantize_rows<T, WAVES, false>(a, x, t, lds, codes, scales);
+    if (!x.wide)
+      quantize_rows<T, WAVES, true, false>(a, x, t, lds, codes, scales);
+    else if (x.had <= SPAN)
+      quantize_rows<T, WAVES, false, true>(a, x, t, lds, codes, scales);
     else
-      quantize_rows<T, WAVES, true>(a, x, t, lds, codes, scales);
+      quantize_rows<T, WAVES, true, true>(a, x, t, lds, codes, scales);
     __syncthreads();
   }
   f32x4 acc[MT][NT];
@@ -154,18 +177,23 @@ __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowAr
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{};
-  for (int s = s0; s < s1; s += U) {
-    if (s > s0) load_w(s);
-    load_x(s);
+  const int shift = 16 * (q & 1);   // the lane's two scales: bytes 2 q and 2 q + 1 of a pair's eight
+  for (int p = p0; p < p1; p += U) {
+    if (p > p0) load_w(p);
+    load_x(p);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (s + u >= s1) break;
+      if (p + u >= p1) break;
 #pragma unroll
       for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
-          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              widen(wv[u][n]), widen(xv[u][m]), acc[m][n], 4, 4, 0, sw[u][n] >> (8 * q), 0, sx[u][m] >> (8 * q));
+        for (int n = 0; n < NT; ++n) {
+          const int s = sw[u][n] >> shift, v = sx[u][m] >> shift;
+          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[u][n][0]), widen(xv[u][m][0]),
+                                                                       acc[m][n], 4, 4, 0, s, 0, v);
+          acc[m][n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(widen(wv[u][n][1]), widen(xv[u][m][1]),
+                                                                       acc[m][n], 4, 4, 1, s, 1, v);
+        }
     }
   }
   // sums [wave][row][column]
@@ -226,30 +254,26 @@ bool mx_few_fused(const ProductArgs& p, const MxRows& x, int64_t block) {
 }
 
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s) {
-  RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block))};
+  RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block)), wide_rows(x)};
   const int bm = fused ? 16 : few_rows(p);
-  // waves per workgroup: enough of them to fill the card (eight per SIMD and more), as long as
-  // each has two steps of K
-  const int64_t tiles = ceil_div(p.N, 16) * (p.offsets ? std::min<int64_t>(p.slots, std::max<int64_t>(p.experts, ceil_div(p.slots, bm)))
-                                                       : ceil_div(p.slots, bm));
-  const int64_t want = ceil_div(device_cu_count() * 12, tiles);
-  int waves = want <= 4 ? 4 : want <= 8 ? 8 : 16;
-  while (waves > 4 && p.steps < 2 * waves) waves /= 2;
+  // Columns per workgroup: 64, so that its rows of x and its fixed costs serve more of the layer, or
+  // as few as leave a workgroup for five of eight compute units (16 rows, 4096 x 4096: 3.7 us
+  // with 16, 6.5 with 64; 11008 x 4096: 8.2 and 7.6; 28672 x 8192: 30 and 24).
+  const int64_t tm = p.offsets ? std::min<int64_t>(p.slots, std::max<int64_t>(p.experts, ceil_div(p.slots, bm))) : ceil_div(p.slots, bm);
+  const int64_t enough = device_cu_count() * 5 / 8;
+  const int nt = ceil_div(p.N, 64) * tm >= enough ? 4 : ceil_div(p.N, 32) * tm >= enough ? 2 : 1;
   if (fused) {
-    if (block > 4096) waves = 16;
-    else if (block > 2048) waves = std::max(waves, 8);
     const bool f32 = x.type == KQ_F32;
-    switch (waves) {
-      case 4: return f32 ? launch<4, 1, 1, 8, float>(p, r, s) : launch<4, 1, 1, 8, uint16_t>(p, r, s);
-      case 8: return f32 ? launch<8, 1, 1, 8, float>(p, r, s) : launch<8, 1, 1, 8, uint16_t>(p, r, s);
-      default: return f32 ? launch<16, 1, 1, 4, float>(p, r, s) : launch<16, 1, 1, 4, uint16_t>(p, r, s);
-    }
+#define KQ_FEW(NT, U)                                                                                   \
+  (block > 8 * SPAN ? (f32 ? launch<16, 1, NT, 1, float>(p, r, s) : launch<16, 1, NT, 1, uint16_t>(p, r, s)) \
+                    : (f32 ? launch<8, 1, NT, U, float>(p, r, s) : launch<8, 1, NT, U, uint16_t>(p, r, s)))
+    return nt == 4 ? KQ_FEW(4, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
+#undef KQ_FEW
   }
-  if (bm == 16)
-    return waves == 4 ? launch<4, 1, 1, 8, void>(p, r, s) : waves == 8 ? launch<8, 1, 1, 8, void>(p, r, s)
-                                                                       : launch<16, 1, 1, 4, void>(p, r, s);
-  if (bm == 32) return waves == 4 ? launch<4, 2, 2, 4, void>(p, r, s) : launch<8, 2, 2, 4, void>(p, r, s);
-  return waves == 4 ? launch<4, 4, 2, 2, void>(p, r, s) : launch<8, 4, 2, 2, void>(p, r, s);
+#define KQ_FEW(MT) \
+  (nt == 4 ? launch<8, MT, 4, 1, void>(p, r, s) : nt == 2 ? launch<8, MT, 2, 2, void>(p, r, s) : launch<8, MT, 1, 2, void>(p, r, s))
+  return bm == 16 ? KQ_FEW(1) : bm == 32 ? KQ_FEW(2) : KQ_FEW(4);
+#undef KQ_FEW
 }
 
 }  // namespace kq

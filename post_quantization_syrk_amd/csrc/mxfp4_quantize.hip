@@ -131,7 +131,7 @@ kq_status mx_quantize(const MxRows& r, int64_t block, uint8_t* codes, uint8_t* s
   a.codes = codes; a.scales = scales; a.values = values; a.ldv = ldv;
   a.v_wide = aligned16(values) && ldv % 8 == 0;
   // rows that start 16 bytes aligned are read 16 bytes at a time
-  const bool wide = aligned16(r.x) && r.ld % (r.type == KQ_F32 ? 4 : 8) == 0;
+  const bool wide = wide_rows(r);
   if (r.type == KQ_F32) return wide ? launch<float, true>(a, s) : launch<float, false>(a, s);
   return wide ? launch<uint16_t, true>(a, s) : launch<uint16_t, false>(a, s);
 }

@@ -16,38 +16,55 @@ constexpr int SPAN = 512;        // columns that a wave holds: 8 neighbouring on
 __device__ __forceinline__ float load1(const float* p) { return *p; }
 __device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((unsigned)*p << 16); }
 
-__device__ __forceinline__ void load8(const float* p, float (&r)[8]) {
-  const float4 u = *(const float4*)p, v = *(const float4*)(p + 4);
-  r[0] = u.x; r[1] = u.y; r[2] = u.z; r[3] = u.w;
-  r[4] = v.x; r[5] = v.y; r[6] = v.z; r[7] = v.w;
-}
-__device__ __forceinline__ void load8(const uint16_t* p, float (&r)[8]) {
-  const u32x4 u = *(const u32x4*)p;
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    r[2 * k] = __uint_as_float(u[k] << 16);
-    r[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-  }
-}
-
-// The lane's columns c .. c + 7 of a row of n values, zero past its end.
+// The lane's columns c .. c + 7 of a row of n values, zero past its end, without a branch around
+// the loads (where paths join the compiler waits for all of them).  WIDE: 16 bytes at a time, of a
+// row that starts 16-byte aligned and ends with a whole dword (wide_rows).
 template <typename T, bool WIDE>
 __device__ __forceinline__ void load_columns(const T* row, int64_t c, int64_t n, float (&r)[8]) {
-  if (WIDE && c + 8 <= n) {
-    load8(row + c, r);
-    return;
-  }
+  if constexpr (WIDE) {
+    // the descriptor ends with the row: n * 4 <= 2^26 bytes
+    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(n * (int64_t)sizeof(T)));
+    const int at = (int)(c * (int64_t)sizeof(T));
+    const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
+    if constexpr (sizeof(T) == 4) {
+      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16, 0, 0);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) r[k] = c + k < n ? load1(row + c + k) : 0.f;
+      for (int k = 0; k < 4; ++k) {
+        r[k] = __uint_as_float(u[k]);
+        r[k + 4] = __uint_as_float(v[k]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        r[2 * k] = __uint_as_float(u[k] << 16);
+        r[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
+      }
+    }
+  } else {
+    float v[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = load1(row + min(c + k, n - 1));
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r[k] = c + k < n ? v[k] : 0.f;
+  }
 }
 
-// The lane's factors sign / d of columns c .. c + 7.
+inline bool wide_rows(const MxRows& r) {
+  return aligned16(r.x) && (r.type == KQ_F32 ? r.ld % 4 == 0 : r.ld % 8 == 0 && r.n % 2 == 0);
+}
+
+// The lane's factors sign / d of columns c .. c + 7, 1 past the last one.
 __device__ __forceinline__ void factors(const float* d, const int8_t* sign, int64_t c, int64_t n, float (&f)[8]) {
+  float dv[8];
+  int sv[8];
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    f[k] = sign && c + k < n && sign[c + k] < 0 ? -1.f : 1.f;
-    if (d && c + k < n) f[k] = __fdiv_rn(f[k], d[c + k]);
+    const int64_t at = min(c + k, n - 1);
+    dv[k] = d ? d[at] : 1.f;
+    sv[k] = sign ? sign[at] : 1;
   }
+#pragma unroll
+  for (int k = 0; k < 8; ++k) f[k] = c + k < n ? __fdiv_rn(sv[k] < 0 ? -1.f : 1.f, dv[k]) : 1.f;
 }
 
 // Butterfly with the lane whose value comes in `with`: the lower lane's sum, the upper one's
