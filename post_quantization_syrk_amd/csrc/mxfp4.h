@@ -12,6 +12,8 @@
 
 namespace kq {
 
+typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
+
 constexpr int MX_BLOCK = 32;     // values per scale
 constexpr int MX_GROUP = 128;    // columns per scale dword; rows are padded to whole groups
 constexpr int64_t MX_MAX_ROWS = (int64_t)1 << 30, MX_MAX_N = (int64_t)1 << 24;

@@ -21,47 +21,45 @@ struct RowArgs {
   const int8_t* sign;
   int had;
   float isb;
-  bool wide;
 };
 
 // Rotates and quantises the tile's rows into LDS: codes [rows][pitch], then scale dwords
-// [rows][steps].
-template <typename T, int WAVES, bool LONG, bool WIDE>
+// [rows][steps].  A rotation block takes S waves (LOGH <= 10: one), and the workgroup's waves take
+// blocks of the rows one after another.
+template <typename T, int WAVES, int LOGH, bool WIDE>
 __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArgs& x, const Tile& t, float* lds,
                                               uint8_t* codes, int* scales) {
-  const int rows = t.last - t.m0, lane = threadIdx.x & 63;
-  auto source = [&](int r) -> const T* {
-    const int row = a.index ? a.index[t.m0 + r] : t.m0 + r;
-    return row >= 0 && row < a.rows ? (const T*)x.x + row * x.ld : nullptr;
-  };
-  for (int64_t c0 = 0; c0 < 2 * a.pitch; c0 += SPAN * WAVES) {
-    const int64_t c = c0 + 8 * threadIdx.x;
-    float f[8], r[8], next[8];
-    auto load = [&](int k, float (&v)[8]) {
-      const T* p = source(k);
-      if (p) {
-        load_columns<T, WIDE>(p, c, x.n, v);
-      } else {
+  constexpr int S = LOGH > 10 ? 1 << (LOGH - 10) : 1, GROUPS = WAVES / S;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int parts = (int)((2 * a.pitch + SPAN * S - 1) / (SPAN * S)), units = parts * (t.last - t.m0);
+  const bool scaled = x.d || x.sign, whole = whole_factors(x.d, x.sign, x.n);
+  for (int u0 = 0; u0 < units; u0 += GROUPS) {   // every wave passes the barriers of a long block
+    const int u = min(u0 + wave / S, units - 1), k = u / parts;
+    const int64_t c = (int64_t)(u % parts) * (SPAN * S) + 16 * ((wave % S) * 64 + lane);
+    const int row = a.index ? a.index[t.m0 + k] : t.m0 + k;
+    const bool in = row >= 0 && row < a.rows;
+    Raw<T> raw;
+    load_columns<WIDE>((const T*)x.x + (in ? row : 0) * x.ld, c, in ? x.n : 1, raw);
+    float r[16], f[16];
+    if (scaled) {
+      if (whole)
+        factors<true>(x.d, x.sign, c, x.n, f);
+      else
+        factors<false>(x.d, x.sign, c, x.n, f);
+    }
+    convert(raw, r);
+    if (!in) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.f;
-      }
-    };
-    load(0, r);
-    const bool scaled = x.d || x.sign;
-    if (scaled) factors(x.d, x.sign, c, x.n, f);
-    for (int k = 0; k < rows; ++k) {
-      if (k + 1 < rows) load(k + 1, next);
-      rotate<WAVES, LONG>(r, scaled, f, x.had, x.isb, lds);
-      float s;
-      bool bad;
-      int four;
-      const unsigned w = encode(r, s, bad, four);
-      if (c < 2 * a.pitch) {
-        *(unsigned*)(codes + k * a.pitch + c / 2) = w;
-        if ((lane & 15) == 0) scales[k * a.steps + (c >> 7)] = four;
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) r[j] = next[j];
+      for (int j = 0; j < 16; ++j) r[j] = 0.f;
+    }
+    rotate<WAVES, LOGH>(r, scaled, f, x.had, x.isb, lds);
+    float s;
+    bool bad;
+    int four;
+    const u32x2 w = encode(r, s, bad, four);
+    if (c < 2 * a.pitch && u0 + wave / S < units) {
+      *(u32x2*)(codes + k * a.pitch + c / 2) = w;
+      if ((lane & 7) == 0) scales[k * a.steps + (c >> 7)] = four;
     }
   }
 }
@@ -74,7 +72,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
 // instruction, so its two loads are neighbours, a row's line is read whole, and both blocks'
 // scales lie in one dword.
 // T: void for quantised activations, else their type, quantised here (MT = 1).
-template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T>
+template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE>
 __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowArgs x) {
   constexpr bool FUSED = !__is_void(T);
   constexpr int BM = 16 * MT, BN = 16 * NT, LD = BN + 4;
@@ -164,12 +162,12 @@ __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowAr
   };
   if (p0 < p1) load_w(p0);
   if constexpr (FUSED) {
-    if (!x.wide)
-      quantize_rows<T, WAVES, true, false>(a, x, t, lds, codes, scales);
-    else if (x.had <= SPAN)
-      quantize_rows<T, WAVES, false, true>(a, x, t, lds, codes, scales);
-    else
-      quantize_rows<T, WAVES, true, true>(a, x, t, lds, codes, scales);
+    switch (x.had > SPAN ? x.had / SPAN : 1) {
+      case 2: quantize_rows<T, WAVES, 11, WIDE>(a, x, t, lds, codes, scales); break;
+      case 4: quantize_rows<T, WAVES, 12, WIDE>(a, x, t, lds, codes, scales); break;
+      case 8: quantize_rows<T, WAVES, 13, WIDE>(a, x, t, lds, codes, scales); break;
+      default: quantize_rows<T, WAVES, -1, WIDE>(a, x, t, lds, codes, scales); break;
+    }
     __syncthreads();
   }
   f32x4 acc[MT][NT];
@@ -219,7 +217,7 @@ __global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowAr
   }
 }
 
-template <int WAVES, int MT, int NT, int U, typename T>
+template <int WAVES, int MT, int NT, int U, typename T, bool WIDE = true>
 kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
   const int64_t tm = ceil_div(p.slots, BM) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
@@ -228,7 +226,7 @@ kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
     bytes = std::max(bytes, sizeof(float) * (size_t)rotate_floats(WAVES) +
                                 (size_t)std::min<int64_t>(p.slots, BM) * (size_t)(p.pitch + 4 * p.steps));
   const dim3 grid((unsigned)ceil_div(p.N, BN), (unsigned)tm), block(64 * WAVES);
-  const auto kernel = p.offsets ? mx_few_kernel<WAVES, MT, NT, U, true, T> : mx_few_kernel<WAVES, MT, NT, U, false, T>;
+  const auto kernel = p.offsets ? mx_few_kernel<WAVES, MT, NT, U, true, T, WIDE> : mx_few_kernel<WAVES, MT, NT, U, false, T, WIDE>;
   if (bytes > 64 * 1024)
     KQ_HIP(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
   kernel<<<grid, block, bytes, s>>>(p, x);
@@ -249,12 +247,12 @@ bool mx_few(const ProductArgs& p) {
   return avg <= testing_value(KQ_TESTING_MX_FEW, 64) && p.slots <= 65535 && p.rows * p.pitch < 0x7fffffff;
 }
 
-bool mx_few_fused(const ProductArgs& p, const MxRows& x, int64_t block) {
-  return p.slots <= 16 && p.slots * x.n <= testing_value(KQ_TESTING_MX_FUSED, 8192) && block <= 8192;
+bool mx_few_fused(const ProductArgs& p, const MxRows& x) {
+  return x.rows > 0 && p.slots <= 16 && p.slots * x.n <= testing_value(KQ_TESTING_MX_FUSED, 8192);
 }
 
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s) {
-  RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block)), wide_rows(x)};
+  RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block))};
   const int bm = fused ? 16 : few_rows(p);
   // Columns per workgroup: 64, so that its rows of x and its fixed costs serve more of the layer, or
   // as few as leave a workgroup for five of eight compute units (16 rows, 4096 x 4096: 3.7 us
@@ -263,10 +261,10 @@ kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, b
   const int64_t enough = device_cu_count() * 5 / 8;
   const int nt = ceil_div(p.N, 64) * tm >= enough ? 4 : ceil_div(p.N, 32) * tm >= enough ? 2 : 1;
   if (fused) {
-    const bool f32 = x.type == KQ_F32;
-#define KQ_FEW(NT, U)                                                                                   \
-  (block > 8 * SPAN ? (f32 ? launch<16, 1, NT, 1, float>(p, r, s) : launch<16, 1, NT, 1, uint16_t>(p, r, s)) \
-                    : (f32 ? launch<8, 1, NT, U, float>(p, r, s) : launch<8, 1, NT, U, uint16_t>(p, r, s)))
+    const bool f32 = x.type == KQ_F32, wide = wide_rows(x);
+#define KQ_FEW(NT, U)                                                                               \
+  (wide ? (f32 ? launch<8, 1, NT, U, float, true>(p, r, s) : launch<8, 1, NT, U, uint16_t, true>(p, r, s))     \
+        : (f32 ? launch<8, 1, NT, U, float, false>(p, r, s) : launch<8, 1, NT, U, uint16_t, false>(p, r, s)))
     return nt == 4 ? KQ_FEW(4, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
 #undef KQ_FEW
   }

@@ -495,7 +495,7 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
   }
   if (p.slots == 0) return KQ_OK;
   const bool few = mx_few(p);
-  if (few && x.type != KQ_MXFP4 && mx_few_fused(p, x, block)) return mx_few_product(p, x, block, true, s);
+  if (few && x.type != KQ_MXFP4 && mx_few_fused(p, x)) return mx_few_product(p, x, block, true, s);
   if (x.type != KQ_MXFP4) KQ_TRY(mx_quantize(x, block, (uint8_t*)p.xc, (uint8_t*)p.xs, nullptr, 0, s));
   if (few) return mx_few_product(p, x, block, false, s);
   switch (p.offsets && x_far(p) ? 44 : testing_value(KQ_TESTING_MX_TILE, 448)) {

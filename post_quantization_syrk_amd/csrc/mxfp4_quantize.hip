@@ -25,81 +25,115 @@ struct QuantArgs {
   int chunks;              // workgroups that share a row
   int run;                 // consecutive rows per workgroup
   bool v_wide;             // rows of values are 16-byte aligned
+  bool whole;              // whole_factors
 };
 
-// A workgroup holds SPAN WAVES columns, eight neighbouring ones per lane, and takes `run` rows
-// one after another; four lanes make a block of 32.  Rotation blocks of up to 512 columns stay
-// inside a wave (DPP and lane swaps), longer ones pass through LDS once (LONG).
-template <typename T, int WAVES, bool LONG, bool WIDE>
-__global__ __launch_bounds__(64 * WAVES) void mx_quantize_kernel(QuantArgs a) {
+// A wave holds SPAN columns, sixteen neighbouring ones per lane, and takes `run` rows one after
+// another, the next one's load in flight.  Rotation blocks of up to SPAN columns stay inside a wave
+// (its four waves work on their own); longer ones are a workgroup's, and pass through LDS.
+// LOGH: the rotation block, 2^LOGH columns (-1: any up to SPAN, decided at run time).
+template <typename T, int LOGH, bool WIDE>
+__global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quantize_kernel(QuantArgs a) {
+  constexpr bool LONG = LOGH > 10;
+  constexpr int WAVES = LONG ? 1 << (LOGH > 10 ? LOGH - 10 : 0) : 4, COLS = LONG ? SPAN * WAVES : SPAN;
   __shared__ __attribute__((aligned(16))) float lds[LONG ? rotate_floats(WAVES) : 4];
   const int lane = threadIdx.x & 63;
-  const int64_t kp = mx_pad(a.n), c = (int64_t)(blockIdx.x % a.chunks) * (SPAN * WAVES) + 8 * threadIdx.x;
-  const int64_t r0 = (int64_t)(blockIdx.x / a.chunks) * a.run, r1 = min(r0 + a.run, a.rows);
-  const bool live = c < kp;
-  if (!LONG && !live) return;
-  const bool scaled = a.d || a.sign;
-  float f[8];
-  if (scaled) factors(a.d, a.sign, c, a.n, f);
-  const T* x = (const T*)a.src;
-  float r[8];
-  load_columns<T, WIDE>(x + r0 * a.ld, c, a.n, r);
+  // the wave's, or workgroup's, columns and rows
+  const unsigned unit = LONG ? blockIdx.x : blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t kp = mx_pad(a.n), c = (int64_t)(unit % a.chunks) * COLS + 16 * (LONG ? (int)threadIdx.x : lane);
+  const int64_t r0 = (int64_t)(unit / a.chunks) * a.run, r1 = min(r0 + a.run, a.rows);
+  if (r0 >= r1) return;
+  const bool live = c < kp, scaled = a.d || a.sign;
+  float f[16];
+  if (scaled) {
+    if (a.whole)
+      factors<true>(a.d, a.sign, c, a.n, f);
+    else
+      factors<false>(a.d, a.sign, c, a.n, f);
+  }
+  const T* x = (const T*)a.src + r0 * a.ld;
+  Raw<T> next;
+  load_columns<WIDE>(x, c, a.n, next);
+  uint8_t* codes = a.codes + r0 * (kp / 2) + c / 2;
+  uint8_t* scales = a.scales + ((c >> 7) * a.rows + r0) * 4;
+  uint16_t* values = a.values + r0 * a.ldv + c;
   for (int64_t row = r0; row < r1; ++row) {
-    float next[8];
-    if (row + 1 < r1) load_columns<T, WIDE>(x + (row + 1) * a.ld, c, a.n, next);
-    rotate<WAVES, LONG>(r, scaled, f, a.had, a.isb, lds);
+    float r[16];
+    convert(next, r);
+    x += row + 1 < r1 ? a.ld : 0;   // (the last row once more rather than a branch)
+    load_columns<WIDE>(x, c, a.n, next);
+    rotate<WAVES, LOGH>(r, scaled, f, a.had, a.isb, lds);
     float s;
     bool bad;
     int four;
-    const unsigned w = encode(r, s, bad, four);
+    const u32x2 w = encode(r, s, bad, four);
     if (live) {
-      *(unsigned*)(a.codes + row * (kp / 2) + c / 2) = w;
-      if ((lane & 15) == 0) *(int*)(a.scales + ((c >> 7) * a.rows + row) * 4) = four;
+      *(u32x2*)codes = w;
+      if ((lane & 7) == 0) *(int*)scales = four;
       if (a.values) {
-        u32x4 o;
-        o[0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
-        o[1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
-        o[2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
-        o[3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
-        if (bad) o = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
-        uint16_t* out = a.values + row * a.ldv + c;
-        if (a.v_wide && c + 8 <= a.n) {
-          *(u32x4*)out = o;
+        u32x4 o[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+          o[k][0] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], s, 0));
+          o[k][1] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], s, 1));
+          o[k][2] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], s, 2));
+          o[k][3] = __builtin_bit_cast(unsigned, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w[k], s, 3));
+          if (bad) o[k] = u32x4{0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u, 0x7fc07fc0u};
+        }
+        if (a.v_wide && c + 16 <= a.n) {
+          ((u32x4*)values)[0] = o[0];
+          ((u32x4*)values)[1] = o[1];
         } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (c + k < a.n) out[k] = (uint16_t)(o[k >> 1] >> (16 * (k & 1)));
+          for (int k = 0; k < 16; ++k)
+            if (c + k < a.n) values[k] = (uint16_t)(o[k >> 3][(k >> 1) & 3] >> (16 * (k & 1)));
         }
       }
     }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = next[k];
+    codes += kp / 2;
+    scales += 4;
+    values += a.ldv;
   }
 }
 
-template <typename T, bool WIDE>
+template <typename T, int LOGH, bool WIDE>
 kq_status launch(QuantArgs a, hipStream_t s) {
-  // a workgroup's waves: those of one rotation block, at least four
-  const int waves = a.had > 8 * SPAN ? 16 : a.had > 4 * SPAN ? 8 : 4;
-  a.chunks = (int)ceil_div(mx_pad(a.n), SPAN * waves);
-  // rows per workgroup: enough to share the factors sign / d and to write the scales' lines whole,
-  // as long as every place on the card (eight waves per SIMD) has a workgroup
-  const int64_t places = (int64_t)device_cu_count() * 32 / waves;
-  a.run = (int)std::max<int64_t>(1, std::min<int64_t>(16, a.rows * a.chunks / (2 * places)));
-  const int64_t grid = ceil_div(a.rows, a.run) * a.chunks;
-  if (grid > 0x7fffffff)
+  constexpr bool LONG = LOGH > 10;
+  constexpr int WAVES = LONG ? 1 << (LOGH > 10 ? LOGH - 10 : 0) : 4, COLS = LONG ? SPAN * WAVES : SPAN;
+  a.chunks = (int)ceil_div(mx_pad(a.n), COLS);
+  // rows per unit (a wave, or a workgroup of a long block): enough to share the factors sign / d,
+  // as long as there are four waves per SIMD
+  const int64_t places = (int64_t)device_cu_count() * 16 / (LONG ? WAVES : 1);
+  a.run = (int)std::max<int64_t>(1, std::min<int64_t>(16, a.rows * a.chunks / places));
+  const int64_t units = ceil_div(a.rows, a.run) * a.chunks, grid = LONG ? units : ceil_div(units, 4);
+  if (units > 0x7fffffff)
     return fail(KQ_ESHAPE, "MXFP4 quantisation: %lld rows of %lld values", (long long)a.rows, (long long)a.n);
-  const dim3 g((unsigned)grid), t(64 * waves);
-  if (a.had <= SPAN)
-    mx_quantize_kernel<T, 4, false, WIDE><<<g, t, 0, s>>>(a);
-  else if (waves == 4)
-    mx_quantize_kernel<T, 4, true, WIDE><<<g, t, 0, s>>>(a);
-  else if (waves == 8)
-    mx_quantize_kernel<T, 8, true, WIDE><<<g, t, 0, s>>>(a);
-  else
-    mx_quantize_kernel<T, 16, true, WIDE><<<g, t, 0, s>>>(a);
+  mx_quantize_kernel<T, LOGH, WIDE><<<dim3((unsigned)grid), dim3(64 * WAVES), 0, s>>>(a);
   KQ_LAUNCHED("mx_quantize_kernel");
   return KQ_OK;
+}
+
+// The block is a constant of the kernel where rows are read 16 bytes at a time (as a variable, its
+// stages copy the sixteen values at every branch); other rows take one kernel up to SPAN.
+template <typename T>
+kq_status launch_block(const QuantArgs& a, bool wide, hipStream_t s) {
+  switch (a.had > SPAN || wide ? __builtin_ctz(a.had) : -1) {
+    case 0: return launch<T, 0, true>(a, s);
+    case 1: return launch<T, 1, true>(a, s);
+    case 2: return launch<T, 2, true>(a, s);
+    case 3: return launch<T, 3, true>(a, s);
+    case 4: return launch<T, 4, true>(a, s);
+    case 5: return launch<T, 5, true>(a, s);
+    case 6: return launch<T, 6, true>(a, s);
+    case 7: return launch<T, 7, true>(a, s);
+    case 8: return launch<T, 8, true>(a, s);
+    case 9: return launch<T, 9, true>(a, s);
+    case 10: return launch<T, 10, true>(a, s);
+    case 11: return wide ? launch<T, 11, true>(a, s) : launch<T, 11, false>(a, s);
+    case 12: return wide ? launch<T, 12, true>(a, s) : launch<T, 12, false>(a, s);
+    case 13: return wide ? launch<T, 13, true>(a, s) : launch<T, 13, false>(a, s);
+    default: return launch<T, -1, false>(a, s);
+  }
 }
 
 }  // namespace
@@ -130,10 +164,9 @@ kq_status mx_quantize(const MxRows& r, int64_t block, uint8_t* codes, uint8_t* s
   a.had = (int)block; a.isb = (float)(1.0 / sqrt((double)block));
   a.codes = codes; a.scales = scales; a.values = values; a.ldv = ldv;
   a.v_wide = aligned16(values) && ldv % 8 == 0;
-  // rows that start 16 bytes aligned are read 16 bytes at a time
+  a.whole = whole_factors(r.d, r.sign, r.n);
   const bool wide = wide_rows(r);
-  if (r.type == KQ_F32) return wide ? launch<float, true>(a, s) : launch<float, false>(a, s);
-  return wide ? launch<uint16_t, true>(a, s) : launch<uint16_t, false>(a, s);
+  return r.type == KQ_F32 ? launch_block<float>(a, wide, s) : launch_block<uint16_t>(a, wide, s);
 }
 
 }  // namespace kq

@@ -1,5 +1,5 @@
-// Device side of the MXFP4 quantisation: the rotation of a row held eight neighbouring columns
-// per lane, and the encoding of those eight (x~ = P D^-1 x, then blocks of 32).
+// Device side of the MXFP4 quantisation: the rotation of a row held sixteen neighbouring columns
+// per lane, and the encoding of those sixteen (x~ = P D^-1 x, then blocks of 32).
 #pragma once
 
 #include "mxfp4.h"
@@ -11,41 +11,60 @@
 namespace kq {
 namespace {
 
-constexpr int SPAN = 512;        // columns that a wave holds: 8 neighbouring ones per lane
+constexpr int SPAN = 1024;       // columns that a wave holds: 16 neighbouring ones per lane
 
-__device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const uint16_t* p) { return __uint_as_float((unsigned)*p << 16); }
+// Sixteen columns as they lie in memory (kept so until their turn: a conversion would wait for
+// the load).
+template <typename T>
+struct Raw {
+  u32x4 v[sizeof(T)];   // 16 columns: two words of bf16, four of fp32
+};
 
-// The lane's columns c .. c + 7 of a row of n values, zero past its end, without a branch around
+// The lane's columns c .. c + 15 of a row of n values, zero past its end, without a branch around
 // the loads (where paths join the compiler waits for all of them).  WIDE: 16 bytes at a time, of a
 // row that starts 16-byte aligned and ends with a whole dword (wide_rows).
-template <typename T, bool WIDE>
-__device__ __forceinline__ void load_columns(const T* row, int64_t c, int64_t n, float (&r)[8]) {
+template <bool WIDE>
+__device__ __forceinline__ void load_columns(const float* row, int64_t c, int64_t n, Raw<float>& r) {
   if constexpr (WIDE) {
     // the descriptor ends with the row: n * 4 <= 2^26 bytes
-    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(n * (int64_t)sizeof(T)));
-    const int at = (int)(c * (int64_t)sizeof(T));
-    const u32x4 u = __builtin_amdgcn_raw_buffer_load_b128(rs, at, 0, 0);
-    if constexpr (sizeof(T) == 4) {
-      const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, at + 16, 0, 0);
+    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(4 * n));
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        r[k] = __uint_as_float(u[k]);
-        r[k + 4] = __uint_as_float(v[k]);
-      }
-    } else {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        r[2 * k] = __uint_as_float(u[k] << 16);
-        r[2 * k + 1] = __uint_as_float(u[k] & 0xffff0000u);
-      }
-    }
+    for (int k = 0; k < 4; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(4 * c) + 16 * k, 0, 0);
   } else {
-    float v[8];
+    unsigned v[16];
 #pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = load1(row + min(c + k, n - 1));
+    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(row[min(c + k, n - 1)]);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = c + k < n ? v[k] : 0.f;
+    for (int k = 0; k < 16; ++k) r.v[k >> 2][k & 3] = c + k < n ? v[k] : 0;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void load_columns(const uint16_t* row, int64_t c, int64_t n, Raw<uint16_t>& r) {
+  if constexpr (WIDE) {
+    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(2 * n));
+#pragma unroll
+    for (int k = 0; k < 2; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(2 * c) + 16 * k, 0, 0);
+  } else {
+    unsigned v[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = row[min(c + k, n - 1)];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v[k] = c + k < n ? v[k] : 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) r.v[k >> 2][k & 3] = v[2 * k] | v[2 * k + 1] << 16;
+  }
+}
+
+__device__ __forceinline__ void convert(const Raw<float>& w, float (&r)[16]) {
+#pragma unroll
+  for (int k = 0; k < 16; ++k) r[k] = __uint_as_float(w.v[k >> 2][k & 3]);
+}
+__device__ __forceinline__ void convert(const Raw<uint16_t>& w, float (&r)[16]) {
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const unsigned u = w.v[k >> 2][k & 3];
+    r[2 * k] = __uint_as_float(u << 16);
+    r[2 * k + 1] = __uint_as_float(u & 0xffff0000u);
   }
 }
 
@@ -53,56 +72,101 @@ inline bool wide_rows(const MxRows& r) {
   return aligned16(r.x) && (r.type == KQ_F32 ? r.ld % 4 == 0 : r.ld % 8 == 0 && r.n % 2 == 0);
 }
 
-// The lane's factors sign / d of columns c .. c + 7, 1 past the last one.
-__device__ __forceinline__ void factors(const float* d, const int8_t* sign, int64_t c, int64_t n, float (&f)[8]) {
-  float dv[8];
-  int sv[8];
+// The lane's factors sign / d of columns c .. c + 15, 1 past the last one.  WHOLE: d and the signs
+// are 16-byte aligned and n is a multiple of 16 (whole_factors), so that a lane takes 16 bytes at a
+// time (one column at a time, the lanes' loads are 64 bytes apart and cost more than a row's
+// rotation).
+template <bool WHOLE>
+__device__ __forceinline__ void factors(const float* d, const int8_t* sign, int64_t c, int64_t n, float (&f)[16]) {
+  float dv[16];
+  bool minus[16];
+  if constexpr (WHOLE) {
+    const int64_t at = min(c, n - 16);
+    u32x4 s = {0, 0, 0, 0};
+    if (sign) s = *(const u32x4*)(sign + at);
 #pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const int64_t at = min(c + k, n - 1);
-    dv[k] = d ? d[at] : 1.f;
-    sv[k] = sign ? sign[at] : 1;
+    for (int k = 0; k < 4; ++k) {
+      const float4 v = d ? *(const float4*)(d + at + 4 * k) : make_float4(1.f, 1.f, 1.f, 1.f);
+      dv[4 * k] = v.x; dv[4 * k + 1] = v.y; dv[4 * k + 2] = v.z; dv[4 * k + 3] = v.w;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) minus[k] = (s[k >> 2] >> (8 * (k & 3) + 7)) & 1;
+  } else {
+    int sv[16];
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int64_t at = min(c + k, n - 1);
+      dv[k] = d ? d[at] : 1.f;
+      sv[k] = sign ? sign[at] : 1;
+    }
+#pragma unroll
+    for (int k = 0; k < 16; ++k) minus[k] = sv[k] < 0;
   }
 #pragma unroll
-  for (int k = 0; k < 8; ++k) f[k] = c + k < n ? __fdiv_rn(sv[k] < 0 ? -1.f : 1.f, dv[k]) : 1.f;
+  for (int k = 0; k < 16; ++k) f[k] = c + k < n ? __fdiv_rn(minus[k] ? -1.f : 1.f, dv[k]) : 1.f;
 }
 
-// Butterfly with the lane whose value comes in `with`: the lower lane's sum, the upper one's
-// difference (lower minus upper); `up`: the sign bit on upper lanes.
+__host__ __device__ inline bool whole_factors(const float* d, const int8_t* sign, int64_t n) {
+  return (((uintptr_t)d | (uintptr_t)sign) & 15) == 0 && n % 16 == 0;
+}
+
+// Butterfly between lanes a power of two apart, `v` with its partner's value: the lower lane gets
+// the sum, the upper one the partner's value minus its own (DPP: a lane move inside an add).
 template <int CTRL>
-__device__ __forceinline__ float across(float v, float with, unsigned up) {
-  const int w = __builtin_amdgcn_mov_dpp((int)__float_as_uint(with), CTRL, 0xf, 0xf, true);
-  return __uint_as_float(w) + __uint_as_float(__float_as_uint(v) ^ up);
+__device__ __forceinline__ float moved(float v) {
+  return __uint_as_float(__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
+}
+template <int CTRL>
+__device__ __forceinline__ float across(float v, unsigned up) {   // up: the sign bit on upper lanes
+  return moved<CTRL>(v) + __uint_as_float(__float_as_uint(v) ^ up);
 }
 
-// Butterflies of strides 8 .. 256 below `had`: lanes 1 .. 32 apart.
-__device__ __forceinline__ void lane_stages(float (&r)[8], int had, int lane) {
+// Butterflies of strides 1 .. 512 below the rotation block, 2^LOGH columns (LOGH < 0: `had`).
+template <int LOGH>
+__device__ __forceinline__ void span_stages(float (&r)[16], int had) {
   constexpr int XOR1 = 0xb1, XOR2 = 0x4e, XOR3 = 0x1b, HALF_MIRROR = 0x141, ROR8 = 0x128;
+  const int lane = threadIdx.x & 63;
+  auto on = [&](int h) { return LOGH < 0 ? had > h : 1 << (LOGH < 0 ? 0 : LOGH) > h; };
   auto up = [&](int bit) { return (unsigned)(lane & bit) << (31 - __builtin_ctz(bit)); };
-  if (had > 8) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = across<XOR1>(r[k], r[k], up(1));
+  for (int h = 1; h < 16; h <<= 1)
+    if (on(h)) {
+#pragma unroll
+      for (int k = 0; k < 16; ++k)
+        if ((k & h) == 0) {
+          const float u = r[k], v = r[k | h];
+          r[k] = u + v;
+          r[k | h] = u - v;
+        }
+    }
+  if (on(16)) {
+    const unsigned u = up(1);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = across<XOR1>(r[k], u);
   }
-  if (had > 16) {
+  if (on(32)) {
+    const unsigned u = up(2);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = across<XOR2>(r[k], r[k], up(2));
+    for (int k = 0; k < 16; ++k) r[k] = across<XOR2>(r[k], u);
   }
-  if (had > 32) {   // lane xor 4 = (xor 7) xor 3
+  if (on(64)) {   // lane xor 4 = (xor 7) xor 3
+    const unsigned u = up(4);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const int m = __builtin_amdgcn_mov_dpp((int)__float_as_uint(r[k]), HALF_MIRROR, 0xf, 0xf, true);
-      r[k] = across<XOR3>(r[k], __uint_as_float(m), up(4));
+    for (int k = 0; k < 16; ++k) {
+      const float m = moved<HALF_MIRROR>(r[k]);
+      r[k] = moved<XOR3>(m) + __uint_as_float(__float_as_uint(r[k]) ^ u);
     }
   }
-  if (had > 64) {
+  if (on(128)) {
+    const unsigned u = up(8);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = across<ROR8>(r[k], r[k], up(8));
+    for (int k = 0; k < 16; ++k) r[k] = across<ROR8>(r[k], u);
   }
   // Two values at a time: the exchange gives a lane both ends of one value's butterfly, a second
   // one hands the results back.
-  if (had > 128) {
+  if (on(256)) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
+    for (int k = 0; k < 16; k += 2) {
       const auto e = __builtin_amdgcn_permlane16_swap(__float_as_uint(r[k]), __float_as_uint(r[k + 1]), false, false);
       const float a = __uint_as_float(e[0]), b = __uint_as_float(e[1]);
       const auto f = __builtin_amdgcn_permlane16_swap(__float_as_uint(a + b), __float_as_uint(a - b), false, false);
@@ -110,9 +174,9 @@ __device__ __forceinline__ void lane_stages(float (&r)[8], int had, int lane) {
       r[k + 1] = __uint_as_float(f[1]);
     }
   }
-  if (had > 256) {
+  if (on(512)) {
 #pragma unroll
-    for (int k = 0; k < 8; k += 2) {
+    for (int k = 0; k < 16; k += 2) {
       const auto e = __builtin_amdgcn_permlane32_swap(__float_as_uint(r[k]), __float_as_uint(r[k + 1]), false, false);
       const float a = __uint_as_float(e[0]), b = __uint_as_float(e[1]);
       const auto f = __builtin_amdgcn_permlane32_swap(__float_as_uint(a + b), __float_as_uint(a - b), false, false);
@@ -122,112 +186,92 @@ __device__ __forceinline__ void lane_stages(float (&r)[8], int had, int lane) {
   }
 }
 
-// Butterflies of strides 512 .. SPAN WAVES / 2 below `had`, between the workgroup's waves
-// through LDS: the lanes' columns are written side by side (the two halves of each lane's eight
-// in planes of their own, half the banks apart, so that neither access conflicts), read 512
-// apart, eight per thread, and written back.  A block of 16 spans takes its last stage while
-// the columns are read back.
-template <int WAVES>
-__device__ __forceinline__ void wave_stages(float (&r)[8], int had, float* v) {
-  constexpr int PLANE = 4 * 64 * WAVES + 32;
-  const int t = threadIdx.x;
-  auto at = [](int i) { return ((i >> 2) & 1) * PLANE + (i >> 3) * 4 + (i & 3); };
+// LDS floats that wave_stages needs for a workgroup of `waves`.
+constexpr int plane_floats(int waves) { return 4 * 64 * waves + 16; }
+constexpr int rotate_floats(int waves) { return 4 * plane_floats(waves); }
+
+// Butterflies of strides 1024 .. 512 S of a block of S waves (the workgroup holds WAVES / S
+// blocks), through LDS: the lanes' columns are written side by side, read 1024 apart, and written
+// back.  The four quarters of each lane's sixteen lie in planes of their own, a quarter of the
+// banks apart, so that neither access conflicts.
+template <int WAVES, int S>
+__device__ __forceinline__ void wave_stages(float (&r)[16], float* v) {
+  constexpr int PLANE = plane_floats(WAVES), P = 16 / S;
+  const int t = threadIdx.x, base = t / (64 * S) * (SPAN * S), col = t % (64 * S);
+  auto at = [](int i) { return ((i >> 2) & 3) * PLANE + (i >> 4) * 4 + (i & 3); };
   __syncthreads();   // the row before has been read back
-  *(float4*)(v + 4 * t) = make_float4(r[0], r[1], r[2], r[3]);
-  *(float4*)(v + PLANE + 4 * t) = make_float4(r[4], r[5], r[6], r[7]);
+#pragma unroll
+  for (int k = 0; k < 4; ++k) *(float4*)(v + k * PLANE + 4 * t) = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
   __syncthreads();
-  // the eight spans 8 (t / 512) + j, column t mod 512; with fewer spans per workgroup (4 waves),
-  // two columns of four spans
-  constexpr int S = WAVES < 8 ? WAVES : 8, P = 8 / S;
   float u[P][S];
-  const int base = (t / (64 * S)) * (SPAN * S), col = t % (64 * S);
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < S; ++j) u[p][j] = v[at(base + SPAN * j + col + 64 * S * p)];
 #pragma unroll
   for (int h = 1; h < S; h <<= 1)
-    if (had > SPAN * h) {
 #pragma unroll
-      for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-        for (int j = 0; j < S; ++j)
-          if ((j & h) == 0) {
-            const float a = u[p][j], b = u[p][j | h];
-            u[p][j] = a + b;
-            u[p][j | h] = a - b;
-          }
-    }
+      for (int j = 0; j < S; ++j)
+        if ((j & h) == 0) {
+          const float a = u[p][j], b = u[p][j | h];
+          u[p][j] = a + b;
+          u[p][j | h] = a - b;
+        }
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int j = 0; j < S; ++j) v[at(base + SPAN * j + col + 64 * S * p)] = u[p][j];
   __syncthreads();
-  const float4 lo = *(const float4*)(v + 4 * t), hi = *(const float4*)(v + PLANE + 4 * t);
-  r[0] = lo.x; r[1] = lo.y; r[2] = lo.z; r[3] = lo.w;
-  r[4] = hi.x; r[5] = hi.y; r[6] = hi.z; r[7] = hi.w;
-  if constexpr (WAVES == 16) {   // had is 16 spans: with fewer, a workgroup has 8 waves
-    const int o = 4 * (t ^ 512);
-    const float4 a = *(const float4*)(v + o), b = *(const float4*)(v + PLANE + o);
-    const unsigned up = (unsigned)(t & 512) << 22;
-    const float w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] = w[k] + __uint_as_float(__float_as_uint(r[k]) ^ up);
+  for (int k = 0; k < 4; ++k) {
+    const float4 w = *(const float4*)(v + k * PLANE + 4 * t);
+    r[4 * k] = w.x; r[4 * k + 1] = w.y; r[4 * k + 2] = w.z; r[4 * k + 3] = w.w;
   }
 }
-
-// LDS floats that wave_stages needs.
-constexpr int rotate_floats(int waves) { return 2 * (4 * 64 * waves + 32); }
 
 // The whole rotation of the lane's columns: factors, butterflies, 1 / sqrt(had).
-template <int WAVES, bool LONG>
-__device__ __forceinline__ void rotate(float (&r)[8], bool scaled, const float (&f)[8], int had, float isb, float* lds) {
+template <int WAVES, int LOGH>
+__device__ __forceinline__ void rotate(float (&r)[16], bool scaled, const float (&f)[16], int had, float isb, float* lds) {
   if (scaled) {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] *= f[k];
+    for (int k = 0; k < 16; ++k) r[k] *= f[k];
   }
+  span_stages<LOGH>(r, had);
+  if constexpr (LOGH > 10) wave_stages<WAVES, 1 << (LOGH - 10)>(r, lds);
+  if (LOGH > 0 || (LOGH < 0 && had > 1)) {
 #pragma unroll
-  for (int h = 1; h < 8; h <<= 1)
-    if (had > h) {
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-        if ((k & h) == 0) {
-          const float u = r[k], v = r[k | h];
-          r[k] = u + v;
-          r[k | h] = u - v;
-        }
-    }
-  lane_stages(r, had, threadIdx.x & 63);
-  if (LONG) wave_stages<WAVES>(r, had, lds);
-  if (had > 1) {
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r[k] *= isb;
+    for (int k = 0; k < 16; ++k) r[k] *= isb;
   }
 }
 
-// The lane's eight codes, column c in the lowest nibble.  Four neighbouring lanes make a block:
+// The lane's sixteen codes, column c in the lowest nibble.  Two neighbouring lanes make a block:
 // its scale (a NaN or infinity in it: 2^127, `bad`, codes zero); `four`: the scale bytes of the
-// 128 columns that the lane's row of 16 lanes holds.
-__device__ __forceinline__ unsigned encode(const float (&r)[8], float& scale, bool& bad, int& four) {
+// 128 columns that the lane's group of 8 lanes holds.
+__device__ __forceinline__ u32x2 encode(const float (&r)[16], float& scale, bool& bad, int& four) {
   const int lane = threadIdx.x & 63;
   unsigned top = 0;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(r[k]) & 0x7fffffffu);
+  for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(r[k]) & 0x7fffffffu);
   top = max(top, (unsigned)__builtin_amdgcn_mov_dpp((int)top, 0xb1, 0xf, 0xf, true));
-  top = max(top, (unsigned)__builtin_amdgcn_mov_dpp((int)top, 0x4e, 0xf, 0xf, true));
   const int ex = (int)(top >> 23);
   bad = ex == 255;
   const int byte = bad ? 255 : max(ex - 2, 0);          // e + 127
   scale = __uint_as_float(byte > 0 ? (unsigned)min(byte, 254) << 23 : 0x00400000u);
-  unsigned w = 0;
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[0], r[1], scale, 0);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[2], r[3], scale, 1);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[4], r[5], scale, 2);
-  w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, r[6], r[7], scale, 3);
-  four = byte << (2 * (lane & 12));
-  four |= __builtin_amdgcn_mov_dpp(four, 0x124, 0xf, 0xf, true);
-  four |= __builtin_amdgcn_mov_dpp(four, 0x128, 0xf, 0xf, true);
-  return bad ? 0 : w;
+  u32x2 w = {0, 0};
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k], r[8 * k + 1], scale, 0);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 2], r[8 * k + 3], scale, 1);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 4], r[8 * k + 5], scale, 2);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 6], r[8 * k + 7], scale, 3);
+    w[k] = bad ? 0 : w[k];
+  }
+  four = byte << (4 * (lane & 6));
+  four |= __builtin_amdgcn_mov_dpp(four, 0x4e, 0xf, 0xf, true);
+  four |= __builtin_amdgcn_mov_dpp(four, 0x141, 0xf, 0xf, true);
+  return w;
 }
 
 }  // namespace

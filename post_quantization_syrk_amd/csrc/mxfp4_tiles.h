@@ -28,14 +28,13 @@ struct ProductArgs {
 // A product with few rows (mxfp4_few.hip): whether it is one, and its launch.  x: the rows to
 // quantise on the way in, at most as many as `mx_few_rows` says, or quantised rows (KQ_MXFP4).
 bool mx_few(const ProductArgs& p);
-bool mx_few_fused(const ProductArgs& p, const MxRows& x, int64_t block);
+bool mx_few_fused(const ProductArgs& p, const MxRows& x);
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s);
 
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
-typedef unsigned u32x2 __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
