@@ -79,7 +79,18 @@ __device__ __forceinline__ Tile tile_at(const ProductArgs& a, const ExpertTable&
   } else {
     find_rows<BM>(a, tab, mt, t);
   }
-  return t;
+  // (the same for every lane; said here, or each copy would loop over its lanes' descriptors)
+  return Tile{__builtin_amdgcn_readfirstlane(t.e), __builtin_amdgcn_readfirstlane(t.m0),
+              __builtin_amdgcn_readfirstlane(t.last), __builtin_amdgcn_readfirstlane(t.n0)};
+}
+
+// A word of LDS that a copy has put there, once the caller knows it has landed: behind a plain
+// read the compiler would wait for every copy and store outstanding.
+__device__ __forceinline__ int read_lds(const int* p) {
+  int v;
+  asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)"
+               : "=&v"(v) : "v"((unsigned)(uintptr_t)(__attribute__((address_space(3))) const void*)p) : "memory");
+  return v;
 }
 
 // One wave's copy of 64 pieces of SIZE bytes into LDS, piece l to `to` + SIZE l; a lane whose
@@ -161,7 +172,6 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
   const uint8_t* pa[CA];   // X_FAR: x beyond the reach of a 32-bit offset
   int stepa[CA];
   int issued;
-  const int slot4 = lane & 3;
   // Points the copies at tile t; `row` gives the row of x behind a row of the tile.
   auto aim = [&](const Tile& t, auto row_of_x) {
     auto x_row = [&](int r) -> int64_t {   // -1: zeros
@@ -171,29 +181,31 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
     };
     auto w_row = [&](int r) -> unsigned { return (unsigned)min((int64_t)r, a.N - 1 - t.n0); };
     issued = 0;
+    int ln = lane;
+    asm volatile("" : "+v"(ln));   // the positions computed here, not kept in registers for every tile
     xc = a.xc + (ROWS == X_ROWS ? t.m0 * a.pitch : 0);
     xs = a.xs + (ROWS == X_ROWS ? (int64_t)t.m0 * 4 : 0);
     wc_e = a.wc + ((int64_t)t.e * a.N + t.n0) * a.pitch;
     ws_e = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
 #pragma unroll
     for (int r = 0; r < CA; ++r) {
-      const int pos = (wave * CA + r) * 16 + (lane >> 2), p = pos % (32 * MT);
+      const int pos = (wave * CA + r) * 16 + (ln >> 2), p = pos % (32 * MT);
       const int64_t row = x_row(pos / (32 * MT) * (32 * MT) + (p & 31) * MT + (p >> 5));
-      const int64_t at = row * a.pitch + 16 * (slot4 ^ ((pos >> 2) & 3));
+      const int64_t at = row * a.pitch + 16 * ((ln & 3) ^ ((pos >> 2) & 3));
       oa[r] = row >= 0 ? (unsigned)at : ALL;
       pa[r] = row >= 0 ? a.xc + at : (const uint8_t*)g_zeros;
       stepa[r] = row >= 0 ? 64 : 0;
     }
 #pragma unroll
     for (int r = 0; r < CB; ++r) {
-      const int pos = (wave * CB + r) * 16 + (lane >> 2), p = pos % (32 * NT);
+      const int pos = (wave * CB + r) * 16 + (ln >> 2), p = pos % (32 * NT);
       ob[r] = w_row(pos / (32 * NT) * (32 * NT) + (p & 31) * NT + (p >> 5)) * (unsigned)a.pitch +
-              16 * (slot4 ^ ((pos >> 2) & 3));
+              16 * ((ln & 3) ^ ((pos >> 2) & 3));
     }
 #pragma unroll
     for (int k = 0; k < SC; ++k) {
       const int si = min(wave * SC + k, SI - 1);
-      const int64_t row = si < MT ? x_row(64 * si + lane) : w_row(64 * (si - MT) + lane);
+      const int64_t row = si < MT ? x_row(64 * si + ln) : w_row(64 * (si - MT) + ln);
       os[k] = row >= 0 ? (unsigned)row * 4 : ALL;
     }
   };
@@ -343,7 +355,10 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
     }
     // the next tile's copies follow the last ones of this tile: those of its last round
     auto aim_next = [&]() {
-      if (more) aim(nt, [&](int r) { return a.index ? next_index[r] : nt.m0 + r; });
+      if (more) aim(nt, [&](int r) {
+        const int x = read_lds(next_index + r);
+        return a.index ? x : nt.m0 + r;
+      });
     };
     for (int k = 0; k < rounds; ++k) {
       if (k == rounds - 1) {
@@ -387,7 +402,10 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
           for (int j = 0; j < 16; ++j) {
             float v[NT];
 #pragma unroll
-            for (int k = 0; k < NT; ++k) v[k] = sums[k][j];
+            for (int k = 0; k < NT; ++k) {
+              v[k] = sums[k][j];
+              asm("" : "+v"(v[k]));   // side by side in the other registers: there is none left of these
+            }
             put(lane_at + (((j >> 2) * 8 + (j & 3)) * MT + m) * pitch, v);
           }
         }
