@@ -128,20 +128,21 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
     __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v[0]), r, off, 0, 0);
 }
 
-// Tiles of BM x BN outputs, 128 of K per stage, waves in 2 x WC, each with MT x NT accumulators
-// of 32 x 32.  A workgroup takes tile after tile; the copies of the next tile's first stages
+// Tiles of BM x BN outputs, 256 of K per stage, waves in 2 x WC, each with MT x NT accumulators
+// of 32 x 32, RING stages in LDS.  A stage is 128 bytes of every row, a whole line: with 64, the
+// copies alone of an 8192 x 8192 x 8192 product took 170 us, with 128 107 us.  A workgroup takes tile after tile; the copies of the next tile's first stages
 // follow those of the last stages of the present one, so the ring never runs dry and the stores
 // of one tile go out while the next is multiplied.
 template <int MT, int NT, int WC, int RING, int ROWS>
-__global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
-  constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 64, PANELS = (BM + BN) * 64;
-  constexpr int CA = 2 * MT / WC, CB = NT;            // copies of x and of W per wave and stage
-  constexpr int SI = (BM + BN) / 64, SC = (SI + 2 * WC - 1) / (2 * WC);   // scale copies: all, per wave
-  constexpr int COPIES = CA + CB + SC;
-  constexpr int STAGE = PANELS + (BM + BN) * 4;
+__global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
+  constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
+  constexpr int CA = 4 * MT / WC, CB = 2 * NT;        // copies of x and of W per wave and stage
+  constexpr int SI = (BM + BN) / 64, SC = (SI + 2 * WC - 1) / (2 * WC);   // scale copies of 128 of K: all, per wave
+  constexpr int COPIES = CA + CB + 2 * SC, SCALES = (BM + BN) * 4;
+  constexpr int STAGE = PANELS + 2 * SCALES;
   __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t b2[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t b2[RING == 4 ? STAGE : 16];
   __shared__ __attribute__((aligned(1024))) uint8_t b3[RING == 4 ? STAGE : 16];
   __shared__ ExpertTable tab[1];
   __shared__ __attribute__((aligned(256))) int next_index[ROWS == X_ROWS ? 64 : BM];
@@ -189,18 +190,18 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
     ws_e = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
 #pragma unroll
     for (int r = 0; r < CA; ++r) {
-      const int pos = (wave * CA + r) * 16 + (ln >> 2), p = pos % (32 * MT);
+      const int pos = (wave * CA + r) * 8 + (ln >> 3), p = pos % (32 * MT);
       const int64_t row = x_row(pos / (32 * MT) * (32 * MT) + (p & 31) * MT + (p >> 5));
-      const int64_t at = row * a.pitch + 16 * ((ln & 3) ^ ((pos >> 2) & 3));
+      const int64_t at = row * a.pitch + 16 * ((ln & 7) ^ ((pos >> 1) & 7));
       oa[r] = row >= 0 ? (unsigned)at : ALL;
       pa[r] = row >= 0 ? a.xc + at : (const uint8_t*)g_zeros;
-      stepa[r] = row >= 0 ? 64 : 0;
+      stepa[r] = row >= 0 ? 128 : 0;
     }
 #pragma unroll
     for (int r = 0; r < CB; ++r) {
-      const int pos = (wave * CB + r) * 16 + (ln >> 2), p = pos % (32 * NT);
+      const int pos = (wave * CB + r) * 8 + (ln >> 3), p = pos % (32 * NT);
       ob[r] = w_row(pos / (32 * NT) * (32 * NT) + (p & 31) * NT + (p >> 5)) * (unsigned)a.pitch +
-              16 * ((ln & 3) ^ ((pos >> 2) & 3));
+              16 * ((ln & 7) ^ ((pos >> 1) & 7));
     }
 #pragma unroll
     for (int k = 0; k < SC; ++k) {
@@ -209,61 +210,71 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
       os[k] = row >= 0 ? (unsigned)row * 4 : ALL;
     }
   };
+  const int stages = (a.steps + 1) / 2;
   auto issue = [&](uint8_t* buf) {
-    const bool live = issued < a.steps;
+    // The last stage of an odd number of steps has no second half: its lanes leave their
+    // descriptors.  (In the swizzled order a lane's half of the row is that of its source.)
+    const bool live = issued < stages, half = (a.steps & 1) && issued >= stages - 1;
     const __amdgpu_buffer_rsrc_t ra = rsrc(xc, live ? (int)ALL : 0), rb = rsrc(wc_e, (int)ALL);
 #pragma unroll
     for (int r = 0; r < CA; ++r) {
       uint8_t* to = buf + (wave * CA + r) * 1024;
+      const bool cut = half && (((lane & 7) ^ (((wave * CA + r) * 8 + (lane >> 3)) >> 1)) & 4);
       if (ROWS == X_FAR) {
-        copy_lds(live ? pa[r] : (const uint8_t*)g_zeros, to);
+        copy_lds(live && !cut ? pa[r] : (const uint8_t*)g_zeros, to);
         pa[r] += stepa[r];
       } else {
-        copy_lds<16>(ra, oa[r], to);
+        copy_lds<16>(ra, cut ? ALL : oa[r], to);
       }
     }
 #pragma unroll
-    for (int r = 0; r < CB; ++r) copy_lds<16>(rb, ob[r], buf + PANEL_A + (wave * CB + r) * 1024);
-#pragma unroll
-    for (int k = 0; k < SC; ++k) {
-      const int si = min(wave * SC + k, SI - 1);
-      copy_lds<4>(rsrc(si < MT ? xs : ws_e, (int)ALL), os[k], buf + PANELS + si * 256);
+    for (int r = 0; r < CB; ++r) {
+      const bool cut = half && (((lane & 7) ^ (((wave * CB + r) * 8 + (lane >> 3)) >> 1)) & 4);
+      copy_lds<16>(rb, cut ? ALL : ob[r], buf + PANEL_A + (wave * CB + r) * 1024);
     }
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+      for (int k = 0; k < SC; ++k) {
+        const int si = min(wave * SC + k, SI - 1);
+        const uint8_t* from = si < MT ? xs + 4 * a.rows * h : ws_e + 4 * a.N * h;
+        copy_lds<4>(rsrc(from, h && half ? 0 : (int)ALL), os[k], buf + PANELS + h * SCALES + si * 256);
+      }
     // past the end the last stage's weights and scales are copied again, with zeros for x
-    const int64_t on = ++issued < a.steps;
-    xc += 64 * on;
-    wc_e += 64 * on;
-    xs += 4 * a.rows * on;
-    ws_e += 4 * a.N * on;
+    const int64_t on = ++issued < stages;
+    xc += 128 * on;
+    wc_e += 128 * on;
+    xs += 8 * a.rows * on;
+    ws_e += 8 * a.N * on;
   };
 
   f32x16 acc[MT][NT];
 
-  const int swz = (l32 >> 2) & 3;
-  const int off0 = (l32 * 4 + (q ^ swz)) * 16, off1 = (l32 * 4 + ((2 + q) ^ swz)) * 16;
+  // operands of 64 of K, quarter h of a stage: the lane's row, its chunk 2 h + q of 16 bytes
   const int sca = PANELS + (wr * 32 * MT + l32 * MT) * 4, scb = PANELS + BM * 4 + (wc * 32 * NT + l32 * NT) * 4;
   auto read = [&](const uint8_t* buf, int h, i32x4 (&xa)[MT], i32x4 (&xb)[NT]) {
-    const uint8_t* pA = buf + wr * MT * 2048 + (h ? off1 : off0);
-    const uint8_t* pB = buf + PANEL_A + wc * NT * 2048 + (h ? off1 : off0);
+    const int off = l32 * 128 + ((2 * h + q) ^ ((l32 >> 1) & 7)) * 16;
+    const uint8_t* pA = buf + wr * MT * 4096 + off;
+    const uint8_t* pB = buf + PANEL_A + wc * NT * 4096 + off;
     xa[0] = *(const i32x4*)pA;
 #pragma unroll
-    for (int n = 0; n < NT; ++n) xb[n] = *(const i32x4*)(pB + n * 2048);
+    for (int n = 0; n < NT; ++n) xb[n] = *(const i32x4*)(pB + n * 4096);
 #pragma unroll
-    for (int m = 1; m < MT; ++m) xa[m] = *(const i32x4*)(pA + m * 2048);
+    for (int m = 1; m < MT; ++m) xa[m] = *(const i32x4*)(pA + m * 4096);
   };
-  auto read_scales = [&](const uint8_t* buf, int (&sa)[MT], int (&sb)[NT]) {
+  auto read_scales = [&](const uint8_t* buf, int h, int (&sa)[MT], int (&sb)[NT]) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sa[m] = *(const int*)(buf + sca + 4 * m) >> (8 * q);
+    for (int m = 0; m < MT; ++m) sa[m] = *(const int*)(buf + h * SCALES + sca + 4 * m) >> (8 * q);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sb[n] = *(const int*)(buf + scb + 4 * n) >> (8 * q);
+    for (int n = 0; n < NT; ++n) sb[n] = *(const int*)(buf + h * SCALES + scb + 4 * n) >> (8 * q);
   };
   auto mma0 = [&](const i32x4 (&xa)[MT], const i32x4 (&xb)[NT], const int (&sa)[MT], const int (&sb)[NT]) {
 #pragma unroll
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int n = 0; n < NT; ++n)
-        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(
-            widen(xa[m]), widen(xb[n]), acc[m][n], 4, 4, 0, sa[m], 0, sb[n]);
+        acc[m][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(widen(xa[m]), widen(xb[n]), acc[m][n], 4, 4, 0,
+                                                                   sa[m], 0, sb[n]);
   };
   auto mma1 = [&](const i32x4 (&xa)[MT], const i32x4 (&xb)[NT], const int (&sa)[MT], const int (&sb)[NT]) {
 #pragma unroll
@@ -280,36 +291,46 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
   int sa[MT], sb[NT], ta[MT], tb[NT];
   issue(b0);
   issue(b1);
-  issue(b2);
-  if constexpr (RING == 4) issue(b3);
+  if constexpr (RING == 4) {
+    issue(b2);
+    issue(b3);
+  }
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   lds_barrier();
   read(b0, 0, xa, xb);
-  read_scales(b0, sa, sb);
+  read_scales(b0, 0, sa, sb);
 
-// Stage s: read the operands of its second half while multiplying the first; wait for this
-// wave's copies of stage s + 1 (at most WAIT newer ones outstanding) and for every wave's reads
-// of stage s; refill its buffer and read the first half of stage s + 1 while multiplying the
-// second half.
-#define KQ_MX_STEP(CUR, NXT, SA, SB, TA, TB, WAIT)           \
+// Stage: read the operands of each quarter while multiplying the one before.  Ahead of the last
+// quarter, wait for this wave's copies of the next stage and for every wave's reads of this one;
+// then refill its buffer and read the next stage's first quarter.
+#define KQ_MX_SPREAD(COUNT, GROUP)                          \
+  _Pragma("unroll") for (int i_ = 0; i_ < (COUNT); ++i_) {  \
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, GROUP);  \
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, GROUP);  \
+  }                                                         \
+  __builtin_amdgcn_sched_barrier(0);
+#define KQ_MX_STAGE(CUR, NXT, WAIT)                         \
   {                                                         \
     read(CUR, 1, ya, yb);                                   \
-    mma0(xa, xb, SA, SB);                                   \
-    _Pragma("unroll") for (int i_ = 0; i_ < MT + NT; ++i_) { \
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);    \
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);    \
-    }                                                       \
-    __builtin_amdgcn_sched_barrier(0);                      \
+    read_scales(CUR, 1, ta, tb);                            \
+    mma0(xa, xb, sa, sb);                                   \
+    KQ_MX_SPREAD(MT + NT + 2, 0)                            \
+    read(CUR, 2, xa, xb);                                   \
+    mma1(ya, yb, sa, sb);                                   \
+    KQ_MX_SPREAD(MT + NT, 0)                                \
+    read(CUR, 3, ya, yb);                                   \
+    mma0(xa, xb, ta, tb);                                   \
+    KQ_MX_SPREAD(MT + NT, 0)                                \
     WAIT;                                                   \
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);                 \
     lds_barrier();                                          \
     issue(CUR);                                             \
     read(NXT, 0, xa, xb);                                   \
-    read_scales(NXT, TA, TB);                               \
-    mma1(ya, yb, SA, SB);                                   \
-    _Pragma("unroll") for (int i_ = 0; i_ < COPIES; ++i_) { \
+    read_scales(NXT, 0, sa, sb);                            \
+    mma1(ya, yb, ta, tb);                                   \
+    _Pragma("unroll") for (int i_ = 0; i_ < MT * NT; ++i_) { \
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);    \
-      __builtin_amdgcn_sched_group_barrier(0x020, 1, 1);    \
+      __builtin_amdgcn_sched_group_barrier(0x020, (COPIES + MT * NT - 1) / (MT * NT), 1); \
       __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);    \
     }                                                       \
     __builtin_amdgcn_sched_barrier(0);                      \
@@ -317,16 +338,13 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
 // A round of the ring, each stage in its buffer
 #define KQ_MX_ROUND()                                                                         \
   if constexpr (RING == 4) {                                                                  \
-    KQ_MX_STEP(b0, b1, sa, sb, ta, tb, wait_stage(k))                                         \
-    KQ_MX_STEP(b1, b2, ta, tb, sa, sb, wait_stage(k))                                         \
-    KQ_MX_STEP(b2, b3, sa, sb, ta, tb, wait_stage(k))                                         \
-    KQ_MX_STEP(b3, b0, ta, tb, sa, sb, wait_stage(1))                                         \
+    KQ_MX_STAGE(b0, b1, wait_stage(k))                                                        \
+    KQ_MX_STAGE(b1, b2, wait_stage(k))                                                        \
+    KQ_MX_STAGE(b2, b3, wait_stage(k))                                                        \
+    KQ_MX_STAGE(b3, b0, wait_stage(1))                                                        \
   } else {                                                                                    \
-    KQ_MX_STEP(b0, b1, sa, sb, ta, tb, wait_stage(k))                                         \
-    KQ_MX_STEP(b1, b2, ta, tb, sa, sb, wait_stage(k))                                         \
-    KQ_MX_STEP(b2, b0, sa, sb, ta, tb, wait_stage(1))                                         \
-    _Pragma("unroll") for (int m_ = 0; m_ < MT; ++m_) sa[m_] = ta[m_];                        \
-    _Pragma("unroll") for (int n_ = 0; n_ < NT; ++n_) sb[n_] = tb[n_];                        \
+    KQ_MX_STAGE(b0, b1, wait_stage(k))                                                        \
+    KQ_MX_STAGE(b1, b0, wait_stage(1))                                                        \
   }
   // Waits for the next stage's copies.  The 16 MT stores of the tile before are newer than the
   // copies of this one's first stages: before the last stage of the first round (k = 0) they stay
@@ -337,7 +355,7 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
     asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(%2)\n.Lstage%=:"
                  :: "s"(k), "n"(AFTER), "n"(STEADY) : "scc", "memory");
   };
-  const int rounds = (a.steps + RING - 1) / RING;   // stages past the end multiply zeros
+  const int rounds = (stages + RING - 1) / RING;   // stages past the end multiply zeros
   const int size = a.y_bf16 ? 2 : 4;
 
   for (;;) {
@@ -443,7 +461,8 @@ __global__ __launch_bounds__(128 * WC, RING == 3 || WC == 4 ? 2 : 1) void mx_til
     t = nt;
   }
 #undef KQ_MX_ROUND
-#undef KQ_MX_STEP
+#undef KQ_MX_STAGE
+#undef KQ_MX_SPREAD
   // the ring's trailing copies must land before its LDS is released
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
 }
@@ -459,7 +478,7 @@ kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC;
   const int64_t tm = ceil_div(p.slots, BM) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
   // one workgroup for each place on the card, or for each tile if there are fewer
-  constexpr int PLACES = 160 * 1024 / (RING * (BM + BN) * 68 + (1 << 13));
+  constexpr int PLACES = 160 * 1024 / (RING * (BM + BN) * 136 + (1 << 13));
   const int64_t total = std::min<int64_t>(ceil_div(tm * ceil_div(p.N, BN), 8),
                                           ceil_div(device_cu_count() * std::min(PLACES, 4), 8)) * 8;
   const dim3 grid((unsigned)total), block(128 * WC);
@@ -467,7 +486,7 @@ kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
     mx_tile_kernel<MT, NT, WC, RING, X_ROWS><<<grid, block, 0, s>>>(p);
   else if (!x_far(p))
     mx_tile_kernel<MT, NT, WC, RING, X_INDEX><<<grid, block, 0, s>>>(p);
-  else if constexpr (MT == 4 && NT == 4)
+  else if constexpr (MT == 4 && WC == 4)
     mx_tile_kernel<MT, NT, WC, RING, X_FAR><<<grid, block, 0, s>>>(p);
   KQ_LAUNCHED("mx_tile_kernel");
   return KQ_OK;
@@ -516,16 +535,16 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
   if (few && x.type != KQ_MXFP4 && mx_few_fused(p, x)) return mx_few_product(p, x, block, true, s);
   if (x.type != KQ_MXFP4) KQ_TRY(mx_quantize(x, block, (uint8_t*)p.xc, (uint8_t*)p.xs, nullptr, 0, s));
   if (few) return mx_few_product(p, x, block, false, s);
-  switch (p.offsets && x_far(p) ? 44 : testing_value(KQ_TESTING_MX_TILE, 448)) {
-    case 44: return launch_tiles<4, 4, 2, 4>(p, s);
-    case 448: return launch_tiles<4, 2, 4, 4>(p, s);
-    case 243: return launch_tiles<2, 4, 2, 3>(p, s);
-    case 423: return launch_tiles<4, 2, 2, 3>(p, s);
-    case 24: return launch_tiles<2, 4, 2, 4>(p, s);
-    case 42: return launch_tiles<4, 2, 2, 4>(p, s);
-    case 22: return launch_tiles<2, 2, 2, 4>(p, s);
-    case 12: return launch_tiles<1, 2, 2, 4>(p, s);
-    default: return launch_tiles<1, 1, 2, 4>(p, s);
+  switch (p.offsets && x_far(p) ? 448 : testing_value(KQ_TESTING_MX_TILE, 448)) {
+    case 448: return launch_tiles<4, 2, 4, 2>(p, s);
+    case 24: return launch_tiles<2, 4, 2, 2>(p, s);
+    case 42: return launch_tiles<4, 2, 2, 2>(p, s);
+    case 22: return launch_tiles<2, 2, 2, 2>(p, s);
+    case 224: return launch_tiles<2, 2, 2, 4>(p, s);
+    case 12: return launch_tiles<1, 2, 2, 2>(p, s);
+    case 124: return launch_tiles<1, 2, 2, 4>(p, s);
+    case 114: return launch_tiles<1, 1, 2, 4>(p, s);
+    default: return launch_tiles<1, 1, 2, 2>(p, s);
   }
 }
 

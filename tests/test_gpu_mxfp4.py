@@ -476,7 +476,7 @@ def _forced(knobs):
 
 
 PATHS = [dict(KQ_TESTING_MX_FUSED=0), dict(KQ_TESTING_MX_FUSED=1 << 20),
-         *(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (448, 24, 42, 22, 12))]
+         *(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (448, 24, 42, 22, 12, 11))]
 
 
 @pytest.mark.parametrize("path", PATHS, ids=str)
