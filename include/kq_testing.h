@@ -32,10 +32,13 @@ enum {
   /* Longest row (bytes) the quantizer's row kernels stage in LDS (default 65536); 0 forces
    * their direct paths, which longer rows take. */
   KQ_TESTING_ROW_LDS_BYTES = 2,
-  /* Outputs per workgroup of the MXFP4 products. */
+  /* Rows and columns of the MXFP4 products' tiles: 256, 128 or 64 (default: by their time). */
   KQ_TESTING_MX_TILE = 3,
-  /* Most rows (per expert, on average) of the MXFP4 products' few-row kernel; most activations that it quantises itself. */
+  /* Most rows (per expert, on average) that the MXFP4 products' few-row kernel takes (default 32
+   * or 16, by the size of the layer); 0: none. */
   KQ_TESTING_MX_FEW = 4,
+  /* Most activations (rows times columns, for experts slots times columns) that the few-row
+   * kernel quantises itself (default 8192); 0: none. */
   KQ_TESTING_MX_FUSED = 5
 };
 

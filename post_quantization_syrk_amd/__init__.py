@@ -443,69 +443,84 @@ def kq_mxfp4_empty(rows: int, n: int, experts: int | None = None, device="cuda")
             torch.empty((*lead, np_ // 128, rows, 4), dtype=torch.uint8, device=device))
 
 
-# One token's call takes less time on the GPU than the checks of the functions above take here, so
-# those below read each tensor's properties once and pass plain integers.
-def _mx_type(t, name: str) -> int:
+# One token's call takes no longer on the GPU than these checks take here, so they read each tensor's
+# properties once and pass plain integers.
+_mx_types = None   # tensor type -> KQ_*, and the types below, once torch is imported
+_mx_f32 = _mx_bf16 = _mx_u8 = _mx_i8 = _mx_i32 = None
+_mx_stream_of = _mx_device = None
+
+
+def _mx_setup() -> None:
+    global _mx_types, _mx_f32, _mx_bf16, _mx_u8, _mx_i8, _mx_i32, _mx_stream_of, _mx_device
     torch = _torch()
-    if isinstance(t, torch.Tensor):
-        if t.dtype is torch.bfloat16:
-            return KQ_BF16
-        if t.dtype is torch.float32:
-            return KQ_F32
-        raise TypeError(f"{name}: dtype {t.dtype} is neither float32 nor bfloat16")
-    raise TypeError(f"{name} must be a device (cuda/hip) tensor")
+    _mx_f32, _mx_bf16, _mx_u8, _mx_i8, _mx_i32 = (torch.float32, torch.bfloat16, torch.uint8, torch.int8, torch.int32)
+    _mx_stream_of, _mx_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    _mx_types = {_mx_f32: KQ_F32, _mx_bf16: KQ_BF16}
+    load_library()
 
 
 def _mx_ptr(t, name: str, dtype) -> int:
-    torch = _torch()
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a device (cuda/hip) tensor")
-    if dtype is not None and t.dtype is not dtype:
-        raise TypeError(f"{name}: dtype {t.dtype} is not {dtype}")
-    return t.data_ptr()
+    try:
+        if t.dtype is dtype and t.is_cuda:
+            return t.data_ptr()
+        kind = f"{t.dtype} on {t.device}"
+    except AttributeError:
+        kind = type(t).__name__
+    raise TypeError(f"{name} must be a device (cuda/hip) tensor of {dtype}, not {kind}")
 
 
-def _mx_stream(stream) -> int:
-    torch = _torch()
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+def _mx_matrix(t, name: str):
+    """(pointer, KQ_* type, rows, columns, leading dimension) of an fp32 or bf16 matrix."""
+    try:
+        kind = _mx_types.get(t.dtype)
+        if kind is None or not t.is_cuda:
+            raise TypeError(f"{name} must be a device (cuda/hip) tensor of float32 or bfloat16, not {t.dtype} on {t.device}")
+        rows, cols = t.shape
+        ld, step = t.stride()
+    except AttributeError:
+        raise TypeError(f"{name} must be a device (cuda/hip) tensor, not {type(t).__name__}") from None
+    except ValueError:
+        raise ValueError(f"{name} must be a matrix, not {tuple(t.shape)}") from None
+    if step != 1 and cols > 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return t.data_ptr(), kind, rows, cols, ld if rows > 1 else cols
 
 
 def _mx_vector(v, name: str, n: int, dtype):
     if v is None:
         return None
+    p = _mx_ptr(v, name, dtype)
     if v.numel() != n or not v.is_contiguous():
         raise ValueError(f"{name} must hold {n} contiguous entries")
-    return _mx_ptr(v, name, dtype)
+    return p
 
 
 def _mx_check(codes, scales, shape: tuple, n: int, name: str):
-    torch = _torch()
-    groups = -(-n // 128)
+    cp, sp, groups = _mx_ptr(codes, f"{name} codes", _mx_u8), _mx_ptr(scales, f"{name} scales", _mx_u8), -(-n // 128)
     if codes.shape != (*shape, 64 * groups) or not codes.is_contiguous():
         raise ValueError(f"{name} codes must be contiguous {(*shape, 64 * groups)}")
     if scales.shape != (*shape[:-1], groups, shape[-1], 4) or not scales.is_contiguous():
         raise ValueError(f"{name} scales must be contiguous {(*shape[:-1], groups, shape[-1], 4)}")
-    return _mx_ptr(codes, f"{name} codes", torch.uint8), _mx_ptr(scales, f"{name} scales", torch.uint8)
+    return cp, sp
 
 
 def kq_mxfp4_quantize(src, codes, scales, d=None, sign=None, had: int = 1, values=None, stream=None) -> None:
     """Rows of src (fp32 or bf16, rows x n) to MXFP4 codes and scales (kq_mxfp4_empty) of
     P D^-1 src; `values` (bf16, rows x n, optional) receives what they stand for."""
-    torch = _torch()
-    lib = load_library()
-    xt = _mx_type(src, "src")
-    rows, n = src.shape
+    if _mx_types is None:
+        _mx_setup()
+    xp, xt, rows, n, ld = _mx_matrix(src, "src")
     cp, sp = _mx_check(codes, scales, (rows,), n, "output")
     vp, ldv = None, 0
     if values is not None:
-        if values.shape != (rows, n):
+        vp, vt, vrows, vcols, ldv = _mx_matrix(values, "values")
+        if vt != KQ_BF16:
+            raise TypeError("values must be bfloat16")
+        if vrows != rows or vcols != n:
             raise ValueError("values must have src's shape")
-        vp, ldv = _mx_ptr(values, "values", torch.bfloat16), _ld(values, "values")
-    st = lib.kq_mxfp4_quantize(_mx_ptr(src, "src", None), xt, rows, n, _ld(src, "src"),
-                               _mx_vector(d, "d", n, torch.float32), _mx_vector(sign, "sign", n, torch.int8), had,
-                               cp, sp, vp, ldv, _mx_stream(stream))
+    st = _lib.kq_mxfp4_quantize(xp, xt, rows, n, ld, _mx_vector(d, "d", n, _mx_f32),
+                                _mx_vector(sign, "sign", n, _mx_i8), had, cp, sp, vp, ldv,
+                                _mx_stream_of(_mx_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "kq_mxfp4_quantize")
 
@@ -520,38 +535,36 @@ def kq_mxfp4_workspace(rows: int, n: int) -> int:
 
 def _mx_rows(x, x_scales, d, sign, n, ws):
     """(pointer, type, rows, n, ld, scales, d, sign, ws, ws bytes) of the activations."""
-    torch = _torch()
+    if _mx_types is None:
+        _mx_setup()
     if x_scales is not None:
         if n is None:
             raise ValueError("quantised rows need n, their number of values")
         if d is not None or sign is not None:
             raise ValueError("quantised rows take no rescale and no signs")
-        rows = x.shape[0]
-        xp, sp = _mx_check(x, x_scales, (rows,), n, "x")
-        return xp, KQ_MXFP4, rows, n, kq_mxfp4_padded(n), sp, None, None, None, 0
-    xt = _mx_type(x, "x")
-    rows, cols = x.shape
+        xp, sp = _mx_check(x, x_scales, (x.shape[0],), n, "x")
+        return xp, KQ_MXFP4, x.shape[0], n, kq_mxfp4_padded(n), sp, None, None, None, 0
+    xp, xt, rows, cols, ld = _mx_matrix(x, "x")
     if n is not None and n != cols:
         raise ValueError(f"x has {cols} columns, not {n}")
     if ws is None:
-        ws = torch.empty(kq_mxfp4_workspace(rows, cols), dtype=torch.uint8, device=x.device)
-    return (_mx_ptr(x, "x", None), xt, rows, cols, _ld(x, "x"), None, _mx_vector(d, "d", cols, torch.float32),
-            _mx_vector(sign, "sign", cols, torch.int8), _mx_ptr(ws, "ws", torch.uint8), ws.numel())
+        ws = _torch().empty(kq_mxfp4_workspace(rows, cols), dtype=_mx_u8, device=x.device)
+    return (xp, xt, rows, cols, ld, None, _mx_vector(d, "d", cols, _mx_f32), _mx_vector(sign, "sign", cols, _mx_i8),
+            _mx_ptr(ws, "ws", _mx_u8), ws.numel())
 
 
 def kq_mxfp4_linear(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1, x_scales=None,
                     n=None, stream=None) -> None:
     """y = Q(P D^-1 x) W^T for a layer held in MXFP4: x fp32 or bf16 [rows, n] (or codes, with
     x_scales and n), y fp32 or bf16 [rows, out]."""
-    lib = load_library()
     xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
     out = w_codes.shape[0]
     cp, sp = _mx_check(w_codes, w_scales, (out,), n, "weight")
-    yt = _mx_type(y, "y")
-    if y.shape != (rows, out):
+    yp, yt, yrows, ycols, ldy = _mx_matrix(y, "y")
+    if yrows != rows or ycols != out:
         raise ValueError(f"y must be {(rows, out)}")
-    st = lib.kq_mxfp4_linear(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, _mx_ptr(y, "y", None), yt,
-                             _ld(y, "y"), wp, wb, _mx_stream(stream))
+    st = _lib.kq_mxfp4_linear(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, yp, yt, ldy, wp, wb,
+                              _mx_stream_of(_mx_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "kq_mxfp4_linear")
 
@@ -561,18 +574,14 @@ def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, s
     """y[s] = Q(P D^-1 x[index[s]]) W_e^T for the slots s of expert e, [offsets[e], offsets[e + 1]):
     index int32 [slots] or None, offsets int32 [experts + 1], weights of kq_mxfp4_empty(out, n,
     experts), y fp32 or bf16 [slots, out].  Offsets and index stay on the device."""
-    torch = _torch()
-    lib = load_library()
     xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
     experts, out = w_codes.shape[0], w_codes.shape[1]
     cp, sp = _mx_check(w_codes, w_scales, (experts, out), n, "weight")
-    yt = _mx_type(y, "y")
-    slots, cols = y.shape
-    if cols != out:
+    yp, yt, slots, ycols, ldy = _mx_matrix(y, "y")
+    if ycols != out:
         raise ValueError(f"y must have {out} columns")
-    st = lib.kq_mxfp4_experts(xp, xt, rows, n, ldx, xsp, dp, gp, had,
-                              _mx_vector(index, "index", slots, torch.int32), slots,
-                              _mx_vector(offsets, "offsets", experts + 1, torch.int32), experts, cp, sp, out,
-                              _mx_ptr(y, "y", None), yt, _ld(y, "y"), wp, wb, _mx_stream(stream))
+    st = _lib.kq_mxfp4_experts(xp, xt, rows, n, ldx, xsp, dp, gp, had, _mx_vector(index, "index", slots, _mx_i32), slots,
+                               _mx_vector(offsets, "offsets", experts + 1, _mx_i32), experts, cp, sp, out, yp, yt, ldy,
+                               wp, wb, _mx_stream_of(_mx_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "kq_mxfp4_experts")

@@ -73,7 +73,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
 // scales lie in one dword.
 // T: void for quantised activations, else their type, quantised here (MT = 1).
 template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE>
-__global__ __launch_bounds__(64 * WAVES) void mx_few_kernel(ProductArgs a, RowArgs x) {
+__global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, RowArgs x) {
   constexpr bool FUSED = !__is_void(T);
   constexpr int BM = 16 * MT, BN = 16 * NT, LD = BN + 4;
   extern __shared__ __attribute__((aligned(16))) float lds[];
@@ -234,30 +234,39 @@ kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
   return KQ_OK;
 }
 
-// Rows of a tile: the fewest that hold the rows per expert, on average, in one.
-int few_rows(const ProductArgs& p) {
-  const int64_t avg = p.offsets ? ceil_div(p.slots, p.experts) : p.slots;
-  return avg <= 16 ? 16 : avg <= 32 ? 32 : 64;
+// Rows per expert, on average.
+int64_t average_rows(const ProductArgs& p) { return p.offsets ? ceil_div(p.slots, p.experts) : p.slots; }
+
+// Row tiles of bm rows, for rows spread evenly over the experts.
+int64_t even_tiles(const ProductArgs& p, int bm) {
+  return p.offsets ? std::max<int64_t>(std::min<int64_t>(p.slots, p.experts), ceil_div(p.slots, bm)) : ceil_div(p.slots, bm);
 }
 
 }  // namespace
 
+// Up to 16 rows, or 32, where 64 x 64 tiles would leave compute units idle, or half of them
+// (16 rows, 4096 x 4096: 4.5 us here, 7.7 in tiles; 11008 x 4096: 7.9 and 8.0; 28672 x 8192:
+// 21.8 and 20.3; 32 rows, 4096 x 4096: 5.4 and 7.8; 11008 x 4096: 9.6 and 8.1).
 bool mx_few(const ProductArgs& p) {
-  const int64_t avg = p.offsets ? ceil_div(p.slots, p.experts) : p.slots;
-  return avg <= testing_value(KQ_TESTING_MX_FEW, 64) && p.slots <= 65535 && p.rows * p.pitch < 0x7fffffff;
+  const int64_t avg = average_rows(p), tiles = even_tiles(p, 64) * ceil_div(p.N, 64);
+  const int64_t rows = tiles < device_cu_count() / 2 ? 32 : tiles < device_cu_count() ? 16 : 0;
+  return avg <= testing_value(KQ_TESTING_MX_FEW, rows) && p.slots <= 65535 && p.rows * p.pitch < 0x7fffffff;
 }
 
+// One token or two: each workgroup quantises them for itself, while its part of the layer is on
+// the way (one token, 4096 x 4096: 7.8 us, and by a kernel of its own 4.5 + 3.7 and a launch; through
+// two of eight experts of 11008 x 4096: 16.4, and 4.2 + 13.8).
 bool mx_few_fused(const ProductArgs& p, const MxRows& x) {
   return x.rows > 0 && p.slots <= 16 && p.slots * x.n <= testing_value(KQ_TESTING_MX_FUSED, 8192);
 }
 
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s) {
   RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block))};
-  const int bm = fused ? 16 : few_rows(p);
+  const int bm = fused || average_rows(p) <= 16 ? 16 : 32;
   // Columns per workgroup: 64, so that its rows of x and its fixed costs serve more of the layer, or
   // as few as leave a workgroup for five of eight compute units (16 rows, 4096 x 4096: 3.7 us
   // with 16, 6.5 with 64; 11008 x 4096: 8.2 and 7.6; 28672 x 8192: 30 and 24).
-  const int64_t tm = p.offsets ? std::min<int64_t>(p.slots, std::max<int64_t>(p.experts, ceil_div(p.slots, bm))) : ceil_div(p.slots, bm);
+  const int64_t tm = even_tiles(p, bm);
   const int64_t enough = device_cu_count() * 5 / 8;
   const int nt = ceil_div(p.N, 64) * tm >= enough ? 4 : ceil_div(p.N, 32) * tm >= enough ? 2 : 1;
   if (fused) {
@@ -270,7 +279,7 @@ kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, b
   }
 #define KQ_FEW(MT) \
   (nt == 4 ? launch<8, MT, 4, 1, void>(p, r, s) : nt == 2 ? launch<8, MT, 2, 2, void>(p, r, s) : launch<8, MT, 1, 2, void>(p, r, s))
-  return bm == 16 ? KQ_FEW(1) : bm == 32 ? KQ_FEW(2) : KQ_FEW(4);
+  return bm == 16 ? KQ_FEW(1) : KQ_FEW(2);
 #undef KQ_FEW
 }
 

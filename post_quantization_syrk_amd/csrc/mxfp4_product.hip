@@ -129,11 +129,12 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 }
 
 // Tiles of BM x BN outputs, 256 of K per stage, waves in 2 x WC, each with MT x NT accumulators
-// of 32 x 32, RING stages in LDS.  A stage is 128 bytes of every row, a whole line: with 64, the
-// copies alone of an 8192 x 8192 x 8192 product took 170 us, with 128 107 us.  A workgroup takes tile after tile; the copies of the next tile's first stages
-// follow those of the last stages of the present one, so the ring never runs dry and the stores
-// of one tile go out while the next is multiplied.
-template <int MT, int NT, int WC, int RING, int ROWS>
+// of 32 x 32, two stages in LDS.  A stage is 128 bytes of every row, a whole line: with 64, the
+// copies alone of an 8192 x 8192 x 8192 product took 170 us, with 128 107 us.  A workgroup takes
+// tile after tile; the copies of the next tile's first stages follow those of the last stages of
+// the present one, so the ring never runs dry and the stores of one tile go out while the next is
+// multiplied.
+template <int MT, int NT, int WC, int ROWS>
 __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
   constexpr int CA = 4 * MT / WC, CB = 2 * NT;        // copies of x and of W per wave and stage
@@ -142,8 +143,6 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   constexpr int STAGE = PANELS + 2 * SCALES;
   __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t b2[RING == 4 ? STAGE : 16];
-  __shared__ __attribute__((aligned(1024))) uint8_t b3[RING == 4 ? STAGE : 16];
   __shared__ ExpertTable tab[1];
   __shared__ __attribute__((aligned(256))) int next_index[ROWS == X_ROWS ? 64 : BM];
   const int lane = threadIdx.x & 63;
@@ -250,10 +249,12 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
 
   f32x16 acc[MT][NT];
 
-  // operands of 64 of K, quarter h of a stage: the lane's row, its chunk 2 h + q of 16 bytes
+  // operands of 64 of K, quarter h of a stage: the lane's row, its chunk 2 h + q of 16 bytes, which
+  // lies in the place with the row's bits 1 .. 3 flipped (so that 16 rows cover all banks)
+  const int off0 = l32 * 128 + (q ^ ((l32 >> 1) & 7)) * 16;
   const int sca = PANELS + (wr * 32 * MT + l32 * MT) * 4, scb = PANELS + BM * 4 + (wc * 32 * NT + l32 * NT) * 4;
   auto read = [&](const uint8_t* buf, int h, i32x4 (&xa)[MT], i32x4 (&xb)[NT]) {
-    const int off = l32 * 128 + ((2 * h + q) ^ ((l32 >> 1) & 7)) * 16;
+    const int off = off0 ^ (32 * h);
     const uint8_t* pA = buf + wr * MT * 4096 + off;
     const uint8_t* pB = buf + PANEL_A + wc * NT * 4096 + off;
     xa[0] = *(const i32x4*)pA;
@@ -291,10 +292,6 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   int sa[MT], sb[NT], ta[MT], tb[NT];
   issue(b0);
   issue(b1);
-  if constexpr (RING == 4) {
-    issue(b2);
-    issue(b3);
-  }
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
   lds_barrier();
   read(b0, 0, xa, xb);
@@ -335,27 +332,16 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     }                                                       \
     __builtin_amdgcn_sched_barrier(0);                      \
   }
-// A round of the ring, each stage in its buffer
-#define KQ_MX_ROUND()                                                                         \
-  if constexpr (RING == 4) {                                                                  \
-    KQ_MX_STAGE(b0, b1, wait_stage(k))                                                        \
-    KQ_MX_STAGE(b1, b2, wait_stage(k))                                                        \
-    KQ_MX_STAGE(b2, b3, wait_stage(k))                                                        \
-    KQ_MX_STAGE(b3, b0, wait_stage(1))                                                        \
-  } else {                                                                                    \
-    KQ_MX_STAGE(b0, b1, wait_stage(k))                                                        \
-    KQ_MX_STAGE(b1, b0, wait_stage(1))                                                        \
-  }
-  // Waits for the next stage's copies.  The 16 MT stores of the tile before are newer than the
-  // copies of this one's first stages: before the last stage of the first round (k = 0) they stay
-  // outstanding (the counter holds 63).  One block of instructions: a branch that the compiler
-  // sees would let it move the matrix instructions across.
-  constexpr int STEADY = (RING - 2) * COPIES, AFTER = STEADY + 16 * MT < 63 ? STEADY + 16 * MT : 63;
+  // Waits for the next stage's copies: nothing newer is outstanding but, in a tile's first stage
+  // (k = 0), the 16 MT stores of the tile before, which may stay so (the counter holds 63).  One
+  // block of instructions: a branch that the compiler sees would let it move the matrix
+  // instructions across.
+  constexpr int STORES = 16 * MT < 63 ? 16 * MT : 63;
   auto wait_stage = [&](int k) {
-    asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(%2)\n.Lstage%=:"
-                 :: "s"(k), "n"(AFTER), "n"(STEADY) : "scc", "memory");
+    asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(0)\n.Lstage%=:"
+                 :: "s"(k), "n"(STORES) : "scc", "memory");
   };
-  const int rounds = (stages + RING - 1) / RING;   // stages past the end multiply zeros
+  const int rounds = (stages + 1) / 2;   // of two stages: one past the end multiplies zeros
   const int size = a.y_bf16 ? 2 : 4;
 
   for (;;) {
@@ -386,7 +372,8 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
         }
         aim_next();
       }
-      KQ_MX_ROUND()
+      KQ_MX_STAGE(b0, b1, wait_stage(k))
+      KQ_MX_STAGE(b1, b0, wait_stage(1))
     }
 
     // Lane l32 holds NT neighbouring columns of 16 MT rows.  The descriptor ends with the tile's
@@ -460,7 +447,6 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     if (!more) break;
     t = nt;
   }
-#undef KQ_MX_ROUND
 #undef KQ_MX_STAGE
 #undef KQ_MX_SPREAD
   // the ring's trailing copies must land before its LDS is released
@@ -473,23 +459,57 @@ size_t scale_bytes(int64_t rows, int64_t n) { return (size_t)rows * (size_t)(mx_
 // Whether an index can reach past the 32-bit offsets of the copies.
 bool x_far(const ProductArgs& p) { return p.rows * p.pitch >= 0xffff0000ll; }
 
-template <int MT, int NT, int WC, int RING>
+// Row tiles of BM rows: at most, over any offsets.
+int64_t row_tiles(const ProductArgs& p, int bm) {
+  return ceil_div(p.slots, bm) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
+}
+
+template <int MT, int NT, int WC>
 kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC;
-  const int64_t tm = ceil_div(p.slots, BM) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
   // one workgroup for each place on the card, or for each tile if there are fewer
-  constexpr int PLACES = 160 * 1024 / (RING * (BM + BN) * 136 + (1 << 13));
-  const int64_t total = std::min<int64_t>(ceil_div(tm * ceil_div(p.N, BN), 8),
+  constexpr int PLACES = 160 * 1024 / (2 * (BM + BN) * 136 + (1 << 13));
+  const int64_t total = std::min<int64_t>(ceil_div(row_tiles(p, BM) * ceil_div(p.N, BN), 8),
                                           ceil_div(device_cu_count() * std::min(PLACES, 4), 8)) * 8;
   const dim3 grid((unsigned)total), block(128 * WC);
   if (!p.offsets)
-    mx_tile_kernel<MT, NT, WC, RING, X_ROWS><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, X_ROWS><<<grid, block, 0, s>>>(p);
   else if (!x_far(p))
-    mx_tile_kernel<MT, NT, WC, RING, X_INDEX><<<grid, block, 0, s>>>(p);
-  else if constexpr (MT == 4 && WC == 4)
-    mx_tile_kernel<MT, NT, WC, RING, X_FAR><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, X_INDEX><<<grid, block, 0, s>>>(p);
+  else if constexpr (MT == 4)
+    mx_tile_kernel<MT, NT, WC, X_FAR><<<grid, block, 0, s>>>(p);
   KQ_LAUNCHED("mx_tile_kernel");
   return KQ_OK;
+}
+
+// The tile with the least time.  Up to 64 rows (of an expert, on average) the layer's bytes are the
+// bound, and the smallest tiles put the most workgroups at them: 8 experts of 11008 x 4096 and a
+// token 14.2 us (64 x 128 tiles: 16.6), 64 of 2048 x 2048 and 96 tokens 19.6 (22.6).  With more
+// rows, by a tile's time and the number of tiles that a compute unit gets: at K = 4096 and a full
+// card 33 us for 256 x 256, 9.4 for 128 x 128, 4.5 for 64 x 64 (4096 x 4096 outputs: 39, 42 and 66
+// in all; 2048 x 4096: 30, 24, 34; 256 x 4096: 24, 12, 8.6).  A smaller tile has to win clearly:
+// its count rounds less, but it reads more.
+kq_status launch_best(const ProductArgs& p, hipStream_t s) {
+  static const struct { int id; double cost; } tiles[] = {{256, 33.0}, {128, 9.4}, {64, 4.5}};
+  const int64_t active = p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0;
+  int64_t best = 64;
+  if ((p.offsets ? ceil_div(p.slots, p.experts) : p.slots) > 64) {
+    double least = 0;
+    for (const auto& t : tiles) {
+      // an expert's last tile is half full, on average, and it has one at least
+      const int64_t tm = p.offsets ? std::max(active, p.slots / t.id + active / 2) : ceil_div(p.slots, t.id);
+      const double cost = t.cost * (double)ceil_div(tm * ceil_div(p.N, t.id), device_cu_count());
+      if (least == 0 || cost < 0.8 * least) {
+        least = cost;
+        best = t.id;
+      }
+    }
+  }
+  switch (p.offsets && x_far(p) ? 256 : testing_value(KQ_TESTING_MX_TILE, best)) {
+    case 256: return launch_tiles<4, 2, 4>(p, s);
+    case 128: return launch_tiles<2, 2, 2>(p, s);
+    default: return launch_tiles<1, 1, 2>(p, s);
+  }
 }
 
 // Checks and quantises the activations (unless they are quantised already), then the product.
@@ -531,21 +551,10 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
     p.xs = (uint8_t*)ws + code_bytes(x.rows, x.n);
   }
   if (p.slots == 0) return KQ_OK;
-  const bool few = mx_few(p);
-  if (few && x.type != KQ_MXFP4 && mx_few_fused(p, x)) return mx_few_product(p, x, block, true, s);
+  if (x.type != KQ_MXFP4 && mx_few_fused(p, x)) return mx_few_product(p, x, block, true, s);
   if (x.type != KQ_MXFP4) KQ_TRY(mx_quantize(x, block, (uint8_t*)p.xc, (uint8_t*)p.xs, nullptr, 0, s));
-  if (few) return mx_few_product(p, x, block, false, s);
-  switch (p.offsets && x_far(p) ? 448 : testing_value(KQ_TESTING_MX_TILE, 448)) {
-    case 448: return launch_tiles<4, 2, 4, 2>(p, s);
-    case 24: return launch_tiles<2, 4, 2, 2>(p, s);
-    case 42: return launch_tiles<4, 2, 2, 2>(p, s);
-    case 22: return launch_tiles<2, 2, 2, 2>(p, s);
-    case 224: return launch_tiles<2, 2, 2, 4>(p, s);
-    case 12: return launch_tiles<1, 2, 2, 2>(p, s);
-    case 124: return launch_tiles<1, 2, 2, 4>(p, s);
-    case 114: return launch_tiles<1, 1, 2, 4>(p, s);
-    default: return launch_tiles<1, 1, 2, 2>(p, s);
-  }
+  if (mx_few(p)) return mx_few_product(p, x, block, false, s);
+  return launch_best(p, s);
 }
 
 }  // namespace

@@ -25,8 +25,8 @@ struct ProductArgs {
   int64_t ldy;
 };
 
-// A product with few rows (mxfp4_few.hip): whether it is one, and its launch.  x: the rows to
-// quantise on the way in, at most as many as `mx_few_rows` says, or quantised rows (KQ_MXFP4).
+// A product with few rows (mxfp4_few.hip): whether it is one, whether it quantises the rows of x
+// itself, and its launch (not fused: the rows are quantised, at p.xc and p.xs).
 bool mx_few(const ProductArgs& p);
 bool mx_few_fused(const ProductArgs& p, const MxRows& x);
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s);

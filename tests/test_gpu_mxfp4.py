@@ -476,7 +476,8 @@ def _forced(knobs):
 
 
 PATHS = [dict(KQ_TESTING_MX_FUSED=0), dict(KQ_TESTING_MX_FUSED=1 << 20),
-         *(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (448, 24, 42, 22, 12, 11))]
+         *(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (256, 128, 64)),
+         dict(KQ_TESTING_MX_FEW=1 << 20)]
 
 
 @pytest.mark.parametrize("path", PATHS, ids=str)
@@ -502,3 +503,165 @@ def test_every_path(rows, n, out, had, path):
             _close(y, xq, wv, kind == "bf16")
             kq.kq_mxfp4_experts(x.cuda(), _dev(index), _dev(offsets), ec, es, z, d=_dev(d), sign=_dev(sg), had=had)
             _experts_check(z, want, mag, n, kind == "bf16")
+
+
+def _random_codes(rows, n, experts=None):
+    """Device codes of any elements with scales 2^-3 .. 2^3 (NaN blocks would spread)."""
+    torch = torch_cuda()
+    kq = _kq()
+    gen = torch.Generator(device="cuda").manual_seed(rows + n)
+    codes, scales = kq.kq_mxfp4_empty(rows, n, experts)
+    codes.random_(0, 256, generator=gen)
+    scales.random_(124, 131, generator=gen)
+    return codes, scales
+
+
+def _values(codes, scales, rows):
+    """64-bit values of the given rows of device codes."""
+    torch = torch_cuda()
+    rows = torch.as_tensor(rows, device="cuda")
+    return om.mx_values(*om.mx_unpack(codes[rows].cpu().numpy(), scales[:, rows].contiguous().cpu().numpy()), 2 * codes.shape[1])
+
+
+@pytest.mark.parametrize("rows", [700_000, 1_060_000])
+def test_experts_of_rows_past_32_bits(rows):
+    """Quantised rows of more than 2 GiB and of more than 4 GiB, read through an index."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    n, out, slots = 8192, 70, 150
+    codes, scales = _random_codes(rows, n)
+    index = rng.integers(0, rows, slots).astype(np.int32)
+    index[[0, 1, 149]] = [rows - 1, 0, rows - 2]
+    wc, ws, wv = _layer(rng, out, n, 2)
+    y = _empty((slots, out), "f32")
+    offsets = np.int32([0, 3, slots])
+    kq.kq_mxfp4_experts(codes, _dev(index), _dev(offsets), wc, ws, y, x_scales=scales, n=n)
+    xq = _values(codes, scales, index)
+    want, mag = _experts_ref(xq, None, offsets, wv, slots, slots)
+    _experts_check(y, want, mag, n, False)
+    near = _empty((slots, out), "f32")   # the same rows side by side: the same sums
+    picked = torch.from_numpy(index).long().cuda()
+    with _forced(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=256)):
+        kq.kq_mxfp4_experts(codes[picked], None, _dev(offsets), wc, ws, near,
+                            x_scales=scales[:, picked].contiguous(), n=n)
+    assert rows < 1_000_000 or torch.equal(y, near)
+
+
+def test_linear_of_an_output_past_32_bits():
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(3)
+    rows, n, out = 1_000_003, 128, 2200
+    codes, scales = _random_codes(rows, n)
+    wc, ws, wv = _layer(rng, out, n)
+    y = _empty((rows, out), "bf16")
+    kq.kq_mxfp4_linear(codes, wc, ws, y, x_scales=scales, n=n)
+    some = np.concatenate([[0, 1, rows - 1, rows - 2, rows - 3], rng.integers(0, rows, 200)])
+    _close(y[torch.from_numpy(some).cuda()], _values(codes, scales, some), wv, True)
+
+
+@pytest.mark.parametrize("slots", [40, 600])
+def test_experts_of_layers_past_32_bits(slots):
+    kq = _kq()
+    rng = np.random.default_rng(slots)
+    n, out, experts = 8192, 4096, 260
+    wc, ws = _random_codes(out, n, experts)
+    x, xs = _random_codes(slots, n)
+    offsets = np.zeros(experts + 1, np.int32)
+    offsets[2:] = slots // 2          # the first half to expert 1, the rest to the last
+    offsets[-1] = slots
+    y = _empty((slots, out), "f32")
+    kq.kq_mxfp4_experts(x, None, _dev(offsets), wc, ws, y, x_scales=xs, n=n)
+    xq = _values(x, xs, np.arange(slots))
+    for lo, hi, e in ((0, slots // 2, 1), (slots // 2, slots, experts - 1)):
+        _close(y[lo:hi], xq[lo:hi], _values(wc[e], ws[e], np.arange(out)), False)
+
+
+def test_quantize_past_32_bits():
+    """The last rows of more than 4 GiB of input, and of more than 2^31 values, as a small call has them."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(4)
+    rows, n, had = 140_000, 16384, 4096
+    d, sg = (_dev(v) for v in _processing(rng, n, True, True))
+    x = torch.empty((rows, n), dtype=torch.bfloat16, device="cuda").normal_()
+    codes, scales = kq.kq_mxfp4_empty(rows, n)
+    values = torch.empty_like(x)
+    kq.kq_mxfp4_quantize(x, codes, scales, d=d, sign=sg, had=had, values=values)
+    for lo in (0, 65_536, rows - 9):
+        c, s = kq.kq_mxfp4_empty(9, n)
+        v = torch.empty((9, n), dtype=torch.bfloat16, device="cuda")
+        kq.kq_mxfp4_quantize(x[lo:lo + 9], c, s, d=d, sign=sg, had=had, values=v)
+        assert torch.equal(codes[lo:lo + 9], c) and torch.equal(scales[:, lo:lo + 9], s)
+        assert torch.equal(values[lo:lo + 9], v)
+
+
+@pytest.mark.parametrize("rows", [1, 20, 70, 300])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_output_rows_far_apart(rows, kind):
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    x = _rows(rng, rows, 384, "bf16")
+    wc, ws, wv = _layer(rng, 150, 384)
+    wide = _empty((rows, (1 << 20) + 8), kind)
+    xq = om.mx_round(x.double().numpy())
+    for path in ({}, dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=256), dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=64)):
+        wide.fill_(123.0)
+        with _forced(path):
+            kq.kq_mxfp4_linear(x.cuda(), wc, ws, wide[:, 3:153])
+        _close(wide[:, 3:153], xq, wv, kind == "bf16")
+        assert bool((wide[:, :3] == 123.0).all()) and bool((wide[:, 153:] == 123.0).all())
+
+
+@pytest.mark.parametrize("path", [{}, dict(KQ_TESTING_MX_FEW=0), *PATHS[2:5]], ids=str)
+@pytest.mark.parametrize("tokens,top,experts,n,out", [(300, 4, 2000, 128, 70), (40, 2, 1025, 384, 40),
+                                                     (4000, 2, 5, 128, 2500), (3000, 1, 1, 640, 1900)])
+def test_many_experts_and_tiles(tokens, top, experts, n, out, path):
+    """More experts than a table in shared memory holds; more tiles than workgroups, behind an index."""
+    announce(f"mxfp4 experts {tokens}x{top} of {experts} {n} -> {out} {path}")
+    kq = _kq()
+    rng = np.random.default_rng(tokens)
+    index, offsets = _sorted_slots(rng, tokens, top, experts, 1.0)
+    index = rng.permutation(tokens).astype(np.int32) if top == 1 else index
+    x, xs = _random_codes(tokens, n)
+    w, ws = _random_codes(out, n, experts)
+    y = _empty((tokens * top, out), "f32")
+    with _forced(path):
+        kq.kq_mxfp4_experts(x, _dev(index), _dev(offsets), w, ws, y, x_scales=xs, n=n)
+    xq = _values(x, xs, np.arange(tokens))
+    for e in np.flatnonzero(np.diff(offsets)):
+        lo, hi = offsets[e], offsets[e + 1]
+        _close(y[lo:hi], xq[index[lo:hi]], _values(w[e], ws[e], np.arange(out)), False)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,n,had", [(1, 4096, 4096), (1, 640, 128), (3, 8192, 8192), (40, 1536, 512), (1, 100, 4),
+                                        (2, 7, 1)])
+def test_operands_at_any_element(rows, n, had, kind):
+    """Rows, factors and signs that begin anywhere, rows any distance apart: the same bits."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(n)
+    x = _rows(rng, rows, n, kind).cuda()
+    d, sg = _processing(rng, n, True, True)
+    wc, ws, _ = _layer(rng, 50, n)
+    want = (*_quantize(x, d, sg, had), _empty((rows, 50), "f32"))
+    kq.kq_mxfp4_linear(x, wc, ws, want[3], d=_dev(d), sign=_dev(sg), had=had)
+    for off, pad in ((1, 1), (2, 0), (3, 4), (8, 3)):
+        wide = torch.full((rows, off + n + pad), float("nan"), dtype=x.dtype, device="cuda")
+        wide[:, off:off + n] = x
+        moved_d = torch.cat([torch.full((off,), float("nan")), torch.from_numpy(d)]).cuda()[off:]
+        moved_s = torch.cat([torch.zeros(off, dtype=torch.int8), torch.from_numpy(sg)]).cuda()[off:]
+        codes, scales = kq.kq_mxfp4_empty(rows, n)
+        values = torch.full((rows, off + n + pad), 7.0, dtype=torch.bfloat16, device="cuda")
+        kq.kq_mxfp4_quantize(wide[:, off:off + n], codes, scales, d=moved_d, sign=moved_s, had=had,
+                             values=values[:, off:off + n])
+        code, scale = om.mx_unpack(codes.cpu().numpy(), scales.cpu().numpy())
+        assert np.array_equal(code, want[0]) and np.array_equal(scale, want[1])
+        assert np.array_equal(values[:, off:off + n].float().cpu().numpy(), want[2])
+        assert bool((values[:, :off] == 7).all()) and bool((values[:, off + n:] == 7).all())
+        y = _empty((rows, 50), "f32")
+        kq.kq_mxfp4_linear(wide[:, off:off + n], wc, ws, y, d=moved_d, sign=moved_s, had=had)
+        assert torch.equal(y, want[3])
