@@ -56,7 +56,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
     float s;
     bool bad;
     int four;
-    const u32x2 w = encode(r, s, bad, four);
+    const u32x2 w = encode<exact_shift(LOGH)>(r, s, bad, four);
     if (c < 2 * a.pitch && u0 + wave / S < units) {
       *(u32x2*)(codes + k * a.pitch + c / 2) = w;
       if ((lane & 7) == 0) scales[k * a.steps + (c >> 7)] = four;

@@ -66,7 +66,7 @@ __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quanti
     float s;
     bool bad;
     int four;
-    const u32x2 w = encode(r, s, bad, four);
+    const u32x2 w = encode<exact_shift(LOGH)>(r, s, bad, four);
     if (live) {
       *(u32x2*)codes = w;
       if ((lane & 7) == 0) *(int*)scales = four;
@@ -101,10 +101,11 @@ kq_status launch(QuantArgs a, hipStream_t s) {
   constexpr bool LONG = LOGH > 10;
   constexpr int WAVES = LONG ? 1 << (LOGH > 10 ? LOGH - 10 : 0) : 4, COLS = LONG ? SPAN * WAVES : SPAN;
   a.chunks = (int)ceil_div(mx_pad(a.n), COLS);
-  // rows per unit (a wave, or a workgroup of a long block): enough to share the factors sign / d,
-  // as long as there are four waves per SIMD
-  const int64_t places = (int64_t)device_cu_count() * 16 / (LONG ? WAVES : 1);
-  a.run = (int)std::max<int64_t>(1, std::min<int64_t>(16, a.rows * a.chunks / places));
+  // rows per unit (a wave, or a workgroup of a long block): all units on the card at once, so that
+  // none is left over and the factors sign / d are computed once (16384 x 8192, one block a row:
+  // 123 us; 16 rows per unit, a round and a third: 130)
+  constexpr int RESIDENT = 4 * (WIDE && sizeof(T) == 2 ? 6 : 5);   // waves per compute unit, by registers
+  a.run = (int)ceil_div(a.rows * a.chunks, (int64_t)device_cu_count() * RESIDENT / (LONG ? WAVES : 1));
   const int64_t units = ceil_div(a.rows, a.run) * a.chunks, grid = LONG ? units : ceil_div(units, 4);
   if (units > 0x7fffffff)
     return fail(KQ_ESHAPE, "MXFP4 quantisation: %lld rows of %lld values", (long long)a.rows, (long long)a.n);

@@ -110,23 +110,24 @@ __host__ __device__ inline bool whole_factors(const float* d, const int8_t* sign
   return (((uintptr_t)d | (uintptr_t)sign) & 15) == 0 && n % 16 == 0;
 }
 
-// Butterfly between lanes a power of two apart, `v` with its partner's value: the lower lane gets
-// the sum, the upper one the partner's value minus its own (DPP: a lane move inside an add).
+// The value of another lane (DPP: the move is part of the add that takes it).
 template <int CTRL>
 __device__ __forceinline__ float moved(float v) {
   return __uint_as_float(__builtin_amdgcn_mov_dpp((int)__float_as_uint(v), CTRL, 0xf, 0xf, true));
 }
-template <int CTRL>
-__device__ __forceinline__ float across(float v, unsigned up) {   // up: the sign bit on upper lanes
-  return moved<CTRL>(v) + __uint_as_float(__float_as_uint(v) ^ up);
+// Holds sixteen values at this point of the program.
+__device__ __forceinline__ void pin(float (&r)[16]) {
+  asm volatile("" : "+v"(r[0]), "+v"(r[1]), "+v"(r[2]), "+v"(r[3]), "+v"(r[4]), "+v"(r[5]), "+v"(r[6]), "+v"(r[7]),
+                    "+v"(r[8]), "+v"(r[9]), "+v"(r[10]), "+v"(r[11]), "+v"(r[12]), "+v"(r[13]), "+v"(r[14]), "+v"(r[15]));
 }
 
-// Butterflies of strides 1 .. 512 below the rotation block, 2^LOGH columns (LOGH < 0: `had`).
+// Butterflies of strides 1 .. 512 below the rotation block, 2^LOGH columns (LOGH < 0: `had`); of a
+// block of S waves those below 64 S.
 template <int LOGH>
 __device__ __forceinline__ void span_stages(float (&r)[16], int had) {
   constexpr int XOR1 = 0xb1, XOR2 = 0x4e, XOR3 = 0x1b, HALF_MIRROR = 0x141, ROR8 = 0x128;
   const int lane = threadIdx.x & 63;
-  auto on = [&](int h) { return LOGH < 0 ? had > h : 1 << (LOGH < 0 ? 0 : LOGH) > h; };
+  auto on = [&](int h) { return LOGH < 0 ? had > h : (LOGH > 10 ? 64 << (LOGH - 10) : 1 << (LOGH < 0 ? 0 : LOGH)) > h; };
   auto up = [&](int bit) { return (unsigned)(lane & bit) << (31 - __builtin_ctz(bit)); };
 #pragma unroll
   for (int h = 1; h < 16; h <<= 1)
@@ -139,28 +140,42 @@ __device__ __forceinline__ void span_stages(float (&r)[16], int had) {
           r[k | h] = u - v;
         }
     }
-  if (on(16)) {
-    const unsigned u = up(1);
+  // Between lanes: the values with the upper lanes' signs turned, then each partner's added.  A lane
+  // move waits for the instruction before it, so that each step is done for all sixteen.
+  float x[16];
+  auto turned = [&](int bit) {
+    const unsigned u = up(bit);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r[k] = across<XOR1>(r[k], u);
+    for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(__float_as_uint(r[k]) ^ u);
+    pin(x);
+  };
+  if (on(16)) {
+    pin(r);
+    turned(1);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = moved<XOR1>(r[k]) + x[k];
+    pin(r);
   }
   if (on(32)) {
-    const unsigned u = up(2);
+    turned(2);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r[k] = across<XOR2>(r[k], u);
+    for (int k = 0; k < 16; ++k) r[k] = moved<XOR2>(r[k]) + x[k];
+    pin(r);
   }
   if (on(64)) {   // lane xor 4 = (xor 7) xor 3
-    const unsigned u = up(4);
+    turned(4);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) {
-      const float m = moved<HALF_MIRROR>(r[k]);
-      r[k] = moved<XOR3>(m) + __uint_as_float(__float_as_uint(r[k]) ^ u);
-    }
+    for (int k = 0; k < 16; ++k) r[k] = moved<HALF_MIRROR>(r[k]);
+    pin(r);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = moved<XOR3>(r[k]) + x[k];
+    pin(r);
   }
   if (on(128)) {
-    const unsigned u = up(8);
+    turned(8);
 #pragma unroll
-    for (int k = 0; k < 16; ++k) r[k] = across<ROR8>(r[k], u);
+    for (int k = 0; k < 16; ++k) r[k] = moved<ROR8>(r[k]) + x[k];
+    pin(r);
   }
   // Two values at a time: the exchange gives a lane both ends of one value's butterfly, a second
   // one hands the results back.
@@ -190,39 +205,33 @@ __device__ __forceinline__ void span_stages(float (&r)[16], int had) {
 constexpr int plane_floats(int waves) { return 4 * 64 * waves + 16; }
 constexpr int rotate_floats(int waves) { return 4 * plane_floats(waves); }
 
-// Butterflies of strides 1024 .. 512 S of a block of S waves (the workgroup holds WAVES / S
-// blocks), through LDS: the lanes' columns are written side by side, read 1024 apart, and written
-// back.  The four quarters of each lane's sixteen lie in planes of their own, a quarter of the
-// banks apart, so that neither access conflicts.
+// Butterflies of strides 64 S .. 512 S of a block of S waves (the workgroup holds WAVES / S
+// blocks), through LDS: the lanes' columns are written side by side, read back sixteen that are
+// 64 S apart, and written again.  The four quarters of each lane's sixteen lie in planes of their
+// own, a quarter of the banks apart, so that neither access conflicts.
 template <int WAVES, int S>
 __device__ __forceinline__ void wave_stages(float (&r)[16], float* v) {
-  constexpr int PLANE = plane_floats(WAVES), P = 16 / S;
-  const int t = threadIdx.x, base = t / (64 * S) * (SPAN * S), col = t % (64 * S);
+  constexpr int PLANE = plane_floats(WAVES);
+  const int t = threadIdx.x, base = t / (64 * S) * (SPAN * S) + t % (64 * S);
   auto at = [](int i) { return ((i >> 2) & 3) * PLANE + (i >> 4) * 4 + (i & 3); };
   __syncthreads();   // the row before has been read back
 #pragma unroll
   for (int k = 0; k < 4; ++k) *(float4*)(v + k * PLANE + 4 * t) = make_float4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
   __syncthreads();
-  float u[P][S];
+  float u[16];
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+  for (int p = 0; p < 16; ++p) u[p] = v[at(base + 64 * S * p)];
 #pragma unroll
-    for (int j = 0; j < S; ++j) u[p][j] = v[at(base + SPAN * j + col + 64 * S * p)];
+  for (int h = 1; h < 16; h <<= 1)
 #pragma unroll
-  for (int h = 1; h < S; h <<= 1)
+    for (int p = 0; p < 16; ++p)
+      if ((p & h) == 0) {
+        const float a = u[p], b = u[p | h];
+        u[p] = a + b;
+        u[p | h] = a - b;
+      }
 #pragma unroll
-    for (int p = 0; p < P; ++p)
-#pragma unroll
-      for (int j = 0; j < S; ++j)
-        if ((j & h) == 0) {
-          const float a = u[p][j], b = u[p][j | h];
-          u[p][j] = a + b;
-          u[p][j | h] = a - b;
-        }
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int j = 0; j < S; ++j) v[at(base + SPAN * j + col + 64 * S * p)] = u[p][j];
+  for (int p = 0; p < 16; ++p) v[at(base + 64 * S * p)] = u[p];
   __syncthreads();
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
@@ -231,7 +240,11 @@ __device__ __forceinline__ void wave_stages(float (&r)[16], float* v) {
   }
 }
 
-// The whole rotation of the lane's columns: factors, butterflies, 1 / sqrt(had).
+// Where 1 / sqrt(had) is 2^-k, the power k that `encode` takes off the exponents instead.
+constexpr int exact_shift(int logh) { return logh > 0 && logh % 2 == 0 ? logh / 2 : 0; }
+
+// The whole rotation of the lane's columns: factors, butterflies, and 1 / sqrt(had) unless encode
+// has it.
 template <int WAVES, int LOGH>
 __device__ __forceinline__ void rotate(float (&r)[16], bool scaled, const float (&f)[16], int had, float isb, float* lds) {
   if (scaled) {
@@ -240,32 +253,52 @@ __device__ __forceinline__ void rotate(float (&r)[16], bool scaled, const float 
   }
   span_stages<LOGH>(r, had);
   if constexpr (LOGH > 10) wave_stages<WAVES, 1 << (LOGH - 10)>(r, lds);
-  if (LOGH > 0 || (LOGH < 0 && had > 1)) {
+  if (LOGH >= 0 ? LOGH % 2 == 1 : had > 1) {
 #pragma unroll
     for (int k = 0; k < 16; ++k) r[k] *= isb;
   }
 }
 
-// The lane's sixteen codes, column c in the lowest nibble.  Two neighbouring lanes make a block:
-// its scale (a NaN or infinity in it: 2^127, `bad`, codes zero); `four`: the scale bytes of the
-// 128 columns that the lane's group of 8 lanes holds.
-__device__ __forceinline__ u32x2 encode(const float (&r)[16], float& scale, bool& bad, int& four) {
-  const int lane = threadIdx.x & 63;
-  unsigned top = 0;
+// The largest magnitude (bits; of an infinity or NaN at least 0x7f800000) of the block of 32 that
+// the lane and its neighbour hold.
+__device__ __forceinline__ unsigned block_top(const float (&r)[16]) {
+  float top = __builtin_fabsf(r[0]);
 #pragma unroll
-  for (int k = 0; k < 16; ++k) top = max(top, __float_as_uint(r[k]) & 0x7fffffffu);
-  top = max(top, (unsigned)__builtin_amdgcn_mov_dpp((int)top, 0xb1, 0xf, 0xf, true));
+  for (int k = 1; k < 16; ++k) top = __builtin_elementwise_maximum(top, __builtin_fabsf(r[k]));   // NaN wins
+  const unsigned b = __float_as_uint(top) & 0x7fffffffu;
+  return max(b, (unsigned)__builtin_amdgcn_mov_dpp((int)b, 0xb1, 0xf, 0xf, true));
+}
+
+// The lane's sixteen codes, column c in the lowest nibble, of r 2^-SHIFT.  Two neighbouring lanes
+// make a block: its scale (a NaN or infinity in it: 2^127, `bad`, codes zero); `four`: the scale
+// bytes of the 128 columns that the lane's group of 8 lanes holds.
+// A product with 2^-SHIFT is exact, and so is a conversion with the scale that much larger, unless
+// the product is subnormal; it is rounded then, so it is computed where a block's largest value
+// comes near that (its scale byte would be under 3: above, every subnormal rounds to zero).
+template <int SHIFT>
+__device__ __forceinline__ u32x2 encode(float (&r)[16], float& scale, bool& bad, int& four) {
+  const int lane = threadIdx.x & 63;
+  unsigned top = block_top(r);
+  int shift = SHIFT;
+  if (SHIFT > 0 && __any(top - 1 < ((SHIFT + 5u) << 23) - 1)) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] *= __uint_as_float((127u - SHIFT) << 23);
+    top = block_top(r);
+    shift = 0;
+  }
   const int ex = (int)(top >> 23);
   bad = ex == 255;
-  const int byte = bad ? 255 : max(ex - 2, 0);          // e + 127
-  scale = __uint_as_float(byte > 0 ? (unsigned)min(byte, 254) << 23 : 0x00400000u);
+  const int byte = bad ? 255 : max(ex - 2 - shift, 0);          // e + 127
+  auto power = [](int b) { return __uint_as_float(b > 0 ? (unsigned)min(b, 254) << 23 : 0x00400000u); };
+  scale = power(byte);
+  const float over = power(byte + shift);
   u32x2 w = {0, 0};
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k], r[8 * k + 1], scale, 0);
-    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 2], r[8 * k + 3], scale, 1);
-    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 4], r[8 * k + 5], scale, 2);
-    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 6], r[8 * k + 7], scale, 3);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k], r[8 * k + 1], over, 0);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 2], r[8 * k + 3], over, 1);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 4], r[8 * k + 5], over, 2);
+    w[k] = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w[k], r[8 * k + 6], r[8 * k + 7], over, 3);
     w[k] = bad ? 0 : w[k];
   }
   four = byte << (4 * (lane & 6));

@@ -665,3 +665,24 @@ def test_operands_at_any_element(rows, n, had, kind):
         y = _empty((rows, 50), "f32")
         kq.kq_mxfp4_linear(wide[:, off:off + n], wc, ws, y, d=moved_d, sign=moved_s, had=had)
         assert torch.equal(y, want[3])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+@pytest.mark.parametrize("n,had", [(1024, 4), (512, 8), (512, 16), (512, 64), (768, 256), (1024, 1024), (2048, 2048),
+                                   (4096, 4096)])
+def test_quantize_near_the_smallest_numbers(n, had, kind):
+    """Rows of every magnitude from the smallest subnormal on, and rows with blocks of all of them:
+    the products with 1 / sqrt(had) are rounded where they are subnormal, as defined."""
+    announce(f"mxfp4 quantize tiny {n} block {had} {kind}")
+    torch = torch_cuda()
+    rng = np.random.default_rng(had)
+    power = np.arange(-149, -100)
+    x = np.ldexp(rng.standard_normal((len(power) + 6, n)), np.concatenate([power, [0] * 6])[:, None])
+    x[-6:] = np.ldexp(x[-6:], np.repeat(rng.integers(-150, -60, (6, n // 32)), 32, axis=1))
+    x = torch.from_numpy(x.astype(np.float32))
+    x = x.to(torch.bfloat16) if kind == "bf16" else x
+    for d, sg in ((None, None), _processing(rng, n, True, True)):
+        code, scale, values = _quantize(x.cuda(), d, sg, had)
+        c, s = om.mx_encode(om.mx_rotate_f32(x.float().numpy(), d, sg, had))
+        assert np.array_equal(scale, s) and np.array_equal(code, c)
+        assert np.array_equal(values, om.mx_values(c, s, n).astype(np.float32))
