@@ -23,7 +23,7 @@ struct QuantArgs {
   uint16_t* values;        // or NULL
   int64_t ldv;
   int chunks;              // workgroups that share a row
-  int run;                 // consecutive rows per workgroup
+  int step;                // rows from one that a unit takes to its next
   bool v_wide;             // rows of values are 16-byte aligned
   bool whole;              // whole_factors
 };
@@ -41,8 +41,8 @@ __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quanti
   // the wave's, or workgroup's, columns and rows
   const unsigned unit = LONG ? blockIdx.x : blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t kp = mx_pad(a.n), c = (int64_t)(unit % a.chunks) * COLS + 16 * (LONG ? (int)threadIdx.x : lane);
-  const int64_t r0 = (int64_t)(unit / a.chunks) * a.run, r1 = min(r0 + a.run, a.rows);
-  if (r0 >= r1) return;
+  const int64_t r0 = unit / a.chunks;
+  if (r0 >= a.rows) return;
   const bool live = c < kp, scaled = a.d || a.sign;
   float f[16];
   if (scaled) {
@@ -57,10 +57,11 @@ __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quanti
   uint8_t* codes = a.codes + r0 * (kp / 2) + c / 2;
   uint8_t* scales = a.scales + ((c >> 7) * a.rows + r0) * 4;
   uint16_t* values = a.values + r0 * a.ldv + c;
-  for (int64_t row = r0; row < r1; ++row) {
+  const int64_t step_x = a.step * a.ld, step_codes = a.step * (kp / 2), step_values = a.step * a.ldv;
+  for (int64_t row = r0; row < a.rows; row += a.step) {
     float r[16];
     convert(next, r);
-    x += row + 1 < r1 ? a.ld : 0;   // (the last row once more rather than a branch)
+    x += row + a.step < a.rows ? step_x : 0;   // (the last row once more rather than a branch)
     load_columns<WIDE>(x, c, a.n, next);
     rotate<WAVES, LOGH>(r, scaled, f, a.had, a.isb, lds);
     float s;
@@ -90,9 +91,9 @@ __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quanti
         }
       }
     }
-    codes += kp / 2;
-    scales += 4;
-    values += a.ldv;
+    codes += step_codes;
+    scales += 4 * (int64_t)a.step;
+    values += step_values;
   }
 }
 
@@ -105,8 +106,9 @@ kq_status launch(QuantArgs a, hipStream_t s) {
   // none is left over and the factors sign / d are computed once (16384 x 8192, one block a row:
   // 123 us; 16 rows per unit, a round and a third: 130)
   constexpr int RESIDENT = 4 * (WIDE && sizeof(T) == 2 ? 6 : 5);   // waves per compute unit, by registers
-  a.run = (int)ceil_div(a.rows * a.chunks, (int64_t)device_cu_count() * RESIDENT / (LONG ? WAVES : 1));
-  const int64_t units = ceil_div(a.rows, a.run) * a.chunks, grid = LONG ? units : ceil_div(units, 4);
+  const int64_t run = ceil_div(a.rows * a.chunks, (int64_t)device_cu_count() * RESIDENT / (LONG ? WAVES : 1));
+  a.step = (int)ceil_div(a.rows, run);
+  const int64_t units = a.step * (int64_t)a.chunks, grid = LONG ? units : ceil_div(units, 4);
   if (units > 0x7fffffff)
     return fail(KQ_ESHAPE, "MXFP4 quantisation: %lld rows of %lld values", (long long)a.rows, (long long)a.n);
   mx_quantize_kernel<T, LOGH, WIDE><<<dim3((unsigned)grid), dim3(64 * WAVES), 0, s>>>(a);
