@@ -686,3 +686,29 @@ def test_quantize_near_the_smallest_numbers(n, had, kind):
         c, s = om.mx_encode(om.mx_rotate_f32(x.float().numpy(), d, sg, had))
         assert np.array_equal(scale, s) and np.array_equal(code, c)
         assert np.array_equal(values, om.mx_values(c, s, n).astype(np.float32))
+
+
+@pytest.mark.parametrize("tokens", [1, 150])
+def test_mixture_example(tokens):
+    """The example's block against its products done one by one in 64 bits on the values that the
+    codes stand for, and against fp32: the processing has to help where channels are large."""
+    torch = torch_cuda()
+    import examples.mxfp4_mixture as ex
+    torch.manual_seed(tokens)
+    x, *weights = ex.make(256 + tokens, 512, 320, 6, seed=tokens)
+    calibration, x = x[:256], x[256:]
+    want = ex.plain(x, *weights, 2)
+    error = {}
+    for processed in (False, True):
+        block = ex.Mixture(*weights, 2, calibration, processed)
+        index, offsets, weight = ex.route(x, weights[3], 2)
+        got = block.up.experts(x, index, offsets)
+        layers = block.up
+        host = lambda v: None if v is None else v.cpu().numpy()  # noqa: E731
+        xq = om.mx_round(om.mx_rotate_f32(x.float().cpu().numpy(), host(layers.d), host(layers.sign), layers.had))
+        w = np.stack([_values(layers.codes[e], layers.scales[e], np.arange(layers.out)) for e in range(6)])
+        ref, mag = _experts_ref(xq, host(index), host(offsets), w, 2 * tokens, tokens)
+        _experts_check(got, ref, mag, 512, True)
+        error[processed] = float((block(x) - want).norm() / want.norm())
+    # four-bit elements are off by up to 1/4 of themselves: 0.1 or so of a product of two of them
+    assert error[True] < 0.25 and error[True] < 0.75 * error[False], error
