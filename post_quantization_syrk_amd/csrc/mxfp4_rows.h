@@ -20,36 +20,30 @@ struct Raw {
   u32x4 v[sizeof(T)];   // 16 columns: two words of bf16, four of fp32
 };
 
-// The lane's columns c .. c + 15 of a row of n values, zero past its end, without a branch around
-// the loads (where paths join the compiler waits for all of them).  WIDE: 16 bytes at a time, of a
-// row that starts 16-byte aligned and ends with a whole dword (wide_rows).
+// The lane's columns c .. c + 15 of a row of n values, zero past its end: the descriptor ends with
+// the row (at most 2^26 bytes).  WIDE: 16 bytes at a time, of a row that starts 16-byte aligned and
+// ends with a whole dword (wide_rows).
 template <bool WIDE>
 __device__ __forceinline__ void load_columns(const float* row, int64_t c, int64_t n, Raw<float>& r) {
+  const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(4 * n));
   if constexpr (WIDE) {
-    // the descriptor ends with the row: n * 4 <= 2^26 bytes
-    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(4 * n));
 #pragma unroll
     for (int k = 0; k < 4; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(4 * c) + 16 * k, 0, 0);
   } else {
-    unsigned v[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(row[min(c + k, n - 1)]);
-#pragma unroll
-    for (int k = 0; k < 16; ++k) r.v[k >> 2][k & 3] = c + k < n ? v[k] : 0;
+    for (int k = 0; k < 16; ++k) r.v[k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(4 * c) + 4 * k, 0, 0);
   }
 }
 template <bool WIDE>
 __device__ __forceinline__ void load_columns(const uint16_t* row, int64_t c, int64_t n, Raw<uint16_t>& r) {
+  const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(2 * n));
   if constexpr (WIDE) {
-    const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(2 * n));
 #pragma unroll
     for (int k = 0; k < 2; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(2 * c) + 16 * k, 0, 0);
   } else {
     unsigned v[16];
 #pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = row[min(c + k, n - 1)];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = c + k < n ? v[k] : 0;
+    for (int k = 0; k < 16; ++k) v[k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * c) + 2 * k, 0, 0);
 #pragma unroll
     for (int k = 0; k < 8; ++k) r.v[k >> 2][k & 3] = v[2 * k] | v[2 * k + 1] << 16;
   }
@@ -73,41 +67,40 @@ inline bool wide_rows(const MxRows& r) {
 }
 
 // The lane's factors sign / d of columns c .. c + 15, 1 past the last one.  WHOLE: d and the signs
-// are 16-byte aligned and n is a multiple of 16 (whole_factors), so that a lane takes 16 bytes at a
+// are 16-byte aligned and n is a multiple of 4 (whole_factors), so that a lane takes 16 bytes at a
 // time (one column at a time, the lanes' loads are 64 bytes apart and cost more than a row's
 // rotation).
 template <bool WHOLE>
 __device__ __forceinline__ void factors(const float* d, const int8_t* sign, int64_t c, int64_t n, float (&f)[16]) {
+  const __amdgpu_buffer_rsrc_t rd = rsrc(d, d ? (int)(4 * n) : 0), rs = rsrc(sign, sign ? (int)n : 0);
   float dv[16];
   bool minus[16];
   if constexpr (WHOLE) {
-    const int64_t at = min(c, n - 16);
-    u32x4 s = {0, 0, 0, 0};
-    if (sign) s = *(const u32x4*)(sign + at);
+    const u32x4 s = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)c, 0, 0);
+    u32x4 v[4];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const float4 v = d ? *(const float4*)(d + at + 4 * k) : make_float4(1.f, 1.f, 1.f, 1.f);
-      dv[4 * k] = v.x; dv[4 * k + 1] = v.y; dv[4 * k + 2] = v.z; dv[4 * k + 3] = v.w;
+    for (int k = 0; k < 4; ++k) v[k] = __builtin_amdgcn_raw_buffer_load_b128(rd, (int)(4 * c) + 16 * k, 0, 0);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      dv[k] = __uint_as_float(v[k >> 2][k & 3]);
+      minus[k] = (s[k >> 2] >> (8 * (k & 3) + 7)) & 1;
     }
-#pragma unroll
-    for (int k = 0; k < 16; ++k) minus[k] = (s[k >> 2] >> (8 * (k & 3) + 7)) & 1;
   } else {
     int sv[16];
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const int64_t at = min(c + k, n - 1);
-      dv[k] = d ? d[at] : 1.f;
-      sv[k] = sign ? sign[at] : 1;
+      dv[k] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rd, (int)(4 * c) + 4 * k, 0, 0));
+      sv[k] = (int8_t)__builtin_amdgcn_raw_buffer_load_b8(rs, (int)c + k, 0, 0);
     }
 #pragma unroll
     for (int k = 0; k < 16; ++k) minus[k] = sv[k] < 0;
   }
 #pragma unroll
-  for (int k = 0; k < 16; ++k) f[k] = c + k < n ? __fdiv_rn(minus[k] ? -1.f : 1.f, dv[k]) : 1.f;
+  for (int k = 0; k < 16; ++k) f[k] = c + k < n ? __fdiv_rn(minus[k] ? -1.f : 1.f, d ? dv[k] : 1.f) : 1.f;
 }
 
 __host__ __device__ inline bool whole_factors(const float* d, const int8_t* sign, int64_t n) {
-  return (((uintptr_t)d | (uintptr_t)sign) & 15) == 0 && n % 16 == 0;
+  return (((uintptr_t)d | (uintptr_t)sign) & 15) == 0 && n % 4 == 0;
 }
 
 // The value of another lane (DPP: the move is part of the add that takes it).
