@@ -17,6 +17,8 @@
  *      H_X^-1, to packed 2/3/4-bit codes, minimizing tr(H_G dW H_X dW^T)
  *      (KronQ README, opening section and "Mapping paper results to flags");
  *   5. the per-sublayer bit allocation to an average bit budget.
+ * It also applies the layers that it has quantised: kq_deploy_linear for packed codes, one token
+ * at a time, and the kq_mxfp4_ calls for layers held in MXFP4, any number of tokens.
  *
  * Conventions for every entry point:
  *   - Matrix arguments are row-major with the stated leading dimension (in
