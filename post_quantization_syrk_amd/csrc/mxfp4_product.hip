@@ -146,6 +146,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   constexpr int SI = (BM + BN) / 64, SC = (SI + 2 * WC - 1) / (2 * WC);   // scale copies of 128 of K: all, per wave
   constexpr int COPIES = CA + CB + 2 * SC, SCALES = (BM + BN) * 4;
   constexpr int STAGE = PANELS + 2 * SCALES;
+  constexpr bool DEEP = MT * NT < 8;   // registers for the operands of all four quarters of a stage
   __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[STAGE];
   __shared__ ExpertTable tab[1];
@@ -270,9 +271,16 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   };
   auto read_scales = [&](const uint8_t* buf, int h, int (&sa)[MT], int (&sb)[NT]) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m) sa[m] = *(const int*)(buf + h * SCALES + sca + 4 * m) >> (8 * q);
+    for (int m = 0; m < MT; ++m) sa[m] = *(const int*)(buf + h * SCALES + sca + 4 * m);
 #pragma unroll
-    for (int n = 0; n < NT; ++n) sb[n] = *(const int*)(buf + h * SCALES + scb + 4 * n) >> (8 * q);
+    for (int n = 0; n < NT; ++n) sb[n] = *(const int*)(buf + h * SCALES + scb + 4 * n);
+  };
+  // The lane's bytes of them: where they are used, not where they are read, since that would wait.
+  auto own_bytes = [&](int (&sa)[MT], int (&sb)[NT]) {
+#pragma unroll
+    for (int m = 0; m < MT; ++m) sa[m] >>= 8 * q;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) sb[n] >>= 8 * q;
   };
   auto mma0 = [&](const i32x4 (&xa)[MT], const i32x4 (&xb)[NT], const int (&sa)[MT], const int (&sb)[NT]) {
 #pragma unroll
@@ -301,25 +309,31 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   lds_barrier();
   read(b0, 0, xa, xb);
   read_scales(b0, 0, sa, sb);
+  i32x4 za[MT], zb[NT], ua[MT], ub[NT];
+  if constexpr (DEEP) read(b0, 1, ya, yb);
 
 // Stage: read the operands of each quarter while multiplying the one before.  Ahead of the last
 // quarter, wait for this wave's copies of the next stage and for every wave's reads of this one;
-// then refill its buffer and read the next stage's first quarter.
+// then refill its buffer and read the next stage's first quarter.  DEEP: by halves, so that a read
+// has two quarters to arrive (2048 x 11008 x 4096, 128 x 128 tiles: 57 -> 55 us; the 256 x 256 tiles'
+// accumulators leave no room).
 #define KQ_MX_SPREAD(COUNT, GROUP)                          \
   _Pragma("unroll") for (int i_ = 0; i_ < (COUNT); ++i_) {  \
     __builtin_amdgcn_sched_group_barrier(0x008, 1, GROUP);  \
-    __builtin_amdgcn_sched_group_barrier(0x100, 1, GROUP);  \
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, GROUP);  \
   }                                                         \
   __builtin_amdgcn_sched_barrier(0);
 #define KQ_MX_STAGE(CUR, NXT, WAIT)                         \
   {                                                         \
+    own_bytes(sa, sb);                                      \
     read(CUR, 1, ya, yb);                                   \
-    read_scales(CUR, 1, ta, tb);                            \
     mma0(xa, xb, sa, sb);                                   \
-    KQ_MX_SPREAD(MT + NT + 2, 0)                            \
+    KQ_MX_SPREAD(MT + NT, 0)                                \
+    read_scales(CUR, 1, ta, tb);                            \
     read(CUR, 2, xa, xb);                                   \
     mma1(ya, yb, sa, sb);                                   \
-    KQ_MX_SPREAD(MT + NT, 0)                                \
+    KQ_MX_SPREAD(MT + NT + 2, 0)                            \
+    own_bytes(ta, tb);                                      \
     read(CUR, 3, ya, yb);                                   \
     mma0(xa, xb, ta, tb);                                   \
     KQ_MX_SPREAD(MT + NT, 0)                                \
@@ -327,13 +341,39 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);                 \
     lds_barrier();                                          \
     issue(CUR);                                             \
-    read(NXT, 0, xa, xb);                                   \
     read_scales(NXT, 0, sa, sb);                            \
+    read(NXT, 0, xa, xb);                                   \
     mma1(ya, yb, ta, tb);                                   \
     _Pragma("unroll") for (int i_ = 0; i_ < MT * NT; ++i_) { \
       __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);    \
       __builtin_amdgcn_sched_group_barrier(0x020, (COPIES + MT * NT - 1) / (MT * NT), 1); \
-      __builtin_amdgcn_sched_group_barrier(0x100, 1, 1);    \
+      __builtin_amdgcn_sched_group_barrier(0x100, 2, 1);    \
+    }                                                       \
+    __builtin_amdgcn_sched_barrier(0);                      \
+  }
+#define KQ_MX_DEEP_STAGE(CUR, NXT, WAIT)                    \
+  {                                                         \
+    own_bytes(sa, sb);                                      \
+    read_scales(CUR, 1, ta, tb);                            \
+    read(CUR, 2, za, zb);                                   \
+    read(CUR, 3, ua, ub);                                   \
+    mma0(xa, xb, sa, sb);                                   \
+    mma1(ya, yb, sa, sb);                                   \
+    KQ_MX_SPREAD(2 * (MT + NT) + 2, 0)                      \
+    WAIT;                                                   \
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);                 \
+    lds_barrier();                                          \
+    own_bytes(ta, tb);                                      \
+    issue(CUR);                                             \
+    read_scales(NXT, 0, sa, sb);                            \
+    read(NXT, 0, xa, xb);                                   \
+    read(NXT, 1, ya, yb);                                   \
+    mma0(za, zb, ta, tb);                                   \
+    mma1(ua, ub, ta, tb);                                   \
+    _Pragma("unroll") for (int i_ = 0; i_ < MT * NT; ++i_) { \
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);    \
+      __builtin_amdgcn_sched_group_barrier(0x020, (COPIES + MT * NT - 1) / (MT * NT), 1); \
+      __builtin_amdgcn_sched_group_barrier(0x100, 3, 1);    \
     }                                                       \
     __builtin_amdgcn_sched_barrier(0);                      \
   }
@@ -377,8 +417,13 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
         }
         aim_next();
       }
-      KQ_MX_STAGE(b0, b1, wait_stage(k))
-      KQ_MX_STAGE(b1, b0, wait_stage(1))
+      if constexpr (DEEP) {
+        KQ_MX_DEEP_STAGE(b0, b1, wait_stage(k))
+        KQ_MX_DEEP_STAGE(b1, b0, wait_stage(1))
+      } else {
+        KQ_MX_STAGE(b0, b1, wait_stage(k))
+        KQ_MX_STAGE(b1, b0, wait_stage(1))
+      }
     }
 
     // Lane l32 holds NT neighbouring columns of 16 MT rows.  The descriptor ends with the tile's
@@ -453,6 +498,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     t = nt;
   }
 #undef KQ_MX_STAGE
+#undef KQ_MX_DEEP_STAGE
 #undef KQ_MX_SPREAD
   // the ring's trailing copies must land before its LDS is released
   __builtin_amdgcn_s_waitcnt(wait_vm(0));
