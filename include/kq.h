@@ -474,7 +474,7 @@ enum {
  * kq_mxfp4_quantize -- rows to MXFP4, with the input side of the incoherence processing.
  *
  *   src        device, rows x n of src_type (KQ_F32 or KQ_BF16), leading dim ld >= n, aligned to
- *              its type (16-byte aligned rows are read faster)
+ *              its type (bf16: the dwords that hold a row's first and last column are read whole)
  *   codes, scales  device, as laid out above
  *   values_opt device bf16, rows x n (leading dim ldv >= n), or NULL: the values that the codes
  *              and scales stand for (exact in bf16)

@@ -34,8 +34,8 @@ enum {
   KQ_TESTING_ROW_LDS_BYTES = 2,
   /* Rows and columns of the MXFP4 products' tiles: 256, 128 or 64 (default: by their time). */
   KQ_TESTING_MX_TILE = 3,
-  /* Most rows (per expert, on average) that the MXFP4 products' few-row kernel takes (default 32
-   * or 16, by the size of the layer); 0: none. */
+  /* Most rows (per expert, on average) that the MXFP4 products' few-row kernel takes (default 16,
+   * 32 or all, by the number of 64 x 64 tiles that the product has); 0: none. */
   KQ_TESTING_MX_FEW = 4,
   /* Most activations (rows times columns, for experts slots times columns) that the few-row
    * kernel quantises itself (default 8192); 0: none. */

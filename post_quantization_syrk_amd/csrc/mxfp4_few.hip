@@ -47,7 +47,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
       else
         factors<false>(x.d, x.sign, c, x.n, f);
     }
-    convert(raw, r);
+    convert<WIDE>(raw, c, x.n, r);
     if (!in) {
 #pragma unroll
       for (int j = 0; j < 16; ++j) r[j] = 0.f;
@@ -247,12 +247,13 @@ int64_t even_tiles(const ProductArgs& p, int bm) {
 
 }  // namespace
 
-// Up to 16 rows, or 32, where 64 x 64 tiles would leave compute units idle, or half of them
-// (16 rows, 4096 x 4096: 4.5 us here, 7.7 in tiles; 11008 x 4096: 7.9 and 8.0; 28672 x 8192:
-// 21.8 and 20.3; 32 rows, 4096 x 4096: 5.4 and 7.8; 11008 x 4096: 9.6 and 8.1).
+// Where 64 x 64 tiles would leave three compute units of four idle; up to 32 rows where half of
+// them; up to 16 where any (64 rows, 4096 x 4096: 6.2 us here, 7.2 in tiles; 256 rows, 1024 x 4096: 6.2
+// and 7.2, 384 rows: 8.3 and 7.3; 512 rows, 256 x 9472: 9.9 and 12.3; 32 rows, 4096 x 4096: 5.0 and 7.2,
+// 11008 x 4096: 8.7 and 7.4; 16 rows, 11008 x 4096: 7.3 and 7.3; 28672 x 8192: 21.8 and 20.3).
 bool mx_few(const ProductArgs& p) {
-  const int64_t avg = average_rows(p), tiles = even_tiles(p, 64) * ceil_div(p.N, 64);
-  const int64_t rows = tiles < device_cu_count() / 2 ? 32 : tiles < device_cu_count() ? 16 : 0;
+  const int64_t avg = average_rows(p), tiles = even_tiles(p, 64) * ceil_div(p.N, 64), cus = device_cu_count();
+  const int64_t rows = 4 * tiles <= cus ? 65535 : 2 * tiles < cus ? 32 : tiles < cus ? 16 : 0;
   return avg <= testing_value(KQ_TESTING_MX_FEW, rows) && p.slots <= 65535 && p.rows * p.pitch < 0x7fffffff;
 }
 
@@ -275,8 +276,8 @@ kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, b
   if (fused) {
     const bool f32 = x.type == KQ_F32, wide = wide_rows(x);
 #define KQ_FEW(NT, U)                                                                               \
-  (wide ? (f32 ? launch<8, 1, NT, U, float, true>(p, r, s) : launch<8, 1, NT, U, uint16_t, true>(p, r, s))     \
-        : (f32 ? launch<8, 1, NT, U, float, false>(p, r, s) : launch<8, 1, NT, U, uint16_t, false>(p, r, s)))
+  (f32 ? launch<8, 1, NT, U, float, true>(p, r, s)                                                   \
+       : wide ? launch<8, 1, NT, U, uint16_t, true>(p, r, s) : launch<8, 1, NT, U, uint16_t, false>(p, r, s))
     return nt == 4 ? KQ_FEW(4, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
 #undef KQ_FEW
   }

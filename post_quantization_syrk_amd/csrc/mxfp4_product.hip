@@ -139,7 +139,7 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 // since four of 128 x 128, which read a third less from LDS, are 2 % slower.  2048 x 11008 x 4096 with
 // 128 x 128 tiles: 56 us, 3.3 PF, bound by the copies, 64 bytes per clock and compute unit at the
 // full rate; 256 x 256 tiles need half of that, and have half as many workgroups (71 us there).
-template <int MT, int NT, int WC, int ROWS>
+template <int MT, int NT, int WC, int RING, int ROWS>
 __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
   constexpr int CA = 4 * MT / WC, CB = 2 * NT;        // copies of x and of W per wave and stage
@@ -149,6 +149,8 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   constexpr bool DEEP = MT * NT < 8;   // registers for the operands of all four quarters of a stage
   __shared__ __attribute__((aligned(1024))) uint8_t b0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t b1[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t b2[RING == 4 ? STAGE : 1024];
+  __shared__ __attribute__((aligned(1024))) uint8_t b3[RING == 4 ? STAGE : 1024];
   __shared__ ExpertTable tab[1];
   __shared__ __attribute__((aligned(256))) int next_index[ROWS == X_ROWS ? 64 : BM];
   const int lane = threadIdx.x & 63;
@@ -305,7 +307,11 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   int sa[MT], sb[NT], ta[MT], tb[NT];
   issue(b0);
   issue(b1);
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  if constexpr (RING == 4) {
+    issue(b2);
+    issue(b3);
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm((RING - 1) * COPIES));
   lds_barrier();
   read(b0, 0, xa, xb);
   read_scales(b0, 0, sa, sb);
@@ -377,16 +383,17 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     }                                                       \
     __builtin_amdgcn_sched_barrier(0);                      \
   }
-  // Waits for the next stage's copies: nothing newer is outstanding but, in a tile's first stage
-  // (k = 0), the 16 MT stores of the tile before, which may stay so (the counter holds 63).  One
-  // block of instructions: a branch that the compiler sees would let it move the matrix
-  // instructions across.
-  constexpr int STORES = 16 * MT < 63 ? 16 * MT : 63;
-  auto wait_stage = [&](int k) {
-    asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(0)\n.Lstage%=:"
-                 :: "s"(k), "n"(STORES) : "scc", "memory");
+  // Waits for the next stage's copies.  Newer than they are those of RING - 2 stages and, in the
+  // first RING - 1 stages of a tile (`after`: there was one before), its 16 MT stores, which may stay
+  // outstanding (the counter holds 63).  One block of instructions: a branch that the compiler sees
+  // would let it move the matrix instructions across.
+  constexpr int NEWER = (RING - 2) * COPIES, STORES = NEWER + 16 * MT < 63 ? NEWER + 16 * MT : 63;
+  auto wait_stage = [&](bool after) {
+    asm volatile("s_waitcnt vmcnt(%1)\n\ts_cmp_lg_u32 %0, 0\n\ts_cbranch_scc1 .Lstage%=\n\ts_waitcnt vmcnt(%2)\n.Lstage%=:"
+                 :: "s"(__builtin_amdgcn_readfirstlane((int)after)), "n"(STORES), "n"(NEWER) : "scc", "memory");
   };
-  const int rounds = (stages + 1) / 2;   // of two stages: one past the end multiplies zeros
+  const int rounds = (stages + RING - 1) / RING;   // stages past the last multiply zeros
+  bool stored = false;
   const int size = a.y_bf16 ? 2 : 4;
 
   for (;;) {
@@ -417,14 +424,21 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
         }
         aim_next();
       }
-      if constexpr (DEEP) {
-        KQ_MX_DEEP_STAGE(b0, b1, wait_stage(k))
-        KQ_MX_DEEP_STAGE(b1, b0, wait_stage(1))
+      const bool after = k == 0 && stored;
+      if constexpr (RING == 4) {
+        KQ_MX_DEEP_STAGE(b0, b1, wait_stage(after))
+        KQ_MX_DEEP_STAGE(b1, b2, wait_stage(after))
+        KQ_MX_DEEP_STAGE(b2, b3, wait_stage(after))
+        KQ_MX_DEEP_STAGE(b3, b0, wait_stage(false))
+      } else if constexpr (DEEP) {
+        KQ_MX_DEEP_STAGE(b0, b1, wait_stage(after))
+        KQ_MX_DEEP_STAGE(b1, b0, wait_stage(false))
       } else {
-        KQ_MX_STAGE(b0, b1, wait_stage(k))
-        KQ_MX_STAGE(b1, b0, wait_stage(1))
+        KQ_MX_STAGE(b0, b1, wait_stage(after))
+        KQ_MX_STAGE(b1, b0, wait_stage(false))
       }
     }
+    stored = true;
 
     // Lane l32 holds NT neighbouring columns of 16 MT rows.  The descriptor ends with the tile's
     // last row, so stores of rows past it are dropped, and so are those of lanes whose columns
@@ -515,20 +529,20 @@ int64_t row_tiles(const ProductArgs& p, int bm) {
   return ceil_div(p.slots, bm) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
 }
 
-template <int MT, int NT, int WC>
+template <int MT, int NT, int WC, int RING>
 kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC;
   // one workgroup for each place on the card, or for each tile if there are fewer
-  constexpr int PLACES = 160 * 1024 / (2 * (BM + BN) * 136 + (1 << 13));
+  constexpr int PLACES = 160 * 1024 / (RING * (BM + BN) * 136 + (1 << 13));
   const int64_t total = std::min<int64_t>(ceil_div(row_tiles(p, BM) * ceil_div(p.N, BN), 8),
                                           ceil_div(device_cu_count() * std::min(PLACES, 4), 8)) * 8;
   const dim3 grid((unsigned)total), block(128 * WC);
   if (!p.offsets)
-    mx_tile_kernel<MT, NT, WC, X_ROWS><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_ROWS><<<grid, block, 0, s>>>(p);
   else if (!x_far(p))
-    mx_tile_kernel<MT, NT, WC, X_INDEX><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_INDEX><<<grid, block, 0, s>>>(p);
   else if constexpr (MT == 4)
-    mx_tile_kernel<MT, NT, WC, X_FAR><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_FAR><<<grid, block, 0, s>>>(p);
   KQ_LAUNCHED("mx_tile_kernel");
   return KQ_OK;
 }
@@ -557,9 +571,9 @@ kq_status launch_best(const ProductArgs& p, hipStream_t s) {
     }
   }
   switch (p.offsets && x_far(p) ? 256 : testing_value(KQ_TESTING_MX_TILE, best)) {
-    case 256: return launch_tiles<4, 2, 4>(p, s);
-    case 128: return launch_tiles<2, 2, 2>(p, s);
-    default: return launch_tiles<1, 1, 2>(p, s);
+    case 256: return launch_tiles<4, 2, 4, 2>(p, s);
+    case 128: return launch_tiles<2, 2, 2, 2>(p, s);
+    default: return launch_tiles<1, 1, 2, 4>(p, s);
   }
 }
 

@@ -64,7 +64,7 @@ __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quanti
   const int64_t step_x = a.step * a.ld, step_codes = a.step * (kp / 2), step_values = a.step * a.ldv;
   for (int64_t row = r0; row < a.rows; row += a.step) {
     float r[16];
-    convert(next, r);
+    convert<WIDE>(next, c, a.n, r);
     x += row + a.step < a.rows ? step_x : 0;   // (the last row once more rather than a branch)
     load_columns<WIDE>(x, c, a.n, next);
     rotate<WAVES, LOGH>(r, scaled, f, a.had, a.isb, lds);
@@ -120,11 +120,21 @@ kq_status launch(QuantArgs a, hipStream_t s) {
   return KQ_OK;
 }
 
-// The block is a constant of the kernel where rows are read 16 bytes at a time (as a variable, its
-// stages copy the sixteen values at every branch); other rows take one kernel up to SPAN.
+// The block is a constant of the kernel (as a variable, its stages copy the sixteen values at every
+// branch), but for bf16 rows that begin or end inside a dword with a short rotation, which is rare:
+// one kernel for those up to SPAN.
 template <typename T>
 kq_status launch_block(const QuantArgs& a, bool wide, hipStream_t s) {
-  switch (a.had > SPAN || wide ? __builtin_ctz(a.had) : -1) {
+  if constexpr (sizeof(T) == 2) {
+    if (!wide) switch (a.had > SPAN || a.had == 1 ? __builtin_ctz(a.had) : -1) {
+      case 0: return launch<T, 0, false>(a, s);
+      case 11: return launch<T, 11, false>(a, s);
+      case 12: return launch<T, 12, false>(a, s);
+      case 13: return launch<T, 13, false>(a, s);
+      default: return launch<T, -1, false>(a, s);
+    }
+  }
+  switch (__builtin_ctz(a.had)) {
     case 0: return launch<T, 0, true>(a, s);
     case 1: return launch<T, 1, true>(a, s);
     case 2: return launch<T, 2, true>(a, s);
@@ -136,10 +146,9 @@ kq_status launch_block(const QuantArgs& a, bool wide, hipStream_t s) {
     case 8: return launch<T, 8, true>(a, s);
     case 9: return launch<T, 9, true>(a, s);
     case 10: return launch<T, 10, true>(a, s);
-    case 11: return wide ? launch<T, 11, true>(a, s) : launch<T, 11, false>(a, s);
-    case 12: return wide ? launch<T, 12, true>(a, s) : launch<T, 12, false>(a, s);
-    case 13: return wide ? launch<T, 13, true>(a, s) : launch<T, 13, false>(a, s);
-    default: return launch<T, -1, false>(a, s);
+    case 11: return launch<T, 11, true>(a, s);
+    case 12: return launch<T, 12, true>(a, s);
+    default: return launch<T, 13, true>(a, s);
   }
 }
 

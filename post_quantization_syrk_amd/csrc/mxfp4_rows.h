@@ -18,52 +18,54 @@ constexpr int SPAN = 1024;       // columns that a wave holds: 16 neighbouring o
 template <typename T>
 struct Raw {
   u32x4 v[sizeof(T)];   // 16 columns: two words of bf16, four of fp32
+  unsigned more;        // and, of a bf16 row that starts or ends inside a dword, the next dword
+  int shift;            // and the bits of its first dword before the row
 };
 
 // The lane's columns c .. c + 15 of a row of n values, zero past its end: the descriptor ends with
-// the row (at most 2^26 bytes).  WIDE: 16 bytes at a time, of a row that starts 16-byte aligned and
-// ends with a whole dword (wide_rows).
+// the row (at most 2^26 bytes).  WIDE: the row begins and ends with a dword (wide_rows; all rows of
+// fp32).  Else the dwords that hold its first and last column are read whole and their other half
+// is dropped; read two bytes at a time, 8794 x 28243 took 480 us.
 template <bool WIDE>
 __device__ __forceinline__ void load_columns(const float* row, int64_t c, int64_t n, Raw<float>& r) {
   const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(4 * n));
-  if constexpr (WIDE) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(4 * c) + 16 * k, 0, 0);
-  } else {
-#pragma unroll
-    for (int k = 0; k < 16; ++k) r.v[k >> 2][k & 3] = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(4 * c) + 4 * k, 0, 0);
-  }
+  for (int k = 0; k < 4; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(4 * c) + 16 * k, 0, 0);
 }
 template <bool WIDE>
 __device__ __forceinline__ void load_columns(const uint16_t* row, int64_t c, int64_t n, Raw<uint16_t>& r) {
-  const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(2 * n));
-  if constexpr (WIDE) {
+  const int before = WIDE ? 0 : (int)((uintptr_t)row & 2);
+  const __amdgpu_buffer_rsrc_t rs = rsrc((const uint8_t*)row - before, WIDE ? (int)(2 * n) : (int)(before + 2 * n + 2) & ~3);
 #pragma unroll
-    for (int k = 0; k < 2; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(2 * c) + 16 * k, 0, 0);
-  } else {
-    unsigned v[16];
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v[k] = (uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, (int)(2 * c) + 2 * k, 0, 0);
-#pragma unroll
-    for (int k = 0; k < 8; ++k) r.v[k >> 2][k & 3] = v[2 * k] | v[2 * k + 1] << 16;
+  for (int k = 0; k < 2; ++k) r.v[k] = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)(2 * c) + 16 * k, 0, 0);
+  if (!WIDE) {
+    r.more = __builtin_amdgcn_raw_buffer_load_b32(rs, (int)(2 * c) + 32, 0, 0);
+    r.shift = 8 * before;
   }
 }
 
-__device__ __forceinline__ void convert(const Raw<float>& w, float (&r)[16]) {
+template <bool WIDE>
+__device__ __forceinline__ void convert(const Raw<float>& w, int64_t c, int64_t n, float (&r)[16]) {
 #pragma unroll
   for (int k = 0; k < 16; ++k) r[k] = __uint_as_float(w.v[k >> 2][k & 3]);
 }
-__device__ __forceinline__ void convert(const Raw<uint16_t>& w, float (&r)[16]) {
+template <bool WIDE>
+__device__ __forceinline__ void convert(const Raw<uint16_t>& w, int64_t c, int64_t n, float (&r)[16]) {
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const unsigned u = w.v[k >> 2][k & 3];
+    unsigned u = w.v[k >> 2][k & 3];
+    if (!WIDE) u = __builtin_amdgcn_alignbit(k < 7 ? w.v[(k + 1) >> 2][(k + 1) & 3] : w.more, u, w.shift);
     r[2 * k] = __uint_as_float(u << 16);
     r[2 * k + 1] = __uint_as_float(u & 0xffff0000u);
+  }
+  if (!WIDE) {
+#pragma unroll
+    for (int k = 0; k < 16; ++k) r[k] = c + k < n ? r[k] : 0.f;
   }
 }
 
 inline bool wide_rows(const MxRows& r) {
-  return aligned16(r.x) && (r.type == KQ_F32 ? r.ld % 4 == 0 : r.ld % 8 == 0 && r.n % 2 == 0);
+  return r.type == KQ_F32 || (((uintptr_t)r.x & 3) == 0 && r.ld % 2 == 0 && r.n % 2 == 0);
 }
 
 // The lane's factors sign / d of columns c .. c + 15, 1 past the last one.  WHOLE: d and the signs
