@@ -129,16 +129,17 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 }
 
 // Tiles of BM x BN outputs, 256 of K per stage, waves in 2 x WC, each with MT x NT accumulators
-// of 32 x 32, two stages in LDS.  A stage is 128 bytes of every row, a whole line: with 64, the
+// of 32 x 32.  A stage is 128 bytes of every row, a whole line: with 64, the
 // copies alone of an 8192 x 8192 x 8192 product took 170 us, with 128 107 us.  A workgroup takes
 // tile after tile; the copies of the next tile's first stages follow those of the last stages of
 // the present one, so the ring never runs dry and the stores of one tile go out while the next is
 // multiplied.
-// 16384 x 8192 x 28672: 1.79 ms, 4.3 PF, the matrix instructions busy 64 % of the time at 1.6 GHz
+// 16384 x 8192 x 28672: 1.78 ms, 4.3 PF, the matrix instructions busy 67 % of the time at 1.6 GHz
 // (alone, from registers, they are held to 1.56 GHz by power: 6.4 PF); eight waves of 128 x 64,
 // since four of 128 x 128, which read a third less from LDS, are 2 % slower.  2048 x 11008 x 4096 with
-// 128 x 128 tiles: 56 us, 3.3 PF, bound by the copies, 64 bytes per clock and compute unit at the
-// full rate; 256 x 256 tiles need half of that, and have half as many workgroups (71 us there).
+// 128 x 128 tiles: 55 us, 3.3 PF; with 256 x 256, on half as many workgroups, 71.
+// RING: stages in LDS; four where a tile is small (256 x 10496 x 2914: 14 us, with two and more
+// workgroups side by side 21).
 template <int MT, int NT, int WC, int RING, int ROWS>
 __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
