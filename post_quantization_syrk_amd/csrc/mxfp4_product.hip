@@ -550,7 +550,7 @@ kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
 
 // The tile with the least time.  Up to 64 rows (of an expert, on average) the layer's bytes are the
 // bound, and the smallest tiles put the most workgroups at them: 8 experts of 11008 x 4096 and a
-// token 14.2 us (64 x 128 tiles: 16.6), 64 of 2048 x 2048 and 96 tokens 19.6 (22.6).  With more
+// token 14.2 us (64 x 128 tiles: 16.6), 64 of 1408 x 2048 and 96 tokens 19.6 (22.6).  With more
 // rows, by a tile's time and the number of tiles that a compute unit gets: at K = 4096 and a full
 // card 33 us for 256 x 256, 9.4 for 128 x 128, 4.5 for 64 x 64 (4096 x 4096 outputs: 39, 42 and 66
 // in all; 2048 x 4096: 30, 24, 34; 256 x 4096: 24, 12, 8.6).  A smaller tile has to win clearly:
