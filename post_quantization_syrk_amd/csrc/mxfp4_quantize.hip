@@ -28,7 +28,7 @@ struct QuantArgs {
 };
 
 // Stores sixteen columns: whole dwords, and where they begin inside one its half and, at the end, the
-// other half (two bytes at a time, 10470 x 10810 took 322 us).
+// other half (10470 x 10810 bf16 with values: 136 us; two bytes at a time 322).
 __device__ __forceinline__ void store_columns(uint16_t* to, const u32x4 (&o)[2]) {
   struct __attribute__((packed, aligned(4))) Four { u32x4 v; };
   struct __attribute__((packed, aligned(4))) Three { unsigned v[3]; };

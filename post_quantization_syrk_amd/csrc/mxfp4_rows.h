@@ -25,7 +25,7 @@ struct Raw {
 // The lane's columns c .. c + 15 of a row of n values, zero past its end: the descriptor ends with
 // the row (at most 2^26 bytes).  WIDE: the row begins and ends with a dword (wide_rows; all rows of
 // fp32).  Else the dwords that hold its first and last column are read whole and their other half
-// is dropped; read two bytes at a time, 8794 x 28243 took 480 us.
+// is dropped (an 8794 x 28243 x with 384 output channels: 265 us; two bytes at a time 577).
 template <bool WIDE>
 __device__ __forceinline__ void load_columns(const float* row, int64_t c, int64_t n, Raw<float>& r) {
   const __amdgpu_buffer_rsrc_t rs = rsrc(row, (int)(4 * n));
