@@ -168,6 +168,17 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _workspace(nbytes: int, device, stream):
+    """Uninitialised device bytes for work on `stream` (None: the current one), from that stream's
+    own pool: whoever had them before, and whoever gets them next, is ordered on the same stream.
+    The caller holds them until the work has been enqueued."""
+    torch = _torch()
+    if stream is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+
+
 def _ld(t, name: str) -> int:
     if t.dim() != 2 or t.stride(1) != 1:
         raise ValueError(f"{name} must be a 2-D tensor with unit column stride")
@@ -533,8 +544,9 @@ def kq_mxfp4_workspace(rows: int, n: int) -> int:
     return b.value
 
 
-def _mx_rows(x, x_scales, d, sign, n, ws):
-    """(pointer, type, rows, n, ld, scales, d, sign, ws, ws bytes) of the activations."""
+def _mx_rows(x, x_scales, d, sign, n, ws, stream):
+    """(pointer, type, rows, n, ld, scales, d, sign, ws, ws bytes) of the activations, and the workspace
+    itself, which the caller holds until the call has returned."""
     if _mx_types is None:
         _mx_setup()
     if x_scales is not None:
@@ -543,21 +555,21 @@ def _mx_rows(x, x_scales, d, sign, n, ws):
         if d is not None or sign is not None:
             raise ValueError("quantised rows take no rescale and no signs")
         xp, sp = _mx_check(x, x_scales, (x.shape[0],), n, "x")
-        return xp, KQ_MXFP4, x.shape[0], n, kq_mxfp4_padded(n), sp, None, None, None, 0
+        return xp, KQ_MXFP4, x.shape[0], n, kq_mxfp4_padded(n), sp, None, None, None, 0, None
     xp, xt, rows, cols, ld = _mx_matrix(x, "x")
     if n is not None and n != cols:
         raise ValueError(f"x has {cols} columns, not {n}")
     if ws is None:
-        ws = _torch().empty(kq_mxfp4_workspace(rows, cols), dtype=_mx_u8, device=x.device)
+        ws = _workspace(kq_mxfp4_workspace(rows, cols), x.device, stream)
     return (xp, xt, rows, cols, ld, None, _mx_vector(d, "d", cols, _mx_f32), _mx_vector(sign, "sign", cols, _mx_i8),
-            _mx_ptr(ws, "ws", _mx_u8), ws.numel())
+            _mx_ptr(ws, "ws", _mx_u8), ws.numel(), ws)
 
 
 def kq_mxfp4_linear(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1, x_scales=None,
                     n=None, stream=None) -> None:
     """y = Q(P D^-1 x) W^T for a layer held in MXFP4: x fp32 or bf16 [rows, n] (or codes, with
     x_scales and n), y fp32 or bf16 [rows, out]."""
-    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb, ws = _mx_rows(x, x_scales, d, sign, n, ws, stream)
     out = w_codes.shape[0]
     cp, sp = _mx_check(w_codes, w_scales, (out,), n, "weight")
     yp, yt, yrows, ycols, ldy = _mx_matrix(y, "y")
@@ -574,7 +586,7 @@ def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, s
     """y[s] = Q(P D^-1 x[index[s]]) W_e^T for the slots s of expert e, [offsets[e], offsets[e + 1]):
     index int32 [slots] or None, offsets int32 [experts + 1], weights of kq_mxfp4_empty(out, n,
     experts), y fp32 or bf16 [slots, out].  Offsets and index stay on the device."""
-    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb = _mx_rows(x, x_scales, d, sign, n, ws)
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb, ws = _mx_rows(x, x_scales, d, sign, n, ws, stream)
     experts, out = w_codes.shape[0], w_codes.shape[1]
     cp, sp = _mx_check(w_codes, w_scales, (experts, out), n, "weight")
     yp, yt, slots, ycols, ldy = _mx_matrix(y, "y")

@@ -712,3 +712,40 @@ def test_mixture_example(tokens):
         error[processed] = float((block(x) - want).norm() / want.norm())
     # four-bit elements are off by up to 1/4 of themselves: 0.1 or so of a product of two of them
     assert error[True] < 0.25 and error[True] < 0.75 * error[False], error
+
+
+@pytest.mark.parametrize("rows", [64, 500])
+def test_default_workspaces_on_given_streams(rows):
+    """Calls on two streams of their own, with the workspaces that the binding allocates, while the
+    current stream allocates and fills blocks of the same size: the bits of a call by itself."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    n, out, experts = 2048, 300, 3
+    d, sg = (_dev(v) for v in _processing(rng, n, True, True))
+    wc, ws, _ = _layer(rng, out, n)
+    ec, es = _random_codes(96, n, experts)
+    index, offsets = (_dev(v) for v in _sorted_slots(rng, rows, 2, experts, 1.0))
+    inputs = [_rows(rng, rows, n, "bf16").cuda() for _ in range(8)]
+    size = kq.kq_mxfp4_workspace(rows, n)
+    want = []
+    for x in inputs:
+        work = torch.empty(size, dtype=torch.uint8, device="cuda")
+        y, z = _empty((rows, out), "f32"), _empty((2 * rows, 96), "bf16")
+        kq.kq_mxfp4_linear(x, wc, ws, y, work, d=d, sign=sg, had=n)
+        kq.kq_mxfp4_experts(x, index, offsets, ec, es, z, work, d=d, sign=sg, had=n)
+        want.append((y, z))
+    got = [(_empty((rows, out), "f32"), _empty((2 * rows, 96), "bf16")) for _ in inputs]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    filled = []
+    for k, x in enumerate(inputs):
+        y, z = got[k]
+        kq.kq_mxfp4_linear(x, wc, ws, y, d=d, sign=sg, had=n, stream=streams[k % 2])
+        filled.append(torch.full((size,), k, dtype=torch.uint8, device="cuda"))
+        kq.kq_mxfp4_experts(x, index, offsets, ec, es, z, d=d, sign=sg, had=n, stream=streams[k % 2])
+        torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    for (y, z), (a, b) in zip(got, want):
+        assert torch.equal(y, a) and torch.equal(z, b)
+    assert all(bool((f == k).all()) for k, f in enumerate(filled))
