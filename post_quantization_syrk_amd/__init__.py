@@ -398,7 +398,7 @@ def kq_flipflop(X, G, iters: int, A, B, ws=None, stream=None, phases: bool = Fal
     if G.shape[0] != T:
         raise ValueError("X and G need the same token count")
     if ws is None:
-        ws = torch.empty(kq_flipflop_workspace(T, n, m), dtype=torch.uint8, device=X.device)
+        ws = _workspace(kq_flipflop_workspace(T, n, m), X.device, stream)
     bf = (torch.int16, torch.uint16, torch.bfloat16)
     ph = (ctypes.c_double * 4)() if phases else None
     st = lib.kq_flipflop(_dev_ptr(X, "X", bf), _ld(X, "X"), _dev_ptr(G, "G", bf), _ld(G, "G"), T, n, m,
@@ -426,8 +426,7 @@ def kq_quantize_two_sided(p: QuantParams, W, HX, HG, packed, scales, zeros, ws=N
     lib = load_library()
     out_n, in_n = W.shape
     if ws is None:
-        ws = torch.empty(kq_quantize_two_sided_workspace(p, out_n, in_n), dtype=torch.uint8,
-                         device=W.device)
+        ws = _workspace(kq_quantize_two_sided_workspace(p, out_n, in_n), W.device, stream)
     f32 = (torch.float32,)
     st = lib.kq_quantize_two_sided(
         ctypes.byref(p), _dev_ptr(W, "W", f32), _dev_ptr(HX, "HX", f32), _dev_ptr(HG, "HG", f32),

@@ -107,3 +107,21 @@ def test_mxfp4_products_hold_their_workspace(watch, experts, stream):
     else:
         kq.kq_mxfp4_linear(x, codes, scales, y, stream=stream)
     _check(w, 1, stream)
+
+
+@pytest.mark.parametrize("stream", [None, STREAM], ids=["current", "given"])
+def test_flipflop_takes_its_workspace_from_its_stream(watch, stream):
+    w = watch("kq_flipflop")
+    x, g = on_device(256, 256, dtype=torch.bfloat16), on_device(256, 128, dtype=torch.bfloat16)
+    kq.kq_flipflop(x, g, 1, on_device(256, 256), on_device(128, 128), stream=stream)
+    _check(w, 1, stream)
+
+
+@pytest.mark.parametrize("stream", [None, STREAM], ids=["current", "given"])
+def test_two_sided_takes_its_workspace_from_its_stream(watch, stream):
+    w = watch("kq_quantize_two_sided")
+    params = kq.make_params(bits=4, group=128)
+    packed, scales, zeros = on_device(128, 16, dtype=torch.int32), on_device(128, 1), on_device(128, 1, dtype=torch.uint8)
+    kq.kq_quantize_two_sided(params, on_device(128, 128), on_device(128, 128), on_device(128, 128), packed, scales,
+                             zeros, stream=stream)
+    _check(w, 1, stream)
