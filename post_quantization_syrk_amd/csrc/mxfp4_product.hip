@@ -103,8 +103,13 @@ __device__ __forceinline__ void copy_lds(__amdgpu_buffer_rsrc_t r, unsigned off,
   else
     __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)to, 4, (int)off, 0, 0, 0);
 }
+template <int SIZE>
 __device__ __forceinline__ void copy_lds(const uint8_t* from, uint8_t* to) {
-  __builtin_amdgcn_global_load_lds((const void*)from, (__attribute__((address_space(3))) void*)to, 16, 0, 0);
+  typedef __attribute__((address_space(3))) void lds_void;
+  if constexpr (SIZE == 16)
+    __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)to, 16, 0, 0);
+  else
+    __builtin_amdgcn_global_load_lds((const void*)from, (lds_void*)to, 4, 0, 0);
 }
 
 // Stores W values side by side at byte offset `off` (a masked offset stores nothing).
@@ -177,7 +182,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   // descriptor and put zeros into LDS.
   constexpr unsigned ALL = 0xfffffff0u;
   const uint8_t *xc, *xs, *wc_e, *ws_e;
-  unsigned oa[CA], ob[CB], os[SC];
+  unsigned oa[CA], ob[CB], os[SC];   // (X_FAR: os holds rows)
   const uint8_t* pa[CA];   // X_FAR: x beyond the reach of a 32-bit offset
   int stepa[CA];
   int issued;
@@ -215,7 +220,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     for (int k = 0; k < SC; ++k) {
       const int si = min(wave * SC + k, SI - 1);
       const int64_t row = si < MT ? x_row(64 * si + ln) : w_row(64 * (si - MT) + ln);
-      os[k] = row >= 0 ? (unsigned)row * 4 : ALL;
+      os[k] = row >= 0 ? (unsigned)row * (ROWS == X_FAR ? 1 : 4) : ALL;
     }
   };
   const int stages = (a.steps + 1) / 2;
@@ -229,7 +234,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
       uint8_t* to = buf + (wave * CA + r) * 1024;
       const bool cut = half && (((lane & 7) ^ (((wave * CA + r) * 8 + (lane >> 3)) >> 1)) & 4);
       if (ROWS == X_FAR) {
-        copy_lds(live && !cut ? pa[r] : (const uint8_t*)g_zeros, to);
+        copy_lds<16>(live && !cut ? pa[r] : (const uint8_t*)g_zeros, to);
         pa[r] += stepa[r];
       } else {
         copy_lds<16>(ra, cut ? ALL : oa[r], to);
@@ -246,7 +251,11 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
       for (int k = 0; k < SC; ++k) {
         const int si = min(wave * SC + k, SI - 1);
         const uint8_t* from = si < MT ? xs + 4 * a.rows * h : ws_e + 4 * a.N * h;
-        copy_lds<4>(rsrc(from, h && half ? 0 : (int)ALL), os[k], buf + PANELS + h * SCALES + si * 256);
+        uint8_t* to = buf + PANELS + h * SCALES + si * 256;
+        if (ROWS == X_FAR)   // (four bytes of 2^30 rows: the last offsets would be the masked ones)
+          copy_lds<4>(os[k] != ALL && !(h && half) ? from + 4 * (uint64_t)os[k] : (const uint8_t*)g_zeros, to);
+        else
+          copy_lds<4>(rsrc(from, h && half ? 0 : (int)ALL), os[k], to);
       }
     // past the end the last stage's weights and scales are copied again, with zeros for x
     const int64_t on = ++issued < stages;

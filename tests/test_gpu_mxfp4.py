@@ -749,3 +749,31 @@ def test_default_workspaces_on_given_streams(rows):
     for (y, z), (a, b) in zip(got, want):
         assert torch.equal(y, a) and torch.equal(z, b)
     assert all(bool((f == k).all()) for k, f in enumerate(filled))
+
+
+def test_experts_of_the_most_rows():
+    """2^30 quantised rows, the most there may be, read through an index up to the last one."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(30)
+    rows, n, out, slots = 1 << 30, 128, 70, 300
+    codes, scales = kq.kq_mxfp4_empty(rows, n)       # 68 GiB, of which the rows below are filled
+    index = rng.integers(0, rows, slots).astype(np.int32)
+    index[:12] = rows - 1 - np.arange(12)
+    index[[20, 250]] = [-1, rows]
+    index[200:208] = rows - 1 - np.arange(8)
+    inside = (index >= 0) & (index < rows)
+    picked = torch.from_numpy(np.unique(index[inside])).long().cuda()
+    some, some_scales = _random_codes(len(picked), n)
+    codes[picked] = some
+    scales[:, picked] = some_scales
+    wc, ws, wv = _layer(rng, out, n, 2)
+    offsets = np.int32([0, 130, slots])
+    xq = np.zeros((slots, n))
+    xq[inside] = _values(codes, scales, index[inside])
+    want, mag = _experts_ref(xq, None, offsets, wv, slots, slots)
+    y = _empty((slots, out), "f32")
+    kq.kq_mxfp4_experts(codes, _dev(index), _dev(offsets), wc, ws, y, x_scales=scales, n=n)
+    _experts_check(y, want, mag, n, False)
+    del codes, scales
+    torch.cuda.empty_cache()
