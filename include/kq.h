@@ -521,8 +521,8 @@ kq_status kq_mxfp4_linear(const void* x, int x_type, int64_t rows, int64_t in, i
  *            a row of zeros.  NULL: slot s reads row s (slots <= rows)
  *   offsets  device int32 [experts + 1], non-decreasing, within [0, slots]: slots sorted by
  *            expert.  An expert may have none; slots before offsets[0] and from
- *            offsets[experts] on are not written.  Offsets that leave [0, slots] are cut to it;
- *            where they decrease, the slots between are unspecified
+ *            offsets[experts] on are not written.  Offsets that leave [0, slots] are cut to it,
+ *            and one below an earlier one counts as that one
  *   w_codes, w_scales  device: experts layers of out rows, one after another (codes
  *            [experts][out][np / 2], scales [experts][np / 128][out][4])
  *   y        device, slots x out

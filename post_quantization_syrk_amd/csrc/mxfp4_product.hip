@@ -24,12 +24,10 @@ template <int BM>
 __device__ __forceinline__ int count_tiles(const ProductArgs& a, ExpertTable& tab) {
   const int lane = threadIdx.x & 63;
   int tm = 0;
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    int c = 0, first = 0, last = 0;
-    if (e0 + lane < a.experts) {
-      expert_range(a, e0 + lane, first, last);
-      c = (last - first + BM - 1) / BM;
-    }
+  for (int e0 = 0, top = 0; e0 < a.experts; e0 += 64) {
+    int first, last;
+    expert_ranges(a, e0, top, first, last);
+    const int c = (last - first + BM - 1) / BM;
     int sum = c;   // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -58,7 +56,7 @@ __device__ __forceinline__ void find_rows(const ProductArgs& a, const ExpertTabl
     const int e = b + __popcll(__ballot(lane < 16 && tab.before[b + (lane & 15)] <= mt)) - 1;
     t.e = __builtin_amdgcn_readfirstlane(e);
     t.m0 = __builtin_amdgcn_readfirstlane(tab.first[t.e] + (mt - tab.before[t.e]) * BM);
-    t.last = __builtin_amdgcn_readfirstlane(max(tab.first[t.e + 1], tab.first[t.e]));
+    t.last = __builtin_amdgcn_readfirstlane(tab.first[t.e + 1]);
     return;
   }
   search_rows<BM>(a, mt, t);

@@ -38,11 +38,21 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
-// Slots [first, last) of expert e, kept inside [0, slots) whatever the offsets hold.
-__device__ __forceinline__ void expert_range(const ProductArgs& a, int e, int& first, int& last) {
-  const int lo = a.offsets[e], hi = a.offsets[e + 1], n = (int)a.slots;
-  first = min(max(lo, 0), n);
-  last = min(max(hi, first), n);
+// Slots [first, last) of expert e0 + lane (none past the last expert), for the lanes of a wave: the
+// offsets cut to [0, slots] and each one below an earlier one raised to it, so that the ranges follow
+// one another, and have no more tiles than slots / BM + experts, whatever the offsets hold.  `top`:
+// the end of the experts before e0 (0 for none), moved on to that of these.
+__device__ __forceinline__ void expert_ranges(const ProductArgs& a, int e0, int& top, int& first, int& last) {
+  const int lane = threadIdx.x & 63, n = (int)a.slots;
+  first = min(max(a.offsets[min(e0 + lane, a.experts)], 0), n);
+  last = min(max(a.offsets[min(e0 + lane + 1, a.experts)], 0), n);
+  if (__any(last < first || first < top)) {
+    first = max(first, top);   // running maximum
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) first = max(first, __shfl_up(first, o));
+    last = max(last, first);
+  }
+  top = __builtin_amdgcn_readlane(last, 63);
 }
 
 // Rows [m0, last) of y with expert e's layer, columns from n0: one tile.
@@ -54,12 +64,10 @@ struct Tile {
 template <int BM>
 __device__ __forceinline__ bool search_rows(const ProductArgs& a, int mt, Tile& t) {
   const int lane = threadIdx.x & 63;
-  for (int e0 = 0; e0 < a.experts; e0 += 64) {
-    int c = 0, first = 0, last = 0;
-    if (e0 + lane < a.experts) {
-      expert_range(a, e0 + lane, first, last);
-      c = (last - first + BM - 1) / BM;
-    }
+  for (int e0 = 0, top = 0; e0 < a.experts; e0 += 64) {
+    int first, last;
+    expert_ranges(a, e0, top, first, last);
+    const int c = (last - first + BM - 1) / BM;
     int sum = c;   // inclusive sum over the lanes
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {

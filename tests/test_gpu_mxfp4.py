@@ -777,3 +777,51 @@ def test_experts_of_the_most_rows():
     _experts_check(y, want, mag, n, False)
     del codes, scales
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("path", [{}, *PATHS[2:]], ids=str)
+@pytest.mark.parametrize("kind", ["three times over", "down at the end of 64", "any", "many"])
+def test_experts_of_decreasing_offsets(kind, path):
+    """An offset below an earlier one counts as that one: every later expert keeps its slots."""
+    announce(f"mxfp4 experts, offsets {kind} {path}")
+    kq = _kq()
+    rng = np.random.default_rng(len(kind))
+    slots, n, out = 2000, 128, 20
+    if kind == "three times over":
+        offsets = np.array([0, 1000, 0, 1000, 0, 1000, 2000])
+    elif kind == "down at the end of 64":
+        offsets = np.concatenate([np.linspace(0, 1500, 65), np.linspace(900, 2000, 40)]).astype(int)
+    else:
+        offsets = rng.integers(-500, 2500, 9 if kind == "any" else 1300)
+        offsets[-400:] = np.sort(offsets[-400:])
+    cut = np.maximum.accumulate(np.clip(offsets, 0, slots))
+    experts = len(offsets) - 1
+    x, xs = _random_codes(slots, n)
+    w, ws = _random_codes(out, n, experts)
+    y = _empty((slots, out), "f32")
+    with _forced(path):
+        kq.kq_mxfp4_experts(x, None, _dev(offsets.astype(np.int32)), w, ws, y, x_scales=xs, n=n)
+    xq = _values(x, xs, np.arange(slots))
+    for e in np.flatnonzero(np.diff(cut))[::-1]:
+        lo, hi = cut[e], cut[e + 1]
+        _close(y[lo:hi], xq[lo:hi], _values(w[e], ws[e], np.arange(out)), False)
+    outside = np.r_[0:cut[0], cut[-1]:slots]
+    assert bool((y[outside] == 123.0).all())
+
+
+def test_experts_of_offsets_that_swing():
+    """2^30 slots, offsets that go up to all of them and down to none 2048 times: the first expert's."""
+    torch = torch_cuda()
+    kq = _kq()
+    slots, rows, n, experts = 1 << 30, 4, 100, 4096
+    x, xs = _random_codes(rows, n)
+    w, ws = _random_codes(1, n, experts)
+    few = _empty((rows, 1), "bf16")
+    kq.kq_mxfp4_linear(x, w[0], ws[0], few, x_scales=xs, n=n)
+    index = torch.arange(rows, dtype=torch.int32, device="cuda").repeat(slots // rows)
+    offsets = torch.tensor([0, slots], dtype=torch.int32, device="cuda").repeat(experts // 2 + 1)[:experts + 1]
+    y = _empty((slots, 1), "bf16")
+    kq.kq_mxfp4_experts(x, index, offsets.contiguous(), w, ws, y, x_scales=xs, n=n)
+    assert bool((y.view(-1, rows) == few.view(1, rows)).all())
+    del index, y
+    torch.cuda.empty_cache()
