@@ -825,3 +825,88 @@ def test_experts_of_offsets_that_swing():
     assert bool((y.view(-1, rows) == few.view(1, rows)).all())
     del index, y
     torch.cuda.empty_cache()
+
+
+def _device_values(codes, scales, rows):
+    torch = torch_cuda()
+    return torch.from_numpy(_values(codes, scales, rows)).cuda()
+
+
+def _close_everywhere(y, xq, w, bf16):
+    """_close for device operands in 64 bits, every entry."""
+    ref, mag = xq @ w.T, xq.abs() @ w.abs().T
+    bound = (xq.shape[1] + 2) * 2.0 ** -24 * mag
+    if bf16:
+        bound = bound * (1 + 2.0 ** -8) + 2.0 ** -8 * ref.abs()
+    off = (y.double() - ref).abs() - bound
+    assert bool((off <= 0).all()), float(off.max())
+
+
+TILES = [dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=t) for t in (256, 128, 64)]
+
+
+@pytest.mark.parametrize("path", TILES, ids=str)
+@pytest.mark.parametrize("n", [1152, 2304])
+@pytest.mark.parametrize("yk,indexed", [("bf16", True), ("f32", True), ("bf16", False)])
+def test_experts_of_many_tiles_and_rounds(n, yk, indexed, path):
+    """Several tiles for every workgroup, each of several rounds of the ring (odd and even numbers of
+    128 columns, last rounds with and without stages past the end), behind a shuffled index that
+    leaves the rows in places: what runs while one tile follows another."""
+    announce(f"mxfp4 experts, many tiles, {n} {yk} {indexed} {path}")
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(n)
+    slots, rows, out, experts = 8000, 4000 if indexed else 8000, 2500, 5
+    offsets = np.int32([3, 1900, 1900, 4333, 7990, 7997])
+    x, xs = _random_codes(rows, n)
+    w, ws = _random_codes(out, n, experts)
+    index = rng.integers(0, rows, slots).astype(np.int32)
+    index[rng.integers(0, slots, 200)] = rng.choice([-1, rows, -2 ** 31, 2 ** 31 - 1], 200)
+    index = index if indexed else None
+    y = _empty((slots, out), yk)
+    with _forced(path):
+        kq.kq_mxfp4_experts(x, _dev(index), _dev(offsets), w, ws, y, x_scales=xs, n=n)
+    xq = _device_values(x, xs, np.arange(rows))
+    if indexed:
+        inside = torch.from_numpy((index >= 0) & (index < rows)).cuda()
+        at = torch.from_numpy(np.clip(index, 0, rows - 1)).long().cuda()
+        xq = xq[at] * inside[:, None]
+    for e in range(experts):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if lo < hi:
+            _close_everywhere(y[lo:hi], xq[lo:hi], _device_values(w[e], ws[e], np.arange(out)), yk == "bf16")
+    assert bool((y[:3] == 123.0).all()) and bool((y[7997:] == 123.0).all())
+
+
+@pytest.mark.parametrize("path", TILES, ids=str)
+@pytest.mark.parametrize("rows,n,out,yk", [(5000, 1408, 4200, "bf16"), (5001, 1280, 4199, "f32")])
+def test_linear_of_many_tiles_and_rounds(rows, n, out, yk, path):
+    announce(f"mxfp4 linear, many tiles, {rows}x{n} -> {out} {yk} {path}")
+    kq = _kq()
+    x, xs = _random_codes(rows, n)
+    w, ws = _random_codes(out, n)
+    y = _empty((rows, out), yk)
+    with _forced(path):
+        kq.kq_mxfp4_linear(x, w, ws, y, x_scales=xs, n=n)
+    _close_everywhere(y, _device_values(x, xs, np.arange(rows)), _device_values(w, ws, np.arange(out)), yk == "bf16")
+
+
+def test_experts_of_rows_past_32_bits_over_many_tiles():
+    """Rows of more than 4 GiB behind an index, several tiles for every workgroup."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(12)
+    rows, n, slots, out, experts = 1_060_000, 8192, 8000, 2500, 5
+    offsets = np.int32([0, 1900, 1900, 4333, 7990, 8000])
+    x, xs = _random_codes(rows, n)
+    w, ws = _random_codes(out, n, experts)
+    index = rng.integers(0, rows, slots).astype(np.int32)
+    index[[0, 1, 4332, 4333, 7999]] = [rows - 1, -1, rows - 2, rows, 0]
+    y = _empty((slots, out), "bf16")
+    kq.kq_mxfp4_experts(x, _dev(index), _dev(offsets), w, ws, y, x_scales=xs, n=n)
+    inside = (index >= 0) & (index < rows)
+    xq = _device_values(x, xs, np.clip(index, 0, rows - 1)) * torch.from_numpy(inside).cuda()[:, None]
+    for e in range(experts):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        if lo < hi:
+            _close_everywhere(y[lo:hi], xq[lo:hi], _device_values(w[e], ws[e], np.arange(out)), True)
