@@ -72,7 +72,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
 // instruction, so its two loads are neighbours, a row's line is read whole, and both blocks'
 // scales lie in one dword.
 // Bound by the layer's bytes and, at these sizes, by the latency of the loads before the first
-// product (16 rows, 11008 x 4096: 24 MB, 7.7 us; 2 experts of it for one token: 48 MB, 15.5 us with
+// product (16 rows, 11008 x 4096: 24 MB, 7.7 us; 2 experts of it for one token: 48 MB, 15.3 us with
 // the token's rotation).
 // T: void for quantised activations, else their type, quantised here (MT = 1).
 template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE>
@@ -258,8 +258,8 @@ bool mx_few(const ProductArgs& p) {
 }
 
 // One token or two: each workgroup quantises them for itself, while its part of the layer is on
-// the way (one token, 4096 x 4096: 7.6 us, and by a kernel of its own 4.5 + 3.7 and a launch; through
-// two of eight experts of 11008 x 4096: 15.5, and 4.2 + 13.8).
+// the way (one token, 4096 x 4096: 7.5 us, and by a kernel of its own 4.5 + 3.7 and a launch; through
+// two of eight experts of 11008 x 4096: 15.3, and 4.2 + 13.8).
 bool mx_few_fused(const ProductArgs& p, const MxRows& x) {
   return x.rows > 0 && p.slots <= 16 && p.slots * x.n <= testing_value(KQ_TESTING_MX_FUSED, 8192);
 }

@@ -137,7 +137,7 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 // tile after tile; the copies of the next tile's first stages follow those of the last stages of
 // the present one, so the ring never runs dry and the stores of one tile go out while the next is
 // multiplied.
-// 16384 x 8192 x 28672: 1.78 ms, 4.3 PF, the matrix instructions busy 67 % of the time at 1.6 GHz
+// 16384 x 8192 x 28672: 1.78 ms, 4.3 PF, the matrix instructions busy 68 % of the time at 1.55 GHz
 // (alone, from registers, they are held to 1.56 GHz by power: 6.4 PF); eight waves of 128 x 64,
 // since four of 128 x 128, which read a third less from LDS, are 2 % slower.  2048 x 11008 x 4096 with
 // 128 x 128 tiles: 55 us, 3.3 PF; with 256 x 256, on half as many workgroups, 71.

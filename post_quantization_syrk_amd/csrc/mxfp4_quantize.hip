@@ -50,9 +50,9 @@ __device__ __forceinline__ void store_columns(uint16_t* to, const u32x4 (&o)[2])
 // for its largest value, four strides of the rotation without any), and takes one row after
 // another, the next one's load in flight.  Rotation blocks of up to SPAN columns stay inside a wave
 // (its four waves work on their own); longer ones are a workgroup's, and pass through LDS once.
-// Bound by HBM without a rotation (28672 x 8192 fp32 with values: 280-305 us, 5.0-5.5 TB/s) and by the
-// vector instructions with a long one (16384 x 8192 bf16, block 8192: 122 us, 3.0 TB/s, VALU 93 %
-// busy); 2048 x 11008 bf16, block 256: 19 us, with values 27; one row of 4096: 4.2 us.
+// Bound by HBM without a rotation (28672 x 8192 fp32 with values: 280-307 us, 5.0-5.5 TB/s) and by the
+// vector instructions with a long one (16384 x 8192 bf16, block 8192: 98-104 us, 3.3-3.5 TB/s, and 121-125
+// in front of a product); 2048 x 11008 bf16, block 256: 19 us, with values 27; one row of 4096: 4.1 us.
 // LOGH: the rotation block, 2^LOGH columns (-1: any up to SPAN, decided at run time).
 template <typename T, int LOGH, bool WIDE>
 __global__ __launch_bounds__(LOGH > 10 ? 64 << (LOGH - 10) : 256) void mx_quantize_kernel(QuantArgs a) {
