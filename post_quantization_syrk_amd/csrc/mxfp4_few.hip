@@ -281,10 +281,10 @@ kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, b
     return nt == 4 ? KQ_FEW(4, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
 #undef KQ_FEW
   }
-#define KQ_FEW(MT) \
-  (nt == 4 ? launch<8, MT, 4, 1, void>(p, r, s) : nt == 2 ? launch<8, MT, 2, 2, void>(p, r, s) : launch<8, MT, 1, 2, void>(p, r, s))
-  return bm == 16 ? KQ_FEW(1) : KQ_FEW(2);
-#undef KQ_FEW
+  // (32 rows never come with 64 columns: where mx_few takes them, such tiles are half as many as the
+  // compute units at most)
+  if (bm == 32) return nt == 1 ? launch<8, 2, 1, 2, void>(p, r, s) : launch<8, 2, 2, 2, void>(p, r, s);
+  return nt == 4 ? launch<8, 1, 4, 1, void>(p, r, s) : nt == 2 ? launch<8, 1, 2, 2, void>(p, r, s) : launch<8, 1, 1, 2, void>(p, r, s);
 }
 
 }  // namespace kq
