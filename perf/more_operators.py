@@ -270,7 +270,7 @@ def prepare(case, seed):
                            index=empty(rows * top, kind=torch.int32), offsets=empty(experts + 1, kind=torch.int32),
                            counts=empty(experts + 2, kind=torch.int32))
         if case["train"]:
-            s["routes"] |= dict(lse=empty(rows), loss=empty(1))
+            s["routes"]["loss"] = empty(1)
             s["dlogits"] = empty(rows, experts, kind=DTYPES[case["x"]])
         return s
     if case["op"] == "combine":
@@ -299,7 +299,6 @@ def _plain_route(s):
     most = torch.where(has, value[:, :1], 0.0)
     p = torch.exp(x - most)
     total = p.sum(1, keepdim=True)
-    lse = (most + torch.log(total)).squeeze(1)
     p = p / torch.where(has, total, 1.0)
     chosen = value > -math.inf
     weight = torch.exp(value - most)
@@ -311,7 +310,7 @@ def _plain_route(s):
     if not case["train"]:
         return out
     share, rows = counts / made.clamp(min=1).double(), used.clamp(min=1).double()
-    out |= dict(lse=lse, loss=(experts * (share * p.sum(0, dtype=torch.float64) / rows).sum()).float()[None])
+    out["loss"] = (experts * (share * p.sum(0, dtype=torch.float64) / rows).sum()).float()[None]
     balance = (s["dloss"].double() * experts * share / rows).float()
     dl = p * (balance - (p * balance).sum(1, keepdim=True))
     dw = torch.where(chosen, s["dweight"], 0.0)
@@ -377,7 +376,7 @@ def run(s):
         kq.kq_route(s["logits"], normalize=case["normalize"], **r)
         if not case["train"]:
             return r
-        kq.kq_route_backward(s["logits"], s["dlogits"], r["weight"], r["expert"], r["counts"], r["lse"], dweight=s["dweight"], dloss=s["dloss"],
+        kq.kq_route_backward(s["logits"], s["dlogits"], r["weight"], r["expert"], r["counts"], dweight=s["dweight"], dloss=s["dloss"],
                              normalize=case["normalize"])
         return {**r, "dlogits": s["dlogits"]}
     if case["op"] == "combine":
@@ -401,7 +400,7 @@ def work(case):
         size = SIZE[case["x"]]
         moved, flops = grid * size + 16 * choices + 8 * case["experts"], grid * (4 + case["top"])
         if case["train"]:
-            moved, flops = moved + 2 * grid * size + 12 * choices + 8 * case["rows"], flops + 6 * grid
+            moved, flops = moved + 2 * grid * size + 12 * choices, flops + 6 * grid
         return {"bytes": moved, "flops": flops}
     if case["op"] == "combine":
         row, choices = case["rows"] * case["n"], case["rows"] * case["top"]
@@ -478,7 +477,7 @@ def _exact_route(case, seed):
     out = dict(weight=weight.detach(), expert=expert, slot=slot.view(expert.shape), index=index, offsets=offsets,
                counts=torch.cat((counts, torch.tensor([made, used], device="cuda"))))
     if case["train"]:
-        out |= dict(lse=torch.logsumexp(l64.detach(), 1), loss=loss.detach()[None], dlogits=grad)
+        out |= dict(loss=loss.detach()[None], dlogits=grad)
     return out
 
 
