@@ -536,6 +536,154 @@ kq_status kq_mxfp4_experts(const void* x, int x_type, int64_t rows, int64_t in, 
                            const uint8_t* w_codes, const uint8_t* w_scales, int64_t out, void* y,
                            int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream);
 
+/*
+ * Around the products of a mixture: routing (kq_route), what follows a product in the same launch
+ * (kq_epilogue), and the sum of the experts' rows (kq_combine).
+ */
+enum {
+  KQ_ACT_NONE = 0,      /* v */
+  KQ_ACT_RELU = 1,      /* max(v, 0); NaN stays NaN */
+  KQ_ACT_SILU = 2,      /* v / (1 + exp(-v)) */
+  KQ_ACT_GELU = 3,      /* v (1 + erf(v / sqrt 2)) / 2 */
+  KQ_ACT_GELU_TANH = 4  /* v (1 + tanh(sqrt(2 / pi) (v + 0.044715 v^3))) / 2 */
+};
+
+/*
+ * What a product applies to its sums before it stores them, in fp32, rounded once to y_type:
+ *   not gated   y[t, o] = act(sum[t, o] + bias[o]) + residual[t, o]
+ *   gated       y[t, o] = act(sum[t, o] + bias[o]) (sum[t, out + o] + bias[out + o]) + residual[t, o]
+ * A gated layer has 2 out rows, those of the gate first.
+ *
+ *   act            KQ_ACT_*
+ *   gated          0 or 1
+ *   bias           device fp32 [layer rows], for kq_mxfp4_experts_epilogue [experts][layer rows],
+ *                  contiguous, or NULL for 0
+ *   residual       device, as many rows as y, of out values of residual_type (KQ_F32 or KQ_BF16),
+ *                  leading dim ldr >= out, or NULL for 0.  It may be y itself (the same address,
+ *                  type and leading dim), else it must not overlap y
+ */
+typedef struct kq_epilogue {
+  int act;
+  int gated;
+  const float* bias;
+  const void* residual;
+  int residual_type;
+  int64_t ldr;
+} kq_epilogue;
+
+/*
+ * kq_mxfp4_linear_epilogue, kq_mxfp4_experts_epilogue -- kq_mxfp4_linear and kq_mxfp4_experts with
+ * an epilogue.  Arguments as for those, and
+ *   out       columns of y: half the layer's rows where it is gated
+ *   w_codes, w_scales  the layer's rows, 2 out of them where it is gated (each expert's, likewise)
+ *   epilogue  host, read during the call; the slots that are not written keep y whatever the residual
+ * The sums are those of the calls without an epilogue.  KQ_ESHAPE for a gated layer of 2^31 bytes of
+ * codes or more, per expert.
+ */
+kq_status kq_mxfp4_linear_epilogue(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                   const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                                   const uint8_t* w_codes, const uint8_t* w_scales, int64_t out,
+                                   const kq_epilogue* epilogue, void* y, int y_type, int64_t ldy, void* ws,
+                                   size_t ws_bytes, void* stream);
+kq_status kq_mxfp4_experts_epilogue(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                    const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                                    const int32_t* index, int64_t slots, const int32_t* offsets, int experts,
+                                    const uint8_t* w_codes, const uint8_t* w_scales, int64_t out,
+                                    const kq_epilogue* epilogue, void* y, int y_type, int64_t ldy, void* ws,
+                                    size_t ws_bytes, void* stream);
+
+/*
+ * kq_route_workspace -- workspace bytes of kq_route.
+ */
+kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
+
+/*
+ * kq_route -- the experts of each row, in the form that kq_mxfp4_experts takes, and the balance loss.
+ *
+ * For a row of logits l: p = softmax(l) over the experts.  The row chooses the `top` experts with the
+ * largest logits, in descending order, the lower index first among equal ones, and never one whose
+ * logit is -inf (closed experts, padding rows): where it runs out, the other choices are missing.
+ * With m the largest logit and c_j the chosen ones, the weights are
+ *   normalize = 0   p[c_j] = exp(l[c_j] - m) / sum_e exp(l[e] - m)
+ *   normalize = 1   exp(l[c_j] - m) / sum_i exp(l[c_i] - m)
+ * A slot is given to every choice, sorted by expert, then by row, then by j.  The balance loss is
+ *   L = experts sum_e f_e P_e,  f_e = count_e / N,  P_e = sum_t p[t, e] / R
+ * over the N choices and the R rows that have a logit above -inf (0 if there are none): 1 where the
+ * experts are equally busy or equally probable.  A row with a NaN or +inf has no softmax: its choices
+ * are missing, and its weights and the loss are NaN.
+ *
+ *   logits   device, rows x experts of type (KQ_F32 or KQ_BF16), leading dim ld >= experts
+ *   weight   device fp32 [rows][top]; 0 for a missing choice (NaN in a row without a softmax)
+ *   expert   device int32 [rows][top]; -1 for a missing choice
+ *   slot     device int32 [rows][top]; -1 for a missing choice
+ *   index    device int32 [rows * top]: the row of each slot, -1 from slot N on
+ *   offsets  device int32 [experts + 1]: each expert's first slot, then N
+ *   counts   device int32 [experts + 2]: choices of each expert, then N, then R
+ *   loss_opt device fp32 [1]: L, or NULL
+ *   ws       device workspace, 16-byte aligned, ws_bytes >= kq_route_workspace(...)
+ * Sizes: rows >= 0, rows * top < 2^31, 1 <= experts <= 4096, 1 <= top <= min(experts, 16).  Asynchronous
+ * on `stream`; the same inputs give the same bits (no order depends on atomics).  The outputs must not
+ * overlap each other or the inputs.
+ */
+kq_status kq_route(const void* logits, int type, int64_t rows, int experts, int64_t ld, int top, int normalize,
+                   float* weight, int32_t* expert, int32_t* slot, int32_t* index, int32_t* offsets,
+                   int32_t* counts, float* loss_opt, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * kq_route_backward -- the gradient of the logits, from those of kq_route's weights and loss.
+ *
+ * With b_e = dloss experts count_e / (N R) (the counts are constants), w_j the weights and dw_j their
+ * gradients (those of missing choices count as 0):
+ *   normalize = 0   dl_e = p_e (b_e - sum p b - sum_j w_j dw_j) + [e = c_j] w_j dw_j
+ *   normalize = 1   dl_e = p_e (b_e - sum p b) + [e = c_j] w_j (dw_j - sum_i w_i dw_i)
+ * in fp32, rounded once to type.  A row without logits above -inf gets zeros, one without a softmax NaN.
+ *
+ *   logits, type, rows, experts, ld, top, normalize  as given to kq_route
+ *   weight, expert, counts  device, as written by kq_route
+ *   dweight_opt  device fp32 [rows][top], or NULL for 0
+ *   dloss_opt    device fp32 [1], or NULL for 0
+ *   dlogits      device, rows x experts of type, leading dim ldd >= experts; may be logits itself
+ * Asynchronous on `stream`.
+ */
+kq_status kq_route_backward(const void* logits, int type, int64_t rows, int experts, int64_t ld, int top,
+                            int normalize, const float* weight, const int32_t* expert, const int32_t* counts,
+                            const float* dweight_opt, const float* dloss_opt, void* dlogits,
+                            int64_t ldd, void* stream);
+
+/*
+ * kq_combine -- the experts' rows back to the rows that they came from:
+ *   y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]],   in fp32, j ascending, rounded once to y_type.
+ *
+ *   z        device, slots x n of z_type (KQ_F32 or KQ_BF16), leading dim ldz >= n
+ *   slot     device int32 [rows][top]; one outside [0, slots) stands for a row of zeros
+ *   weight   device fp32 [rows][top], or NULL for 1
+ *   residual device, rows x n of residual_type, leading dim ldr >= n, or NULL for 0; it may be y itself
+ *            (the same address, type and leading dim)
+ *   y        device, rows x n of y_type, leading dim ldy >= n
+ * All aligned to their type.  Sizes: 0 <= rows, slots <= 2^30, rows * top < 2^31, 1 <= n <= 2^24,
+ * 1 <= top <= 64.  Asynchronous on `stream`; the same inputs give the same bits.
+ */
+kq_status kq_combine(const void* z, int z_type, int64_t slots, int64_t n, int64_t ldz, const int32_t* slot,
+                     const float* weight, int64_t rows, int top, const void* residual, int residual_type,
+                     int64_t ldr, void* y, int y_type, int64_t ldy, void* stream);
+
+/*
+ * kq_combine_backward -- the gradients of kq_combine's z and weights from that of y (the residual's is
+ * that of y):
+ *   dz[slot[t, j]] = weight[t, j] dy[t],   dweight[t, j] = sum_i dy[t, i] z[slot[t, j], i].
+ *
+ *   dy       device, rows x n of dy_type, leading dim lddy >= n
+ *   z        device, as given to kq_combine; read only for dweight (else it may be NULL)
+ *   slot, weight  as given to kq_combine.  No slot may be named twice within [0, slots)
+ *   dz_opt   device, slots x n of z_type, leading dim lddz >= n, or NULL.  Rows of slots that no choice
+ *            names are left as they were.  May be z itself (the same address and leading dim)
+ *   dweight_opt  device fp32 [rows][top], or NULL; 0 for a slot outside [0, slots)
+ * Alignment, sizes and determinism as for kq_combine; sums in fp32.
+ */
+kq_status kq_combine_backward(const void* dy, int dy_type, int64_t rows, int64_t n, int64_t lddy, const void* z,
+                              int z_type, int64_t slots, int64_t ldz, const int32_t* slot, const float* weight,
+                              int top, void* dz_opt, int64_t lddz, float* dweight_opt, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,6 +20,8 @@ LIB_PATH = os.path.join(HERE, "libkq.so")
 KQ_OK, KQ_EINVAL, KQ_ESHAPE, KQ_ENOTSPD, KQ_EWORKSPACE, KQ_ENOTIMPL, KQ_EHIP = range(7)
 KQ_BIIP_FULL, KQ_BIIP_NO_RESCALE, KQ_BIIP_IN_ONLY, KQ_BIIP_OUT_ONLY = range(4)
 KQ_F32, KQ_BF16, KQ_MXFP4 = range(3)
+KQ_ACT_NONE, KQ_ACT_RELU, KQ_ACT_SILU, KQ_ACT_GELU, KQ_ACT_GELU_TANH = range(5)
+ACTS = {"none": KQ_ACT_NONE, "relu": KQ_ACT_RELU, "silu": KQ_ACT_SILU, "gelu": KQ_ACT_GELU, "gelu_tanh": KQ_ACT_GELU_TANH}
 STATUS_NAMES = {0: "KQ_OK", 1: "KQ_EINVAL", 2: "KQ_ESHAPE", 3: "KQ_ENOTSPD", 4: "KQ_EWORKSPACE",
                 5: "KQ_ENOTIMPL", 6: "KQ_EHIP"}
 
@@ -30,7 +32,9 @@ EXPORTED = ("kq_version", "kq_last_error", "kq_accumulate_hessian", "kq_sensitiv
             "kq_allocate_bits", "kq_deploy_linear", "kq_deploy_linear_group",
             "kq_flipflop_workspace", "kq_flipflop", "kq_quantize_two_sided_workspace",
             "kq_quantize_two_sided", "kq_mxfp4_quantize", "kq_mxfp4_workspace", "kq_mxfp4_linear",
-            "kq_mxfp4_experts", "kq_testing_select")
+            "kq_mxfp4_experts", "kq_mxfp4_linear_epilogue", "kq_mxfp4_experts_epilogue",
+            "kq_route_workspace", "kq_route", "kq_route_backward", "kq_combine", "kq_combine_backward",
+            "kq_testing_select")
 
 
 class KQError(RuntimeError):
@@ -56,6 +60,12 @@ class QuantParams(ctypes.Structure):
     _fields_ = [("bits", ctypes.c_int), ("group", ctypes.c_int), ("block", ctypes.c_int),
                 ("damp", ctypes.c_float), ("asym", ctypes.c_int), ("act_order", ctypes.c_int),
                 ("w_clip", ctypes.c_int)]
+
+
+class Epilogue(ctypes.Structure):
+    """kq_epilogue (include/kq.h)."""
+    _fields_ = [("act", ctypes.c_int), ("gated", ctypes.c_int), ("bias", ctypes.c_void_p),
+                ("residual", ctypes.c_void_p), ("residual_type", ctypes.c_int), ("ldr", ctypes.c_int64)]
 
 
 _vp, _i64, _int, _f32, _sz = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -91,6 +101,15 @@ _SIGS = {
                          _vp, _sz, _vp], _int),
     "kq_mxfp4_experts": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp,
                           _i64, _vp, _int, _i64, _vp, _sz, _vp], _int),
+    "kq_mxfp4_linear_epilogue": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _vp, _i64,
+                                  ctypes.POINTER(Epilogue), _vp, _int, _i64, _vp, _sz, _vp], _int),
+    "kq_mxfp4_experts_epilogue": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _int, _vp, _vp,
+                                   _i64, ctypes.POINTER(Epilogue), _vp, _int, _i64, _vp, _sz, _vp], _int),
+    "kq_route_workspace": ([_i64, _int, _int, ctypes.POINTER(_sz)], _int),
+    "kq_route": ([_vp, _int, _i64, _int, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp], _int),
+    "kq_route_backward": ([_vp, _int, _i64, _int, _i64, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "kq_combine": ([_vp, _int, _i64, _i64, _i64, _vp, _vp, _i64, _int, _vp, _int, _i64, _vp, _int, _i64, _vp], _int),
+    "kq_combine_backward": ([_vp, _int, _i64, _i64, _i64, _vp, _int, _i64, _i64, _vp, _vp, _int, _vp, _i64, _vp, _vp], _int),
     "kq_testing_select": ([_int, _i64], _int),
 }
 
@@ -596,3 +615,188 @@ def kq_mxfp4_experts(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, s
                                wp, wb, _mx_stream_of(_mx_device()) if stream is None else stream.cuda_stream)
     if st:
         _check(st, "kq_mxfp4_experts")
+
+
+def _mx_here(device, stream) -> int:
+    """The stream to use, once the tensors' device is found to be the current one (and the stream's)."""
+    current = _mx_device()
+    if device != current:
+        raise ValueError(f"the tensors are on device {device}, the current device is {current}")
+    if stream is None:
+        return _mx_stream_of(current)
+    if stream.device_index != current:
+        raise ValueError(f"the stream is on device {stream.device_index}, the current device is {current}")
+    return stream.cuda_stream
+
+
+def _mx_same(device, *tensors) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on devices {device} and {t.get_device()}")
+
+
+def _epilogue(bias, act, gated, residual, rows: int, out: int, experts):
+    """A kq_epilogue for `rows` x `out` outputs (experts: of that many layers, None: of one)."""
+    wide = out * (2 if gated else 1)
+    if bias is not None:
+        if tuple(bias.shape) != ((wide,) if experts is None else (experts, wide)):
+            raise ValueError(f"bias must be {(wide,) if experts is None else (experts, wide)}")
+        bias = _mx_vector(bias, "bias", bias.numel(), _mx_f32)
+    if act not in ACTS:
+        raise ValueError(f"act must be one of {', '.join(ACTS)}")
+    rp, rt, ldr = None, 0, 0
+    if residual is not None:
+        rp, rt, rrows, rcols, ldr = _mx_matrix(residual, "residual")
+        if rrows != rows or rcols != out:
+            raise ValueError(f"residual must be {(rows, out)}")
+    return Epilogue(ACTS[act], 1 if gated else 0, bias, rp, rt, ldr)
+
+
+def kq_mxfp4_linear_epilogue(x, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1, x_scales=None,
+                             n=None, bias=None, act: str = "none", gated: bool = False, residual=None, stream=None) -> None:
+    """y = act(Q(P D^-1 x) W^T + bias) + residual, as kq_mxfp4_linear; act: none, relu, silu, gelu or
+    gelu_tanh; gated: the layer has twice y's columns, y = act(first half) * second half + residual.
+    bias fp32 [layer rows], residual fp32 or bf16 like y (it may be y)."""
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb, ws = _mx_rows(x, x_scales, d, sign, n, ws, stream)
+    yp, yt, yrows, out, ldy = _mx_matrix(y, "y")
+    cp, sp = _mx_check(w_codes, w_scales, (2 * out if gated else out,), n, "weight")
+    if yrows != rows:
+        raise ValueError(f"y must have {rows} rows")
+    device = y.get_device()
+    _mx_same(device, x, w_codes, w_scales, d, sign, bias, residual, ws, x_scales)
+    ep = _epilogue(bias, act, gated, residual, rows, out, None)
+    st = _lib.kq_mxfp4_linear_epilogue(xp, xt, rows, n, ldx, xsp, dp, gp, had, cp, sp, out, ctypes.byref(ep), yp, yt, ldy,
+                                       wp, wb, _mx_here(device, stream))
+    if st:
+        _check(st, "kq_mxfp4_linear_epilogue")
+
+
+def kq_mxfp4_experts_epilogue(x, index, offsets, w_codes, w_scales, y, ws=None, d=None, sign=None, had: int = 1,
+                              x_scales=None, n=None, bias=None, act: str = "none", gated: bool = False, residual=None,
+                              stream=None) -> None:
+    """kq_mxfp4_experts with the epilogue of kq_mxfp4_linear_epilogue: bias fp32 [experts, layer rows],
+    residual like y, by slots."""
+    xp, xt, rows, n, ldx, xsp, dp, gp, wp, wb, ws = _mx_rows(x, x_scales, d, sign, n, ws, stream)
+    yp, yt, slots, out, ldy = _mx_matrix(y, "y")
+    experts = w_codes.shape[0]
+    cp, sp = _mx_check(w_codes, w_scales, (experts, 2 * out if gated else out), n, "weight")
+    device = y.get_device()
+    _mx_same(device, x, index, offsets, w_codes, w_scales, d, sign, bias, residual, ws, x_scales)
+    ep = _epilogue(bias, act, gated, residual, slots, out, experts)
+    st = _lib.kq_mxfp4_experts_epilogue(xp, xt, rows, n, ldx, xsp, dp, gp, had, _mx_vector(index, "index", slots, _mx_i32),
+                                        slots, _mx_vector(offsets, "offsets", experts + 1, _mx_i32), experts, cp, sp, out,
+                                        ctypes.byref(ep), yp, yt, ldy, wp, wb, _mx_here(device, stream))
+    if st:
+        _check(st, "kq_mxfp4_experts_epilogue")
+
+
+def kq_route_workspace(rows: int, experts: int, top: int) -> int:
+    """Workspace bytes of kq_route."""
+    b = ctypes.c_size_t(0)
+    _check(load_library().kq_route_workspace(rows, experts, top, ctypes.byref(b)), "kq_route_workspace")
+    return b.value
+
+
+def _choices(expert, name: str):
+    try:
+        rows, top = expert.shape
+    except (AttributeError, ValueError):
+        raise ValueError(f"{name} must be a matrix [rows, top]") from None
+    return rows, top
+
+
+def kq_route(logits, weight, expert, slot, index, offsets, counts, loss=None, normalize: bool = False, ws=None,
+             stream=None) -> None:
+    """The `top` experts of each row of logits (fp32 or bf16 [rows, experts]): weight fp32, expert and
+    slot int32 [rows, top]; for kq_mxfp4_experts, index int32 [rows * top] and offsets int32
+    [experts + 1]; counts int32 [experts + 2] (each expert's choices, all, rows with a softmax); for
+    training, the balance loss fp32 [1].  normalize: weights sum to one."""
+    if _mx_types is None:
+        _mx_setup()
+    xp, xt, rows, experts, ld = _mx_matrix(logits, "logits")
+    erows, top = _choices(expert, "expert")
+    if erows != rows:
+        raise ValueError(f"expert must have {rows} rows")
+    n, device = rows * top, logits.get_device()
+    if ws is None:
+        ws = _workspace(kq_route_workspace(rows, experts, top), logits.device, stream)
+    _mx_same(device, weight, expert, slot, index, offsets, counts, loss, ws)
+    st = _lib.kq_route(xp, xt, rows, experts, ld, top, 1 if normalize else 0, _mx_vector(weight, "weight", n, _mx_f32),
+                       _mx_vector(expert, "expert", n, _mx_i32), _mx_vector(slot, "slot", n, _mx_i32),
+                       _mx_vector(index, "index", n, _mx_i32), _mx_vector(offsets, "offsets", experts + 1, _mx_i32),
+                       _mx_vector(counts, "counts", experts + 2, _mx_i32), _mx_vector(loss, "loss", 1, _mx_f32), _mx_ptr(ws, "ws", _mx_u8), ws.numel(), _mx_here(device, stream))
+    if st:
+        _check(st, "kq_route")
+
+
+def kq_route_backward(logits, dlogits, weight, expert, counts, dweight=None, dloss=None, normalize: bool = False,
+                      stream=None) -> None:
+    """dlogits (like logits, which it may be) from the gradients of kq_route's weights, dweight fp32
+    [rows, top], and loss, dloss fp32 [1]; weight, expert and counts as kq_route left them."""
+    if _mx_types is None:
+        _mx_setup()
+    xp, xt, rows, experts, ld = _mx_matrix(logits, "logits")
+    gp, gt, grows, gcols, ldd = _mx_matrix(dlogits, "dlogits")
+    if gt != xt or grows != rows or gcols != experts:
+        raise ValueError("dlogits must have the type and shape of logits")
+    erows, top = _choices(expert, "expert")
+    if erows != rows:
+        raise ValueError(f"expert must have {rows} rows")
+    n, device = rows * top, logits.get_device()
+    _mx_same(device, dlogits, weight, expert, counts, dweight, dloss)
+    st = _lib.kq_route_backward(xp, xt, rows, experts, ld, top, 1 if normalize else 0,
+                                _mx_vector(weight, "weight", n, _mx_f32), _mx_vector(expert, "expert", n, _mx_i32),
+                                _mx_vector(counts, "counts", experts + 2, _mx_i32), _mx_vector(dweight, "dweight", n, _mx_f32),
+                                _mx_vector(dloss, "dloss", 1, _mx_f32), gp, ldd, _mx_here(device, stream))
+    if st:
+        _check(st, "kq_route_backward")
+
+
+def kq_combine(z, slot, y, weight=None, residual=None, stream=None) -> None:
+    """y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]]: z fp32 or bf16 [slots, n], slot int32
+    [rows, top] (outside z: zeros), weight fp32 [rows, top] or None for 1, y and residual (which may be
+    y) fp32 or bf16 [rows, n]."""
+    if _mx_types is None:
+        _mx_setup()
+    zp, zt, slots, n, ldz = _mx_matrix(z, "z")
+    yp, yt, rows, ycols, ldy = _mx_matrix(y, "y")
+    srows, top = _choices(slot, "slot")
+    if srows != rows or ycols != n:
+        raise ValueError(f"y must be {(srows, n)}")
+    rp, rt, ldr = None, 0, 0
+    if residual is not None:
+        rp, rt, rrows, rcols, ldr = _mx_matrix(residual, "residual")
+        if rrows != rows or rcols != n:
+            raise ValueError(f"residual must be {(rows, n)}")
+    device = y.get_device()
+    _mx_same(device, z, slot, weight, residual)
+    st = _lib.kq_combine(zp, zt, slots, n, ldz, _mx_vector(slot, "slot", rows * top, _mx_i32),
+                         _mx_vector(weight, "weight", rows * top, _mx_f32), rows, top, rp, rt, ldr, yp, yt, ldy,
+                         _mx_here(device, stream))
+    if st:
+        _check(st, "kq_combine")
+
+
+def kq_combine_backward(dy, z, slot, dz=None, weight=None, dweight=None, stream=None) -> None:
+    """The gradients of kq_combine's z (dz, of z's type and shape) and weights (dweight fp32 [rows, top])
+    from dy fp32 or bf16 [rows, n]; either may be left out.  No slot may be named twice."""
+    if _mx_types is None:
+        _mx_setup()
+    gp, gt, rows, n, lddy = _mx_matrix(dy, "dy")
+    zp, zt, slots, zcols, ldz = _mx_matrix(z, "z")
+    srows, top = _choices(slot, "slot")
+    if srows != rows or zcols != n:
+        raise ValueError(f"z must have {n} columns and slot {rows} rows")
+    op, ldo = None, n
+    if dz is not None:
+        op, ot, orows, ocols, ldo = _mx_matrix(dz, "dz")
+        if ot != zt or orows != slots or ocols != n:
+            raise ValueError("dz must have the type and shape of z")
+    device = dy.get_device()
+    _mx_same(device, z, slot, weight, dz, dweight)
+    st = _lib.kq_combine_backward(gp, gt, rows, n, lddy, zp, zt, slots, ldz,
+                                  _mx_vector(slot, "slot", rows * top, _mx_i32), _mx_vector(weight, "weight", rows * top, _mx_f32),
+                                  top, op, ldo, _mx_vector(dweight, "dweight", rows * top, _mx_f32),
+                                  _mx_here(device, stream))
+    if st:
+        _check(st, "kq_combine_backward")

@@ -1,0 +1,240 @@
+// The sum of the experts' rows back to the rows that they came from, and its gradients.
+#include "device_util.h"
+#include "kq_internal.h"
+
+#include <algorithm>
+
+namespace kq {
+namespace {
+
+constexpr int VEC = 8;   // neighbouring columns of a lane
+constexpr int MAX_TOP = 64;
+
+// Eight values as they lie in memory, at any alignment of their type.
+template <typename T>
+struct __attribute__((packed, aligned(sizeof(T)))) Pack {
+  T v[VEC];
+};
+
+__device__ __forceinline__ float value(float v) { return v; }
+__device__ __forceinline__ float value(uint16_t v) { return __uint_as_float((unsigned)v << 16); }
+__device__ __forceinline__ void put(float v, float& to) { to = v; }
+__device__ __forceinline__ void put(float v, uint16_t& to) { to = __builtin_bit_cast(uint16_t, (__bf16)v); }
+
+// Columns c .. c + 7 of a row of n (zeros past its end).
+template <typename T>
+__device__ __forceinline__ Pack<T> load(const T* row, int64_t c, int64_t n) {
+  Pack<T> k{};
+  if (c + VEC <= n) {
+    k = *(const Pack<T>*)(row + c);
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c + i < n) k.v[i] = row[c + i];
+  }
+  return k;
+}
+template <typename T>
+__device__ __forceinline__ void store(T* row, int64_t c, int64_t n, const float (&v)[VEC]) {
+  Pack<T> k;
+#pragma unroll
+  for (int i = 0; i < VEC; ++i) put(v[i], k.v[i]);
+  if (c + VEC <= n) {
+    *(Pack<T>*)(row + c) = k;
+  } else {
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      if (c + i < n) row[c + i] = k.v[i];
+  }
+}
+
+struct CombineArgs {
+  const void* z;
+  int64_t slots, n, ldz;
+  const int32_t* slot;
+  const float* weight;
+  int64_t rows;
+  int top;
+  const void* residual;
+  int64_t ldr;
+  void* y;
+  int64_t ldy;
+  int64_t chunks;   // lanes that share a row
+};
+
+template <typename Z, typename Y, typename R>
+__global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
+  const int64_t units = a.rows * a.chunks;
+  for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
+    const int64_t t = u / a.chunks, c = (u - t * a.chunks) * VEC;
+    float acc[VEC] = {};
+    if (a.residual) {
+      const Pack<R> r = load((const R*)a.residual + t * a.ldr, c, a.n);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] = value(r.v[i]);
+    }
+    for (int j = 0; j < a.top; ++j) {
+      const int s = a.slot[t * a.top + j];
+      const float w = a.weight ? a.weight[t * a.top + j] : 1.f;
+      Pack<Z> k{};
+      if (s >= 0 && s < a.slots) k = load((const Z*)a.z + s * a.ldz, c, a.n);
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) acc[i] += w * value(k.v[i]);
+    }
+    store((Y*)a.y + t * a.ldy, c, a.n, acc);
+  }
+}
+
+struct BackArgs {
+  const void* dy;
+  int64_t rows, n, lddy;
+  const void* z;
+  int64_t slots, ldz;
+  const int32_t* slot;
+  const float* weight;
+  int top;
+  void* dz;
+  int64_t lddz;
+  float* dweight;
+};
+
+// A row per workgroup of WAVES, KB choices at a time.
+constexpr int KB = 8;
+template <typename D, typename Z, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
+  __shared__ float sums[WAVES][KB];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    const D* dy = (const D*)a.dy + t * a.lddy;
+    for (int j0 = 0; j0 < a.top; j0 += KB) {
+      int s[KB];
+      float w[KB], dot[KB];
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+        const int64_t at = t * a.top + min(j0 + j, a.top - 1);
+        const int k = a.slot[at];
+        s[j] = j0 + j < a.top && k >= 0 && k < a.slots ? k : -1;
+        w[j] = a.weight ? a.weight[at] : 1.f;
+        dot[j] = 0.f;
+      }
+      for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
+        const Pack<D> d = load(dy, c, a.n);
+#pragma unroll
+        for (int j = 0; j < KB; ++j) {
+          if (s[j] < 0) continue;
+          if (a.dweight) {
+            const Pack<Z> z = load((const Z*)a.z + s[j] * a.ldz, c, a.n);
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[j] += value(d.v[i]) * value(z.v[i]);
+          }
+          if (a.dz) {
+            float v[VEC];
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) v[i] = w[j] * value(d.v[i]);
+            store((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
+          }
+        }
+      }
+      if (!a.dweight) continue;
+#pragma unroll
+      for (int j = 0; j < KB; ++j) {
+#pragma unroll
+        for (int o = 1; o < 64; o <<= 1) dot[j] += __shfl_xor(dot[j], o);
+        if (lane == 0) sums[wave][j] = dot[j];
+      }
+      __syncthreads();
+      if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.top) {
+        float v = 0.f;
+        for (int k = 0; k < WAVES; ++k) v += sums[k][threadIdx.x];
+        a.dweight[t * a.top + j0 + threadIdx.x] = v;
+      }
+      __syncthreads();
+    }
+  }
+}
+
+bool typed(int t) { return t == KQ_F32 || t == KQ_BF16; }
+bool off_type(const void* p, int t) { return (uintptr_t)p & (t == KQ_F32 ? 3 : 1); }
+
+constexpr int64_t MAX_ROWS = (int64_t)1 << 30, MAX_N = (int64_t)1 << 24;
+
+// What both directions ask of z's slots, the choices and the rows.
+kq_status check_choices(const char* fn, int z_type, int64_t slots, int64_t n, int64_t ldz, const int32_t* slot, const float* weight,
+                        int64_t rows, int top) {
+  if (!typed(z_type)) return fail(KQ_EINVAL, "%s: z of type %d", fn, z_type);
+  if (rows < 0 || rows > MAX_ROWS || slots < 0 || slots > MAX_ROWS || n < 1 || n > MAX_N)
+    return fail(KQ_ESHAPE, "%s: %lld rows, %lld slots of %lld values", fn, (long long)rows, (long long)slots, (long long)n);
+  if (top < 1 || top > MAX_TOP || rows * top > 0x7fffffff) return fail(KQ_ESHAPE, "%s: top %d (1 .. %d) of %lld rows", fn, top, MAX_TOP, (long long)rows);
+  if (ldz < n) return fail(KQ_ESHAPE, "%s: ldz %lld < %lld", fn, (long long)ldz, (long long)n);
+  if (rows > 0 && !slot) return fail(KQ_EINVAL, "%s: NULL slot", fn);
+  if (((uintptr_t)slot | (uintptr_t)weight) & 3) return fail(KQ_EINVAL, "%s: slot or weight not aligned", fn);
+  return KQ_OK;
+}
+
+template <typename Z, typename Y, typename R>
+kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
+  const int64_t blocks = std::min<int64_t>(ceil_div(a.rows * a.chunks, 256), 1 << 30);
+  combine_kernel<Z, Y, R><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+  KQ_LAUNCHED("combine_kernel");
+  return KQ_OK;
+}
+
+template <typename D, typename Z>
+kq_status launch_backward(const BackArgs& a, hipStream_t s) {
+  const dim3 grid((unsigned)a.rows);
+  if (a.n <= 64 * VEC * 4)
+    combine_backward_kernel<D, Z, 1><<<grid, dim3(64), 0, s>>>(a);
+  else
+    combine_backward_kernel<D, Z, 4><<<grid, dim3(256), 0, s>>>(a);
+  KQ_LAUNCHED("combine_backward_kernel");
+  return KQ_OK;
+}
+
+}  // namespace
+}  // namespace kq
+
+extern "C" kq_status kq_combine(const void* z, int z_type, int64_t slots, int64_t n, int64_t ldz, const int32_t* slot,
+                                const float* weight, int64_t rows, int top, const void* residual, int residual_type,
+                                int64_t ldr, void* y, int y_type, int64_t ldy, void* stream) {
+  using namespace kq;
+  const char* fn = "kq_combine";
+  KQ_TRY(check_choices(fn, z_type, slots, n, ldz, slot, weight, rows, top));
+  if (!typed(y_type)) return fail(KQ_EINVAL, "%s: y of type %d", fn, y_type);
+  if (ldy < n) return fail(KQ_ESHAPE, "%s: ldy %lld < %lld", fn, (long long)ldy, (long long)n);
+  if (rows > 0 && !y) return fail(KQ_EINVAL, "%s: NULL y", fn);
+  if (rows > 0 && slots > 0 && !z) return fail(KQ_EINVAL, "%s: NULL z", fn);
+  if (off_type(z, z_type) || off_type(y, y_type)) return fail(KQ_EINVAL, "%s: z or y not aligned to its type", fn);
+  if (residual) {
+    if (!typed(residual_type)) return fail(KQ_EINVAL, "%s: residual of type %d", fn, residual_type);
+    if (ldr < n) return fail(KQ_ESHAPE, "%s: ldr %lld < %lld", fn, (long long)ldr, (long long)n);
+    if (off_type(residual, residual_type)) return fail(KQ_EINVAL, "%s: residual not aligned to its type", fn);
+  }
+  if (rows == 0) return KQ_OK;
+  const CombineArgs a{z, slots, n, ldz, slot, weight, rows, top, residual, ldr, y, ldy, ceil_div(n, VEC)};
+  hipStream_t s = as_stream(stream);
+#define KQ_COMBINE(Z, Y) \
+  (residual_type == KQ_F32 || !residual ? launch_combine<Z, Y, float>(a, s) : launch_combine<Z, Y, uint16_t>(a, s))
+  if (z_type == KQ_F32) return y_type == KQ_F32 ? KQ_COMBINE(float, float) : KQ_COMBINE(float, uint16_t);
+  return y_type == KQ_F32 ? KQ_COMBINE(uint16_t, float) : KQ_COMBINE(uint16_t, uint16_t);
+#undef KQ_COMBINE
+}
+
+extern "C" kq_status kq_combine_backward(const void* dy, int dy_type, int64_t rows, int64_t n, int64_t lddy, const void* z,
+                                         int z_type, int64_t slots, int64_t ldz, const int32_t* slot, const float* weight,
+                                         int top, void* dz_opt, int64_t lddz, float* dweight_opt, void* stream) {
+  using namespace kq;
+  const char* fn = "kq_combine_backward";
+  KQ_TRY(check_choices(fn, z_type, slots, n, ldz, slot, weight, rows, top));
+  if (!typed(dy_type)) return fail(KQ_EINVAL, "%s: dy of type %d", fn, dy_type);
+  if (lddy < n) return fail(KQ_ESHAPE, "%s: lddy %lld < %lld", fn, (long long)lddy, (long long)n);
+  if (rows > 0 && !dy) return fail(KQ_EINVAL, "%s: NULL dy", fn);
+  if (rows > 0 && slots > 0 && dweight_opt && !z) return fail(KQ_EINVAL, "%s: NULL z", fn);
+  if (dz_opt && lddz < n) return fail(KQ_ESHAPE, "%s: lddz %lld < %lld", fn, (long long)lddz, (long long)n);
+  if (off_type(dy, dy_type) || off_type(z, z_type) || off_type(dz_opt, z_type) || ((uintptr_t)dweight_opt & 3))
+    return fail(KQ_EINVAL, "%s: an argument is not aligned to its type", fn);
+  if (rows == 0 || (!dz_opt && !dweight_opt)) return KQ_OK;
+  const BackArgs a{dy, rows, n, lddy, z, slots, ldz, slot, weight, top, dz_opt, lddz, dweight_opt};
+  hipStream_t s = as_stream(stream);
+  if (dy_type == KQ_F32) return z_type == KQ_F32 ? launch_backward<float, float>(a, s) : launch_backward<float, uint16_t>(a, s);
+  return z_type == KQ_F32 ? launch_backward<uint16_t, float>(a, s) : launch_backward<uint16_t, uint16_t>(a, s);
+}

@@ -75,7 +75,7 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
 // product (16 rows, 11008 x 4096: 24 MB, 7.7 us; 2 experts of it for one token: 48 MB, 15.3 us with
 // the token's rotation).
 // T: void for quantised activations, else their type, quantised here (MT = 1).
-template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE>
+template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE, int EPI>
 __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, RowArgs x) {
   constexpr bool FUSED = !__is_void(T);
   constexpr int BM = 16 * MT, BN = 16 * NT, LD = BN + 4;
@@ -95,12 +95,13 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
   const int pairs = (a.steps + 1) / 2, per = (pairs + WAVES - 1) / WAVES;
   const int p0 = wave * per, p1 = min(p0 + per, pairs);
 
-  const uint8_t* wc = a.wc + ((int64_t)t.e * a.N + t.n0) * a.pitch;
-  const uint8_t* ws = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
+  const int w0 = first_row<EPI>(t.n0);
+  const uint8_t* wc = a.wc + ((int64_t)t.e * a.N + w0) * a.pitch;
+  const uint8_t* ws = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)w0 * 4;
   unsigned ow[NT], os[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    const unsigned r = (unsigned)min((int64_t)16 * n + l16, a.N - 1 - t.n0);
+    const unsigned r = (unsigned)layer_row<EPI>(a, t.n0, 16 * n + l16);
     ow[n] = r * (unsigned)a.pitch + 32 * q;
     os[n] = r * 4;
   }
@@ -205,14 +206,31 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
     for (int n = 0; n < NT; ++n)
       *(f32x4*)(lds + ((wave * BM + 16 * m + l16) * LD + 16 * n + 4 * q)) = acc[m][n];
   __syncthreads();
-  const int count = (t.last - t.m0) * BN;
+  constexpr int PAIR = EPI == EPI_GATED ? 2 : 1, COLS = BN / PAIR;
+  const int count = (t.last - t.m0) * COLS;
   for (int o = threadIdx.x; o < count; o += 64 * WAVES) {
-    const int r = o / BN, c = o % BN;
+    const int r = o / COLS, c = o % COLS;
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += lds[(w * BM + r) * LD + c];
-    if (t.n0 + c >= a.N) continue;
-    const int64_t at = (t.m0 + r) * a.ldy + t.n0 + c;
+    for (int w = 0; w < WAVES; ++w) v += lds[(w * BM + r) * LD + PAIR * c];
+    if (t.n0 + PAIR * c >= a.N) continue;
+    if constexpr (EPI != EPI_NONE) {
+      const float* bias = a.bias + (int64_t)t.e * a.N + w0 + c;
+      if (a.bias) v += *bias;
+      v = activate(a.act, v);
+      if constexpr (EPI == EPI_GATED) {
+        float u = 0.f;
+#pragma unroll
+        for (int w = 0; w < WAVES; ++w) u += lds[(w * BM + r) * LD + 2 * c + 1];
+        if (a.bias) u += bias[a.N >> 1];
+        v *= u;
+      }
+      if (a.residual) {
+        const int64_t from = (t.m0 + r) * a.ldr + w0 + c;
+        v += a.r_bf16 ? __uint_as_float((unsigned)((const uint16_t*)a.residual)[from] << 16) : ((const float*)a.residual)[from];
+      }
+    }
+    const int64_t at = (t.m0 + r) * a.ldy + w0 + c;
     if (a.y_bf16)
       ((uint16_t*)a.y)[at] = to_bf16(v);
     else
@@ -220,8 +238,8 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
   }
 }
 
-template <int WAVES, int MT, int NT, int U, typename T, bool WIDE = true>
-kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
+template <int WAVES, int MT, int NT, int U, typename T, bool WIDE, int EPI>
+kq_status launch_epi(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
   constexpr int BM = 16 * MT, BN = 16 * NT;
   const int64_t tm = ceil_div(p.slots, BM) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
   size_t bytes = sizeof(float) * (size_t)WAVES * BM * (BN + 4);
@@ -229,12 +247,21 @@ kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
     bytes = std::max(bytes, sizeof(float) * (size_t)rotate_floats(WAVES) +
                                 (size_t)std::min<int64_t>(p.slots, BM) * (size_t)(p.pitch + 4 * p.steps));
   const dim3 grid((unsigned)ceil_div(p.N, BN), (unsigned)tm), block(64 * WAVES);
-  const auto kernel = p.offsets ? mx_few_kernel<WAVES, MT, NT, U, true, T, WIDE> : mx_few_kernel<WAVES, MT, NT, U, false, T, WIDE>;
+  const auto kernel = p.offsets ? mx_few_kernel<WAVES, MT, NT, U, true, T, WIDE, EPI> : mx_few_kernel<WAVES, MT, NT, U, false, T, WIDE, EPI>;
   if (bytes > 64 * 1024)
     KQ_HIP(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)bytes));
   kernel<<<grid, block, bytes, s>>>(p, x);
   KQ_LAUNCHED("mx_few_kernel");
   return KQ_OK;
+}
+
+template <int WAVES, int MT, int NT, int U, typename T, bool WIDE = true>
+kq_status launch(const ProductArgs& p, const RowArgs& x, hipStream_t s) {
+  switch (p.epi) {
+    case EPI_GATED: return launch_epi<WAVES, MT, NT, U, T, WIDE, EPI_GATED>(p, x, s);
+    case EPI_PLAIN: return launch_epi<WAVES, MT, NT, U, T, WIDE, EPI_PLAIN>(p, x, s);
+    default: return launch_epi<WAVES, MT, NT, U, T, WIDE, EPI_NONE>(p, x, s);
+  }
 }
 
 // Rows per expert, on average.

@@ -143,7 +143,7 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 // 128 x 128 tiles: 55 us, 3.3 PF; with 256 x 256, on half as many workgroups, 71.
 // RING: stages in LDS; four where a tile is small (256 x 10496 x 2914: 14 us, with two and more
 // workgroups side by side 21).
-template <int MT, int NT, int WC, int RING, int ROWS>
+template <int MT, int NT, int WC, int RING, int ROWS, int EPI>
 __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
   constexpr int CA = 4 * MT / WC, CB = 2 * NT;        // copies of x and of W per wave and stage
@@ -191,14 +191,14 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
       const int x = row_of_x(min(r, t.last - 1 - t.m0));
       return x >= 0 && x < a.rows ? x : -1;
     };
-    auto w_row = [&](int r) -> unsigned { return (unsigned)min((int64_t)r, a.N - 1 - t.n0); };
+    auto w_row = [&](int r) -> unsigned { return (unsigned)layer_row<EPI>(a, t.n0, r); };
     issued = 0;
     int ln = lane;
     asm volatile("" : "+v"(ln));   // the positions computed here, not kept in registers for every tile
     xc = a.xc + (ROWS == X_ROWS ? t.m0 * a.pitch : 0);
     xs = a.xs + (ROWS == X_ROWS ? (int64_t)t.m0 * 4 : 0);
-    wc_e = a.wc + ((int64_t)t.e * a.N + t.n0) * a.pitch;
-    ws_e = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)t.n0 * 4;
+    wc_e = a.wc + ((int64_t)t.e * a.N + first_row<EPI>(t.n0)) * a.pitch;
+    ws_e = a.ws + (int64_t)t.e * a.N * (4 * a.steps) + (int64_t)first_row<EPI>(t.n0) * 4;
 #pragma unroll
     for (int r = 0; r < CA; ++r) {
       const int pos = (wave * CA + r) * 8 + (ln >> 3), p = pos % (32 * MT);
@@ -463,7 +463,58 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
         asm volatile("" : "+a"(v[k]));
       }
     };
-    if (!a.y_far && (t.n0 + BN <= a.N || a.N % NT == 0)) {
+    if constexpr (EPI != EPI_NONE) {
+      // PAIR columns of the layer make one of y; of two lanes that hold a pair (NT = 1) the first stores
+      constexpr int PAIR = EPI == EPI_GATED ? 2 : 1, W = NT >= PAIR ? NT / PAIR : 1;
+      const int64_t cols = a.N / PAIR, c0 = n / PAIR;   // columns of y; the lane's first
+      const int f0 = first_row<EPI>(t.n0), mine = (int)(cols - c0 < 0 ? 0 : cols - c0 < W ? cols - c0 : W);
+      const bool first = NT >= PAIR || (lane & 1) == 0;
+      float bias[NT];
+#pragma unroll
+      for (int k = 0; k < NT; ++k) {
+        const int v = n - t.n0 + k;
+        bias[k] = a.bias ? a.bias[(int64_t)t.e * a.N + f0 + layer_row<EPI>(a, t.n0, v)] : 0.f;
+      }
+      int part = q;
+      asm volatile("" : "+v"(part));   // its addresses computed here, not ahead of the loop
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        f32x16 sums[NT];
+        take(m, sums);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int r = wr * 32 * MT + ((j >> 2) * 8 + part * 4 + (j & 3)) * MT + m;
+          float v[NT];
+#pragma unroll
+          for (int k = 0; k < NT; ++k) v[k] = sums[k][j] + bias[k];
+          if constexpr (EPI == EPI_GATED) {
+            const float other = NT == 1 ? __shfl_xor(v[0], 1) : v[NT - 1];
+            v[0] = activate(a.act, v[0]) * other;
+          } else {
+#pragma unroll
+            for (int k = 0; k < NT; ++k) v[k] = activate(a.act, v[k]);
+          }
+          if (r < rows && first) {
+            const int64_t row = t.m0 + r;
+#pragma unroll
+            for (int k = 0; k < W; ++k)
+              if (k < mine) {
+                float o = v[k];
+                if (a.residual) {
+                  const int64_t from = row * a.ldr + c0 + k;
+                  o += a.r_bf16 ? __uint_as_float((unsigned)((const uint16_t*)a.residual)[from] << 16) : ((const float*)a.residual)[from];
+                }
+                const int64_t at = row * a.ldy + c0 + k;
+                if (a.y_bf16)
+                  ((uint16_t*)a.y)[at] = to_bf16(o);
+                else
+                  ((float*)a.y)[at] = o;
+              }
+          }
+        }
+      }
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));   // fewer stores than the next round's waits count on
+    } else if (!a.y_far && (t.n0 + BN <= a.N || a.N % NT == 0)) {
       const int pitch = (int)a.ldy * size;
       const __amdgpu_buffer_rsrc_t ry = rsrc(y0, rows < BM ? rows * pitch : OOB);
       const int first = (wr * 32 * MT + q * 4 * MT) * pitch + (wc * 32 + l32) * NT * size;
@@ -537,7 +588,7 @@ int64_t row_tiles(const ProductArgs& p, int bm) {
   return ceil_div(p.slots, bm) + (p.offsets ? std::min<int64_t>(p.experts, p.slots) : 0);
 }
 
-template <int MT, int NT, int WC, int RING>
+template <int MT, int NT, int WC, int RING, int EPI>
 kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC;
   // one workgroup for each place on the card, or for each tile if there are fewer
@@ -546,13 +597,22 @@ kq_status launch_tiles(const ProductArgs& p, hipStream_t s) {
                                           ceil_div(device_cu_count() * std::min(PLACES, 4), 8)) * 8;
   const dim3 grid((unsigned)total), block(128 * WC);
   if (!p.offsets)
-    mx_tile_kernel<MT, NT, WC, RING, X_ROWS><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_ROWS, EPI><<<grid, block, 0, s>>>(p);
   else if (!x_far(p))
-    mx_tile_kernel<MT, NT, WC, RING, X_INDEX><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_INDEX, EPI><<<grid, block, 0, s>>>(p);
   else if constexpr (MT == 4)
-    mx_tile_kernel<MT, NT, WC, RING, X_FAR><<<grid, block, 0, s>>>(p);
+    mx_tile_kernel<MT, NT, WC, RING, X_FAR, EPI><<<grid, block, 0, s>>>(p);
   KQ_LAUNCHED("mx_tile_kernel");
   return KQ_OK;
+}
+
+template <int EPI>
+kq_status launch_size(const ProductArgs& p, int64_t tile, hipStream_t s) {
+  switch (tile) {
+    case 256: return launch_tiles<4, 2, 4, 2, EPI>(p, s);
+    case 128: return launch_tiles<2, 2, 2, 2, EPI>(p, s);
+    default: return launch_tiles<1, 1, 2, 4, EPI>(p, s);
+  }
 }
 
 // The tile with the least time.  Up to 64 rows (of an expert, on average) the layer's bytes are the
@@ -578,17 +638,18 @@ kq_status launch_best(const ProductArgs& p, hipStream_t s) {
       }
     }
   }
-  switch (p.offsets && x_far(p) ? 256 : testing_value(KQ_TESTING_MX_TILE, best)) {
-    case 256: return launch_tiles<4, 2, 4, 2>(p, s);
-    case 128: return launch_tiles<2, 2, 2, 2>(p, s);
-    default: return launch_tiles<1, 1, 2, 4>(p, s);
+  best = p.offsets && x_far(p) ? 256 : testing_value(KQ_TESTING_MX_TILE, best);
+  switch (p.epi) {
+    case EPI_GATED: return launch_size<EPI_GATED>(p, best, s);
+    case EPI_PLAIN: return launch_size<EPI_PLAIN>(p, best, s);
+    default: return launch_size<EPI_NONE>(p, best, s);
   }
 }
 
 // Checks and quantises the activations (unless they are quantised already), then the product.
-kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, void* ws, size_t ws_bytes,
-                  hipStream_t s) {
-  int64_t block = 1;
+kq_status product(const char* fn, const MxRows& x, ProductArgs p, const kq_epilogue* ep, int y_type, void* ws,
+                  size_t ws_bytes, hipStream_t s) {
+  int64_t block = 1, out = p.N;
   if (x.type == KQ_MXFP4) {
     if (x.rows < 0 || x.rows > MX_MAX_ROWS || x.n < 1 || x.n > MX_MAX_N)
       return fail(KQ_ESHAPE, "%s: %lld rows of %lld values", fn, (long long)x.rows, (long long)x.n);
@@ -601,8 +662,8 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
     if (x.scales) return fail(KQ_EINVAL, "%s: scales go with quantised rows only", fn);
   }
   if (y_type != KQ_F32 && y_type != KQ_BF16) return fail(KQ_EINVAL, "%s: output type %d", fn, y_type);
-  if (p.N < 1 || p.N > MX_MAX_N) return fail(KQ_ESHAPE, "%s: %lld output channels", fn, (long long)p.N);
-  if (p.ldy < p.N) return fail(KQ_ESHAPE, "%s: ldy %lld < %lld", fn, (long long)p.ldy, (long long)p.N);
+  if (out < 1 || out > MX_MAX_N) return fail(KQ_ESHAPE, "%s: %lld output channels", fn, (long long)out);
+  if (p.ldy < out) return fail(KQ_ESHAPE, "%s: ldy %lld < %lld", fn, (long long)p.ldy, (long long)out);
   if (!p.wc || !p.ws) return fail(KQ_EINVAL, "%s: NULL weights", fn);
   if (!aligned16(p.wc) || !aligned16(p.ws)) return fail(KQ_EINVAL, "%s: weights must be 16-byte aligned", fn);
   if (p.slots > 0 && !p.y) return fail(KQ_EINVAL, "%s: NULL output", fn);
@@ -613,6 +674,24 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, int y_type, vo
   p.rows = x.rows;
   p.y_bf16 = y_type == KQ_BF16;
   p.y_far = p.ldy > (1 << 20);
+  if (ep) {
+    if (ep->act < KQ_ACT_NONE || ep->act > KQ_ACT_GELU_TANH) return fail(KQ_EINVAL, "%s: activation %d", fn, ep->act);
+    if (ep->gated != 0 && ep->gated != 1) return fail(KQ_EINVAL, "%s: gated %d", fn, ep->gated);
+    if ((uintptr_t)ep->bias & 3) return fail(KQ_EINVAL, "%s: bias not aligned to its type", fn);
+    if (ep->gated) {
+      p.N = 2 * out;
+      if (p.N > MX_MAX_N || p.N * p.pitch >= ((int64_t)1 << 31))   // its halves lie 32-bit offsets apart
+        return fail(KQ_ESHAPE, "%s: a gated layer of %lld rows and %lld bytes of codes", fn, (long long)p.N, (long long)(p.N * p.pitch));
+    }
+    if (ep->residual) {
+      if (ep->residual_type != KQ_F32 && ep->residual_type != KQ_BF16) return fail(KQ_EINVAL, "%s: residual of type %d", fn, ep->residual_type);
+      if (ep->ldr < out) return fail(KQ_ESHAPE, "%s: ldr %lld < %lld", fn, (long long)ep->ldr, (long long)out);
+      if ((uintptr_t)ep->residual & (ep->residual_type == KQ_F32 ? 3 : 1)) return fail(KQ_EINVAL, "%s: residual not aligned to its type", fn);
+      p.y_far |= ep->ldr > (1 << 20);
+    }
+    p.epi = ep->gated ? EPI_GATED : ep->act != KQ_ACT_NONE || ep->bias || ep->residual ? EPI_PLAIN : EPI_NONE;
+    p.act = ep->act; p.bias = ep->bias; p.residual = ep->residual; p.r_bf16 = ep->residual_type == KQ_BF16; p.ldr = ep->ldr;
+  }
   if (x.type == KQ_MXFP4) {
     p.xc = (const uint8_t*)x.x;
     p.xs = x.scales;
@@ -642,16 +721,54 @@ extern "C" kq_status kq_mxfp4_workspace(int64_t rows, int64_t n, size_t* bytes) 
   return KQ_OK;
 }
 
+namespace kq {
+namespace {
+
+kq_status linear(const char* fn, const MxRows& x, const uint8_t* w_codes, const uint8_t* w_scales, int64_t out,
+                 const kq_epilogue* ep, void* y, int y_type, int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  ProductArgs p{};
+  p.wc = w_codes; p.ws = w_scales; p.N = out; p.experts = 1; p.slots = x.rows; p.y = y; p.ldy = ldy;
+  return product(fn, x, p, ep, y_type, ws, ws_bytes, as_stream(stream));
+}
+
+kq_status experts_of(const char* fn, const MxRows& x, const int32_t* index, int64_t slots, const int32_t* offsets, int experts,
+                     const uint8_t* w_codes, const uint8_t* w_scales, int64_t out, const kq_epilogue* ep, void* y, int y_type,
+                     int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
+  if (experts < 1 || experts > 4096) return fail(KQ_ESHAPE, "%s: %d experts (1 .. 4096)", fn, experts);
+  if (slots < 0 || slots > MX_MAX_ROWS) return fail(KQ_ESHAPE, "%s: %lld slots", fn, (long long)slots);
+  if (!offsets) return fail(KQ_EINVAL, "%s: NULL offsets", fn);
+  if (((uintptr_t)offsets | (uintptr_t)index) & 3) return fail(KQ_EINVAL, "%s: offsets or index not aligned", fn);
+  if (!index && slots > x.rows)
+    return fail(KQ_ESHAPE, "%s: %lld slots of %lld rows need an index", fn, (long long)slots, (long long)x.rows);
+  ProductArgs p{};
+  p.wc = w_codes; p.ws = w_scales; p.N = out; p.index = index; p.offsets = offsets; p.experts = experts;
+  p.slots = slots; p.y = y; p.ldy = ldy;
+  return product(fn, x, p, ep, y_type, ws, ws_bytes, as_stream(stream));
+}
+
+}  // namespace
+}  // namespace kq
+
 extern "C" kq_status kq_mxfp4_linear(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
                                      const uint8_t* x_scales, const float* d, const int8_t* sign,
                                      int64_t had, const uint8_t* w_codes, const uint8_t* w_scales,
                                      int64_t out, void* y, int y_type, int64_t ldy, void* ws,
                                      size_t ws_bytes, void* stream) {
   using namespace kq;
-  ProductArgs p{};
-  p.wc = w_codes; p.ws = w_scales; p.N = out; p.experts = 1; p.slots = rows; p.y = y; p.ldy = ldy;
-  return product("kq_mxfp4_linear", MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, p, y_type, ws,
-                 ws_bytes, as_stream(stream));
+  return linear("kq_mxfp4_linear", MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, w_codes, w_scales, out, nullptr,
+                y, y_type, ldy, ws, ws_bytes, stream);
+}
+
+extern "C" kq_status kq_mxfp4_linear_epilogue(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                              const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                                              const uint8_t* w_codes, const uint8_t* w_scales, int64_t out,
+                                              const kq_epilogue* epilogue, void* y, int y_type, int64_t ldy, void* ws,
+                                              size_t ws_bytes, void* stream) {
+  using namespace kq;
+  const char* fn = "kq_mxfp4_linear_epilogue";
+  if (!epilogue) return fail(KQ_EINVAL, "%s: NULL epilogue", fn);
+  return linear(fn, MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, w_codes, w_scales, out, epilogue, y, y_type, ldy,
+                ws, ws_bytes, stream);
 }
 
 extern "C" kq_status kq_mxfp4_experts(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
@@ -661,16 +778,19 @@ extern "C" kq_status kq_mxfp4_experts(const void* x, int x_type, int64_t rows, i
                                       const uint8_t* w_scales, int64_t out, void* y, int y_type,
                                       int64_t ldy, void* ws, size_t ws_bytes, void* stream) {
   using namespace kq;
-  const char* fn = "kq_mxfp4_experts";
-  if (experts < 1 || experts > 4096) return fail(KQ_ESHAPE, "%s: %d experts (1 .. 4096)", fn, experts);
-  if (slots < 0 || slots > MX_MAX_ROWS) return fail(KQ_ESHAPE, "%s: %lld slots", fn, (long long)slots);
-  if (!offsets) return fail(KQ_EINVAL, "%s: NULL offsets", fn);
-  if (((uintptr_t)offsets | (uintptr_t)index) & 3) return fail(KQ_EINVAL, "%s: offsets or index not aligned", fn);
-  if (!index && slots > rows)
-    return fail(KQ_ESHAPE, "%s: %lld slots of %lld rows need an index", fn, (long long)slots, (long long)rows);
-  ProductArgs p{};
-  p.wc = w_codes; p.ws = w_scales; p.N = out; p.index = index; p.offsets = offsets; p.experts = experts;
-  p.slots = slots; p.y = y; p.ldy = ldy;
-  return product(fn, MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, p, y_type, ws, ws_bytes,
-                 as_stream(stream));
+  return experts_of("kq_mxfp4_experts", MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, index, slots, offsets, experts,
+                    w_codes, w_scales, out, nullptr, y, y_type, ldy, ws, ws_bytes, stream);
+}
+
+extern "C" kq_status kq_mxfp4_experts_epilogue(const void* x, int x_type, int64_t rows, int64_t in, int64_t ldx,
+                                               const uint8_t* x_scales, const float* d, const int8_t* sign, int64_t had,
+                                               const int32_t* index, int64_t slots, const int32_t* offsets, int experts,
+                                               const uint8_t* w_codes, const uint8_t* w_scales, int64_t out,
+                                               const kq_epilogue* epilogue, void* y, int y_type, int64_t ldy, void* ws,
+                                               size_t ws_bytes, void* stream) {
+  using namespace kq;
+  const char* fn = "kq_mxfp4_experts_epilogue";
+  if (!epilogue) return fail(KQ_EINVAL, "%s: NULL epilogue", fn);
+  return experts_of(fn, MxRows{x, x_type, rows, in, ldx, x_scales, d, sign, had}, index, slots, offsets, experts, w_codes,
+                    w_scales, out, epilogue, y, y_type, ldy, ws, ws_bytes, stream);
 }

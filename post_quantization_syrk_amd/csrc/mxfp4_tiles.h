@@ -21,9 +21,33 @@ struct ProductArgs {
   int64_t slots;
   void* y;
   bool y_bf16;
-  bool y_far;              // rows of y too far apart for 32-bit offsets inside a tile
+  bool y_far;              // rows of y (or of the residual) too far apart for 32-bit offsets inside a tile
   int64_t ldy;
+  int epi;                 // EPI_*; what it applies:
+  int act;
+  const float* bias;       // experts x N, or NULL
+  const void* residual;    // or NULL
+  bool r_bf16;
+  int64_t ldr;
 };
+
+// What a product applies to its sums: nothing, act(sum + bias) + residual, or that with pairs of
+// columns, act(sum + bias) * (other sum + its bias) + residual.  A gated layer's N rows are those of
+// the gate, then as many others; its columns are taken in pairs, so that both of a pair lie in one
+// lane (or two neighbouring ones): column v is row v / 2 of the half v % 2.
+enum { EPI_NONE, EPI_PLAIN, EPI_GATED };
+
+// Row of the layer, from the first row of a tile at column n0, of column n0 + r.
+template <int EPI>
+__device__ __forceinline__ int64_t layer_row(const ProductArgs& a, int n0, int64_t r) {
+  const int64_t c = r < a.N - 1 - n0 ? r : a.N - 1 - n0;   // (past the last column: that one)
+  return EPI == EPI_GATED ? (c & 1) * (a.N >> 1) + (c >> 1) : c;
+}
+// The first row of a tile at column n0, and the column of y where it begins.
+template <int EPI>
+__device__ __forceinline__ int first_row(int n0) {
+  return EPI == EPI_GATED ? n0 >> 1 : n0;
+}
 
 // A product with few rows (mxfp4_few.hip): whether it is one, whether it quantises the rows of x
 // itself, and its launch (not fused: the rows are quantised, at p.xc and p.xs).
@@ -53,6 +77,21 @@ __device__ __forceinline__ void expert_ranges(const ProductArgs& a, int e0, int&
     last = max(last, first);
   }
   top = __builtin_amdgcn_readlane(last, 63);
+}
+
+// act(v).  2^(v log2 e) from the hardware's exponential: the product's rounding puts a relative error
+// of |v| 2^-24 on it, which is at most 3e-8 of an activation's value next to 1.
+__device__ __forceinline__ float sigmoid_times(float v, float u) {   // v / (1 + exp(-u))
+  return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * u));
+}
+__device__ __forceinline__ float activate(int act, float v) {
+  switch (act) {
+    case KQ_ACT_RELU: return v < 0.f ? 0.f : v;
+    case KQ_ACT_SILU: return sigmoid_times(v, v);
+    case KQ_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.707106781f));
+    case KQ_ACT_GELU_TANH: return sigmoid_times(v, 1.59576912f * (v + 0.044715f * v * v * v));   // 1 + tanh u = 2 / (1 + exp(-2 u))
+    default: return v;
+  }
 }
 
 // Rows [m0, last) of y with expert e's layer, columns from n0: one tile.
