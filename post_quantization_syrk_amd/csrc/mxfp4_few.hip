@@ -217,7 +217,9 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
     if constexpr (EPI != EPI_NONE) {
       const float* bias = a.bias + (int64_t)t.e * a.N + w0 + c;
       if (a.bias) v += *bias;
-      v = activate(a.act, v);
+      float half[1] = {v};
+      activate(a.act, half);
+      v = half[0];
       if constexpr (EPI == EPI_GATED) {
         float u = 0.f;
 #pragma unroll

@@ -3,6 +3,7 @@
 #include "mxfp4_tiles.h"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace kq {
 namespace {
@@ -131,6 +132,12 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
     __builtin_amdgcn_raw_buffer_store_b16(to_bf16(v[0]), r, off, 0, 0);
 }
 
+// The value of the neighbouring lane (lanes 2 i and 2 i + 1 in each other's place).
+__device__ __forceinline__ float other_lane(float v) {
+  const int u = __float_as_int(v);
+  return __int_as_float(__builtin_amdgcn_update_dpp(u, u, 0xb1, 0xf, 0xf, true));
+}
+
 // Tiles of BM x BN outputs, 256 of K per stage, waves in 2 x WC, each with MT x NT accumulators
 // of 32 x 32.  A stage is 128 bytes of every row, a whole line: with 64, the
 // copies alone of an 8192 x 8192 x 8192 product took 170 us, with 128 107 us.  A workgroup takes
@@ -144,7 +151,7 @@ __device__ __forceinline__ void store_bf16(__amdgpu_buffer_rsrc_t r, int off, co
 // RING: stages in LDS; four where a tile is small (256 x 10496 x 2914: 14 us, with two and more
 // workgroups side by side 21).
 template <int MT, int NT, int WC, int RING, int ROWS, int EPI>
-__global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
+__global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void mx_tile_kernel(ProductArgs a) {
   constexpr int BM = 64 * MT, BN = 32 * NT * WC, PANEL_A = BM * 128, PANELS = (BM + BN) * 128;
   constexpr int CA = 4 * MT / WC, CB = 2 * NT;        // copies of x and of W per wave and stage
   constexpr int SI = (BM + BN) / 64, SC = (SI + 2 * WC - 1) / (2 * WC);   // scale copies of 128 of K: all, per wave
@@ -156,6 +163,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   __shared__ __attribute__((aligned(1024))) uint8_t b2[RING == 4 ? STAGE : 1024];
   __shared__ __attribute__((aligned(1024))) uint8_t b3[RING == 4 ? STAGE : 1024];
   __shared__ ExpertTable tab[1];
+  __shared__ __attribute__((aligned(256))) float bias_lds[EPI != EPI_NONE ? 2 : 1][EPI != EPI_NONE ? BN : 1];
   __shared__ __attribute__((aligned(256))) int next_index[ROWS == X_ROWS ? 64 : BM];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -402,6 +410,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
   };
   const int rounds = (stages + RING - 1) / RING;   // stages past the last multiply zeros
   bool stored = false;
+  int turn = 0;   // tiles done
   const int size = a.y_bf16 ? 2 : 4;
 
   for (;;) {
@@ -416,6 +425,13 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     if (ROWS != X_ROWS && more && a.index) {
       const int r = min(64 * (wave % MT) + lane, nt.last - 1 - nt.m0);
       copy_lds<4>(rsrc(a.index + nt.m0, (int)ALL), 4 * r, (uint8_t*)(next_index + 64 * (wave % MT)));
+    }
+    // The tile's bias, by column, behind the next one's in time: waves may still read the last
+    // tile's.  Older than every copy of this tile's last stage, it has landed when that one's have.
+    if (EPI != EPI_NONE && a.bias) {
+      const int c = 64 * (wave % (BN / 64));
+      copy_lds<4>(rsrc(a.bias + (int64_t)t.e * a.N + first_row<EPI>(t.n0), (int)ALL),
+                  4 * (unsigned)layer_row<EPI>(a, t.n0, c + lane), (uint8_t*)(bias_lds[turn & 1] + c));
     }
     // the next tile's copies follow the last ones of this tile: those of its last round
     auto aim_next = [&]() {
@@ -464,56 +480,165 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
       }
     };
     if constexpr (EPI != EPI_NONE) {
-      // PAIR columns of the layer make one of y; of two lanes that hold a pair (NT = 1) the first stores
+      // PAIR columns of the layer make W of y in a lane; of two lanes that hold a pair between them
+      // (NT = 1) the first one stores.
       constexpr int PAIR = EPI == EPI_GATED ? 2 : 1, W = NT >= PAIR ? NT / PAIR : 1;
-      const int64_t cols = a.N / PAIR, c0 = n / PAIR;   // columns of y; the lane's first
-      const int f0 = first_row<EPI>(t.n0), mine = (int)(cols - c0 < 0 ? 0 : cols - c0 < W ? cols - c0 : W);
-      const bool first = NT >= PAIR || (lane & 1) == 0;
+      const int64_t cols = a.N / PAIR;
+      const int col = (wc * 32 + l32) * NT / PAIR, f0 = first_row<EPI>(t.n0);
+      const bool stores = NT >= PAIR || (lane & 1) == 0;
       float bias[NT];
 #pragma unroll
-      for (int k = 0; k < NT; ++k) {
-        const int v = n - t.n0 + k;
-        bias[k] = a.bias ? a.bias[(int64_t)t.e * a.N + f0 + layer_row<EPI>(a, t.n0, v)] : 0.f;
-      }
-      int part = q;
-      asm volatile("" : "+v"(part));   // its addresses computed here, not ahead of the loop
+      for (int k = 0; k < NT; ++k)
+        bias[k] = a.bias ? __int_as_float(read_lds((const int*)(bias_lds[turn & 1] + (wc * 32 + l32) * NT + k))) : 0.f;
+      // Four rows of the lane's, rows 8 g + 4 q of m's: their values
+      auto finish = [&](const f32x16 (&sums)[NT], int g, float (&v)[4 * W]) {
+        float s[NT][4];
 #pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        f32x16 sums[NT];
-        take(m, sums);
+        for (int k = 0; k < NT; ++k)
 #pragma unroll
-        for (int j = 0; j < 16; ++j) {
-          const int r = wr * 32 * MT + ((j >> 2) * 8 + part * 4 + (j & 3)) * MT + m;
-          float v[NT];
+          for (int i = 0; i < 4; ++i) s[k][i] = sums[k][4 * g + i] + bias[k];
+        activate(a.act, s[0]);
+        if constexpr (EPI == EPI_PLAIN && NT == 2) activate(a.act, s[NT - 1]);
 #pragma unroll
-          for (int k = 0; k < NT; ++k) v[k] = sums[k][j] + bias[k];
+        for (int i = 0; i < 4; ++i) {
           if constexpr (EPI == EPI_GATED) {
-            const float other = NT == 1 ? __shfl_xor(v[0], 1) : v[NT - 1];
-            v[0] = activate(a.act, v[0]) * other;
+            v[i] = NT == 2 ? s[0][i] * s[NT - 1][i] : s[0][i] * other_lane(sums[0][4 * g + i] + bias[0]);
           } else {
 #pragma unroll
-            for (int k = 0; k < NT; ++k) v[k] = activate(a.act, v[k]);
+            for (int k = 0; k < W; ++k) v[i * W + k] = s[k][i];
           }
-          if (r < rows && first) {
-            const int64_t row = t.m0 + r;
+        }
+      };
+      if (!a.y_far && (W == 1 || t.n0 + BN <= a.N || a.N % NT == 0)) {
+        // Step k: rows 8 (k % 4) + 4 q .. + 3 of m = k / 4.  The four rows' offsets are the same in every
+        // step, from a base that moves on (64 offsets of their own would spill).
+        const int r_size = a.r_bf16 ? 2 : 4, pitch = (int)a.ldy * size, r_pitch = (int)a.ldr * r_size;
+        uint8_t* y1 = (uint8_t*)a.y + ((int64_t)t.m0 * a.ldy + f0) * size;
+        const uint8_t* r1 = (const uint8_t*)a.residual + ((int64_t)t.m0 * a.ldr + f0) * r_size;
+        auto view = [&](const uint8_t* base, int bytes, int k) {
+          const int back = (8 * (k % 4) * MT + k / 4) * bytes;
+          return rsrc(base + back, rows < BM ? max(rows * bytes - back, 0) : OOB);
+        };
+        const int row0 = wr * 32 * MT + q * 4 * MT;
+        const bool in = stores && f0 + col + W <= cols;
+        const int at = in ? row0 * pitch + col * size : OOB;   // (masked, and so it is with rows added)
+        const int from = in ? row0 * r_pitch + col * r_size : OOB;
+        // Residuals are read ahead, since a step is far shorter than a read takes: four steps of one dword
+        // (two bf16 values, or one value) per row, two steps of two.
+        constexpr int STEPS = 4 * MT;
+        u32x16 raw{};
+        auto fetch = [&](int k, auto words) {
+          constexpr int D = decltype(words)::value;
+          const __amdgpu_buffer_rsrc_t rr = view(r1, r_pitch, k);
+          int lane_from = from;
+          asm volatile("" : "+v"(lane_from));
 #pragma unroll
-            for (int k = 0; k < W; ++k)
-              if (k < mine) {
-                float o = v[k];
-                if (a.residual) {
-                  const int64_t from = row * a.ldr + c0 + k;
+          for (int i = 0; i < 4; ++i) {
+            const int off = lane_from + i * MT * r_pitch, to = D * (4 * k % (16 / D) + i);
+            if constexpr (D == 2) {
+              const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(rr, off, 0, 0);
+              raw[to] = u[0];
+              raw[to + 1] = u[1];
+            } else {
+              raw[to] = __builtin_amdgcn_raw_buffer_load_b32(rr, off, 0, 0);
+            }
+          }
+        };
+        auto fetch_half = [&](int k) {   // one bf16 value per row
+          const __amdgpu_buffer_rsrc_t rr = view(r1, r_pitch, k);
+          int lane_from = from;
+          asm volatile("" : "+v"(lane_from));
+#pragma unroll
+          for (int i = 0; i < 4; ++i) raw[4 * (k % 4) + i] = __builtin_amdgcn_raw_buffer_load_b16(rr, lane_from + i * MT * r_pitch, 0, 0);
+        };
+        auto fetch_ahead = [&](int k, int first, int count) {   // steps k + first .. of this residual's distance
+          if (W == 1 && a.r_bf16) {
+#pragma unroll
+            for (int j = 0; j < count; ++j)
+              if (k + first + j < STEPS) fetch_half(k + first + j);
+          } else if (W == 1 || a.r_bf16) {
+#pragma unroll
+            for (int j = 0; j < count; ++j)
+              if (k + first + j < STEPS) fetch(k + first + j, std::integral_constant<int, 1>());
+          } else {
+#pragma unroll
+            for (int j = 0; j < (count + 1) / 2; ++j)
+              if (k + first / 2 + j < STEPS) fetch(k + first / 2 + j, std::integral_constant<int, 2>());
+          }
+        };
+        if (a.residual) fetch_ahead(0, 0, 4);
+        f32x16 sums[NT];
+#pragma unroll
+        for (int k = 0; k < STEPS; ++k) {
+          if (k % 4 == 0) take(k / 4, sums);
+          __builtin_amdgcn_sched_barrier(0);
+          float v[4 * W];
+          finish(sums, k % 4, v);
+          if (a.residual) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if constexpr (W == 1) {
+                const unsigned u = raw[4 * (k % 4) + i];
+                v[i] += __uint_as_float(a.r_bf16 ? u << 16 : u);
+              } else {
+                const unsigned u = raw[4 * (k % 4) + i], f0 = raw[8 * (k % 2) + 2 * i], f1 = raw[8 * (k % 2) + 2 * i + 1];
+                v[2 * i] += __uint_as_float(a.r_bf16 ? u << 16 : f0);
+                v[2 * i + 1] += __uint_as_float(a.r_bf16 ? u & 0xffff0000u : f1);
+              }
+            }
+            fetch_ahead(k, 4, 1);
+          }
+          const __amdgpu_buffer_rsrc_t ry = view(y1, pitch, k);
+          int lane_at = at;
+          asm volatile("" : "+v"(lane_at));
+          auto store = [&](auto put) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float o[W];
+#pragma unroll
+              for (int c = 0; c < W; ++c) o[c] = v[i * W + c];
+              put(lane_at + i * MT * pitch, o);
+            }
+          };
+          if (a.y_bf16)
+            store([&](int off, const float (&o)[W]) { store_bf16<W>(ry, off, o); });
+          else
+            store([&](int off, const float (&o)[W]) { store_f32<W>(ry, off, o); });
+        }
+      } else {
+        // a last column that ends inside a lane's, or rows too far apart for 32-bit offsets
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          f32x16 sums[NT];
+          take(m, sums);
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float v[4 * W];
+            __builtin_amdgcn_sched_barrier(0);
+            finish(sums, g, v);
+            int part = q;
+            asm volatile("" : "+v"(part));   // each step's addresses in their turn
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int r = wr * 32 * MT + (8 * g + part * 4 + i) * MT + m;
+              const int64_t row = t.m0 + r;
+#pragma unroll
+              for (int k = 0; k < W; ++k) {
+                if (r >= rows || !stores || f0 + col + k >= cols) continue;
+                float o = v[i * W + k];
+                const int64_t from = row * a.ldr + f0 + col + k, at = row * a.ldy + f0 + col + k;
+                if (a.residual)
                   o += a.r_bf16 ? __uint_as_float((unsigned)((const uint16_t*)a.residual)[from] << 16) : ((const float*)a.residual)[from];
-                }
-                const int64_t at = row * a.ldy + c0 + k;
                 if (a.y_bf16)
                   ((uint16_t*)a.y)[at] = to_bf16(o);
                 else
                   ((float*)a.y)[at] = o;
               }
+            }
           }
         }
+        __builtin_amdgcn_s_waitcnt(wait_vm(0));   // fewer stores than the next round's waits count on
       }
-      __builtin_amdgcn_s_waitcnt(wait_vm(0));   // fewer stores than the next round's waits count on
     } else if (!a.y_far && (t.n0 + BN <= a.N || a.N % NT == 0)) {
       const int pitch = (int)a.ldy * size;
       const __amdgpu_buffer_rsrc_t ry = rsrc(y0, rows < BM ? rows * pitch : OOB);
@@ -569,6 +694,12 @@ __global__ __launch_bounds__(128 * WC, WC == 4 ? 2 : 1) void mx_tile_kernel(Prod
     }
     if (!more) break;
     t = nt;
+    ++turn;
+    if constexpr (EPI != EPI_NONE) {   // the next tile's first operands once more: held through the above they would not fit
+      read(b0, 0, xa, xb);
+      read_scales(b0, 0, sa, sb);
+      if constexpr (DEEP) read(b0, 1, ya, yb);
+    }
   }
 #undef KQ_MX_STAGE
 #undef KQ_MX_DEEP_STAGE

@@ -60,6 +60,7 @@ namespace {
 typedef int i32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef unsigned u32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // Slots [first, last) of expert e0 + lane (none past the last expert), for the lanes of a wave: the
@@ -79,18 +80,41 @@ __device__ __forceinline__ void expert_ranges(const ProductArgs& a, int e0, int&
   top = __builtin_amdgcn_readlane(last, 63);
 }
 
-// act(v).  2^(v log2 e) from the hardware's exponential: the product's rounding puts a relative error
-// of |v| 2^-24 on it, which is at most 3e-8 of an activation's value next to 1.
-__device__ __forceinline__ float sigmoid_times(float v, float u) {   // v / (1 + exp(-u))
+// v / (1 + exp(-u)).  The product u log2 e rounds by 2^-24 of itself, a relative error of |u| 2^-24 in
+// the exponential; the sigmoid moves by at most 0.23 times that (u s (1 - s) <= 0.23).
+__device__ __forceinline__ float sigmoid_times(float v, float u) {
   return v * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * u));
 }
-__device__ __forceinline__ float activate(int act, float v) {
-  switch (act) {
-    case KQ_ACT_RELU: return v < 0.f ? 0.f : v;
-    case KQ_ACT_SILU: return sigmoid_times(v, v);
-    case KQ_ACT_GELU: return 0.5f * v * (1.f + erff(v * 0.707106781f));
-    case KQ_ACT_GELU_TANH: return sigmoid_times(v, 1.59576912f * (v + 0.044715f * v * v * v));   // 1 + tanh u = 2 / (1 + exp(-2 u))
-    default: return v;
+// v Phi(v), Phi the normal distribution: with a = |v|, Phi(-a) = 2^-(a^2 log2(e) / 2 + r(a)), where r
+// grows slowly, from 1 at 0 to 3.9 at 6.  The polynomial is r's, fitted over [0, 6] for the least
+// error of v Phi(v) relative to v (2.3 roundings); past 6, where Phi(-a) < 2^-29, r(6) serves.
+__device__ __forceinline__ float gelu(float v) {
+  const float a = fabsf(v), t = fminf(a, 6.f);
+  float r = fmaf(-8.4700869e-06f, t, 5.3903324e-05f);
+  r = fmaf(r, t, 4.2123639e-04f);
+  r = fmaf(r, t, -7.3892716e-03f);
+  r = fmaf(r, t, 5.2691109e-02f);
+  r = fmaf(r, t, -2.6219437e-01f);
+  r = fmaf(r, t, 1.1511109f);
+  r = fmaf(r, t, 0.99999988f);
+  const float tail = __builtin_amdgcn_exp2f(-fmaf(a * a, 0.72134752f, r));
+  return v * (v < 0.f ? tail : 1.f - tail);
+}
+// act of C values, the same act for every lane.
+template <int C>
+__device__ __forceinline__ void activate(int act, float (&v)[C]) {
+  if (act == KQ_ACT_SILU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = sigmoid_times(v[i], v[i]);
+  } else if (act == KQ_ACT_RELU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = v[i] < 0.f ? 0.f : v[i];
+  } else if (act == KQ_ACT_GELU) {
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = gelu(v[i]);
+  } else if (act == KQ_ACT_GELU_TANH) {   // 1 + tanh(u) = 2 / (1 + exp(-2 u))
+#pragma unroll
+    for (int i = 0; i < C; ++i) v[i] = sigmoid_times(v[i], v[i] * fmaf(0.0713548163f * v[i], v[i], 1.59576912f));
   }
 }
 
