@@ -1,10 +1,11 @@
 // Routing of rows to a mixture's experts: softmax, the `top` largest logits, slots sorted by expert,
 // counts and the balance loss, and the gradient of the logits.
 //
-// Rows are dealt to waves in contiguous chunks.  A first kernel takes the softmax and the choices of
-// its chunks' rows and counts each chunk's choices per expert; a second sums the counts over the
-// chunks, which gives every chunk its first slot at each expert; a third gives the chunk's choices
-// their slots, in order.  Every order is that of the rows, so nothing depends on timing.
+// Rows are dealt to workgroups in contiguous chunks, a chunk's rows to its waves likewise.  The first
+// kernel takes the softmax and the choices of its rows, counts each wave's choices per expert, and
+// leaves every choice's rank among its chunk's at that expert; the second sums the chunks' counts over
+// the chunks; the third adds to a rank what lies before its chunk.  Few rows are one chunk, and the
+// first kernel does all of it.  Every order is that of the rows, so nothing depends on timing.
 #include "device_util.h"
 #include "kq_internal.h"
 
@@ -14,7 +15,8 @@ namespace kq {
 namespace {
 
 constexpr int MAX_TOP = 16, MAX_EXPERTS = 4096;
-constexpr int WAVES = 4;   // per workgroup of the first and third kernel
+constexpr int MAX_CHUNKS = 1024;
+constexpr int PLACERS = 256, BACK_WAVES = 4;   // threads of the third kernel, waves of the gradient's
 
 struct RouteArgs {
   const void* logits;
@@ -29,7 +31,7 @@ struct RouteArgs {
   int32_t* counts;
   float* loss;
   int chunks;
-  int64_t per;            // rows of a chunk
+  int64_t per;            // rows of a wave; a chunk has those of its workgroup's waves
   int32_t* hist;          // [chunks][experts + 1]: choices per expert, rows with a softmax
   float* prob;            // [chunks][experts]: sums of probabilities
   double* mean;           // [experts]: over all chunks
@@ -85,11 +87,28 @@ __device__ __forceinline__ void load_row(const T* p, int l, int n, bool wide, fl
   }
 }
 
-// Over the LPR lanes of a row, the result in all of them.
+// Over the LPR lanes (16 or 64) of a row, the result in all of them: rotations inside sixteen lanes,
+// which cost no more than the operation, then exchanges of sixteens and halves.
+template <int CTRL, typename V>
+__device__ __forceinline__ V moved(V v) {
+  return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
+}
 template <int LPR, typename V, typename F>
 __device__ __forceinline__ V reduce_row(V v, F f) {
-#pragma unroll
-  for (int o = 1; o < LPR; o <<= 1) v = f(v, __shfl_xor(v, o));
+  v = f(v, moved<0x128>(v));
+  v = f(v, moved<0x124>(v));
+  v = f(v, moved<0x122>(v));
+  v = f(v, moved<0x121>(v));
+  if constexpr (LPR == 64) {
+    unsigned u = __builtin_bit_cast(unsigned, v);
+    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    const unsigned a0 = a[0], a1 = a[1];
+    v = f(__builtin_bit_cast(V, a0), __builtin_bit_cast(V, a1));
+    u = __builtin_bit_cast(unsigned, v);
+    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    const unsigned b0 = b[0], b1 = b[1];
+    v = f(__builtin_bit_cast(V, b0), __builtin_bit_cast(V, b1));
+  }
   return v;
 }
 template <int LPR>
@@ -105,9 +124,9 @@ __device__ __forceinline__ int row_min(int v) {
   return reduce_row<LPR>(v, [](int a, int b) { return min(a, b); });
 }
 
-// The rows [r0, r1) of a chunk, by one wave: weights, experts; its choices per expert added to
-// hist (LDS, [experts], zero before), its probabilities summed in prob.  Returns its rows with a
-// logit above -inf.
+// The rows [r0, r1), by one wave: weights, experts, and each choice's rank among the wave's at its
+// expert, in slot; hist (LDS, [experts], zero before) counts the choices; the rows' probabilities are
+// added to prob.  Returns its rows with a logit above -inf.
 template <typename T, int LPR, int VPL>
 __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64_t r1, int* hist, float (&prob)[VPL]) {
   using R = Row<LPR, VPL>;
@@ -166,86 +185,25 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
       const float by = a.normalize ? total : sum;
       a.weight[row * a.top + l] = bad ? NAN : chosen >= 0 ? mine / by : 0.f;
       a.expert[row * a.top + l] = chosen;
-      if (chosen >= 0) atomicAdd(hist + chosen, 1);
     }
+    // a row's choices are distinct, so row by row no two lanes count at one expert
+    int rank = 0;
+#pragma unroll
+    for (int g = 0; g < ROWS; ++g) {
+      if (lane / LPR == g && in && chosen >= 0) {
+        rank = hist[chosen];
+        hist[chosen] = rank + 1;
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");   // (one lane's view would allow all at once)
+      __builtin_amdgcn_wave_barrier();
+    }
+    if (in && l < a.top) a.slot[row * a.top + l] = rank;
   }
   return used;
 }
 
-// Adds the waves' sums of probabilities, in order, into sums (LDS, [experts], zero before).
-template <int LPR, int VPL>
-__device__ __forceinline__ void add_prob(const RouteArgs& a, const float (&prob)[VPL], float* sums) {
-  using R = Row<LPR, VPL>;
-  const int lane = threadIdx.x & 63, l = lane % LPR;
-#pragma unroll
-  for (int v = 0; v < VPL; ++v) {
-    float s = prob[v];
-#pragma unroll
-    for (int o = LPR; o < 64; o <<= 1) s += __shfl_xor(s, o);
-    const int c = R::column(v) + R::W * l;
-    if (lane < LPR && c < a.experts) sums[c] = s;
-  }
-}
-
-template <typename T, int LPR, int VPL>
-__global__ __launch_bounds__(64 * WAVES) void route_rows_kernel(RouteArgs a) {
-  extern __shared__ int lds[];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int chunk = blockIdx.x * WAVES + wave;
-  int* hist = lds + wave * a.experts;
-  for (int e = lane; e < a.experts; e += 64) hist[e] = 0;
-  __syncthreads();
-  if (chunk >= a.chunks) return;
-  const int64_t r0 = chunk * a.per, r1 = min(r0 + a.per, a.rows);
-  float prob[VPL] = {};
-  const int used = route_chunk<T, LPR, VPL>(a, r0, r1, hist, prob);
-  int32_t* to = a.hist + (int64_t)chunk * (a.experts + 1);
-  for (int e = lane; e < a.experts; e += 64) to[e] = hist[e];
-  if (lane == 0) to[a.experts] = used;
-  if (a.loss) add_prob<LPR, VPL>(a, prob, a.prob + (int64_t)chunk * a.experts);
-}
-
-// Sixteen experts (and, past the last, the count of rows) per workgroup: the chunks' counts become
-// the choices of the chunks before, the totals go to counts, the probabilities' sums to mean.
-__global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
-  __shared__ int seg[64][17];
-  __shared__ double seg_p[64][17];
-  const int k = threadIdx.x & 15, s = threadIdx.x >> 4, e = blockIdx.x * 16 + k;
-  const int per = (a.chunks + 63) / 64, c0 = min(s * per, a.chunks), c1 = min(c0 + per, a.chunks);
-  const int64_t pitch = a.experts + 1;
-  int n = 0;
-  double p = 0;
-  if (e <= a.experts)
-    for (int c = c0; c < c1; ++c) n += a.hist[c * pitch + e];
-  if (e < a.experts && a.loss)
-    for (int c = c0; c < c1; ++c) p += a.prob[(int64_t)c * a.experts + e];
-  seg[s][k] = n;
-  seg_p[s][k] = p;
-  __syncthreads();
-  if (e > a.experts) return;
-  int before = 0, total = 0;
-  for (int i = 0; i < 64; ++i) {
-    if (i == s) before = total;
-    total += seg[i][k];
-  }
-  if (s == 0) {
-    a.counts[e == a.experts ? e + 1 : e] = total;
-    if (e < a.experts && a.loss) {
-      double sum = 0;
-      for (int i = 0; i < 64; ++i) sum += seg_p[i][k];
-      a.mean[e] = sum;
-    }
-  }
-  if (e < a.experts)
-    for (int c = c0; c < c1; ++c) {
-      const int v = a.hist[c * pitch + e];
-      a.hist[c * pitch + e] = before;
-      before += v;
-    }
-}
-
-// Exclusive prefix sums of counts[0 .. n) into first[0 .. n], by one wave.
-__device__ __forceinline__ void first_slots(const int32_t* counts, int n, int* first) {
+// Exclusive prefix sums of n counts into first[0 .. n], by one wave.
+__device__ __forceinline__ void first_slots(const int* counts, int n, int* first) {
   const int lane = threadIdx.x & 63;
   int base = 0;
   for (int e0 = 0; e0 < n; e0 += 64) {
@@ -262,73 +220,188 @@ __device__ __forceinline__ void first_slots(const int32_t* counts, int n, int* f
   if (lane == 0) first[n] = base;
 }
 
-// Slots for the choices [i0, i1) of a chunk, in order: next[e] (LDS) is the next slot at expert e.
-__device__ __forceinline__ void place(const RouteArgs& a, int64_t i0, int64_t i1, int* next) {
-  const int lane = threadIdx.x & 63;
-  const int bits = 32 - __builtin_clz(a.experts);   // of experts 0 .. experts (none: experts)
-  for (int64_t i = i0; i < i1; i += 64) {
-    const bool in = i + lane < i1;
-    const int e = in ? a.expert[i + lane] : -1;
-    const int key = e < 0 ? a.experts : e;
-    unsigned long long same = __ballot(in);
-    for (int b = 0; b < bits; ++b) {
-      const unsigned long long set = __ballot((key >> b) & 1);
-      same &= (key >> b) & 1 ? set : ~set;
-    }
-    const int rank = __popcll(same & ((1ull << lane) - 1));
-    int slot = -1;
-    if (e >= 0) {
-      slot = next[e] + rank;
-      if (rank == 0) next[e] = slot + __popcll(same);   // (reads of this round come before: one wave)
-    }
-    if (in) {
-      a.slot[i + lane] = slot;
-      if (slot >= 0) a.index[slot] = (int32_t)((i + lane) / a.top);
-    }
-  }
-}
-
-// Offsets, the total, the loss and the index past the last slot, from the counts: one workgroup of
-// THREADS; first: the experts' first slots.
-template <int THREADS>
-__device__ __forceinline__ void finish(const RouteArgs& a, const int* first, double* shared) {
-  const int made = first[a.experts];
-  for (int e = threadIdx.x; e <= a.experts; e += THREADS) a.offsets[e] = first[e];
-  if (threadIdx.x == 0) a.counts[a.experts] = made;
-  if (a.loss) {
-    const int used = a.counts[a.experts + 1];
-    double s = 0;
-    for (int e = threadIdx.x; e < a.experts; e += THREADS) s += (double)(first[e + 1] - first[e]) * a.mean[e];
-    // (an expert without choices adds nothing, but a NaN probability has to show)
+// The loss, by all THREADS of a workgroup: sums(e) gives expert e's sum of probabilities.
+template <int THREADS, typename F>
+__device__ __forceinline__ void write_loss(const RouteArgs& a, const int* first, int used, double* shared, F sums) {
+  double s = 0;   // (an expert without choices adds nothing, but a probability that is NaN has to show)
+  for (int e = threadIdx.x; e < a.experts; e += THREADS) s += (double)(first[e + 1] - first[e]) * sums(e);
 #pragma unroll
-    for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      s = 0;
-      for (int i = 0; i < THREADS / 64; ++i) s += shared[i];
-      *a.loss = (float)(s * a.experts / ((double)max(made, 1) * max(used, 1)));
-    }
-  }
+  for (int o = 1; o < 64; o <<= 1) s += __shfl_xor(s, o);
+  if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = s;
+  __syncthreads();
+  if (threadIdx.x != 0) return;
+  s = 0;
+  for (int i = 0; i < THREADS / 64; ++i) s += shared[i];
+  *a.loss = (float)(s * a.experts / ((double)max(first[a.experts], 1) * max(used, 1)));
 }
 
-__global__ __launch_bounds__(64 * WAVES) void route_place_kernel(RouteArgs a) {
-  extern __shared__ int lds[];   // first slots [experts + 1], then each wave's next slots [experts]
+template <typename T, int LPR, int VPL, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void route_rows_kernel(RouteArgs a) {
+  using R = Row<LPR, VPL>;
+  constexpr int THREADS = 64 * WAVES;
+  extern __shared__ __attribute__((aligned(16))) int lds[];   // [WAVES][experts], then of one chunk [experts] and [experts + 1]
+  __shared__ int used[WAVES];
   __shared__ double shared[WAVES];
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  if (wave == 0) first_slots(a.counts, a.experts, lds);
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), n = a.experts;
+  for (int e = threadIdx.x; e < WAVES * n; e += THREADS) lds[e] = 0;
   __syncthreads();
-  const int made = lds[a.experts];
-  for (int64_t i = made + (int64_t)blockIdx.x * (64 * WAVES) + threadIdx.x; i < a.rows * a.top; i += (int64_t)gridDim.x * (64 * WAVES))
-    a.index[i] = -1;
-  if (blockIdx.x == 0) finish<64 * WAVES>(a, lds, shared);
-  const int chunk = blockIdx.x * WAVES + wave;
-  if (chunk >= a.chunks) return;
-  int* next = lds + a.experts + 1 + wave * a.experts;
-  const int32_t* before = a.hist + (int64_t)chunk * (a.experts + 1);
-  for (int e = lane; e < a.experts; e += 64) next[e] = lds[e] + before[e];
-  const int64_t r0 = chunk * a.per, r1 = min(r0 + a.per, a.rows);
-  place(a, r0 * a.top, r1 * a.top, next);
+  const int64_t c0 = (int64_t)blockIdx.x * WAVES * a.per, r0 = min(c0 + wave * a.per, a.rows), r1 = min(r0 + a.per, a.rows);
+  float prob[VPL] = {};
+  const int mine = route_chunk<T, LPR, VPL>(a, r0, r1, lds + wave * n, prob);
+  if (lane == 0) used[wave] = mine;
+  __syncthreads();
+  // counts of the waves before, and of the chunk
+  int* total = lds + WAVES * n;
+  int* first = total + n;
+  const bool one = gridDim.x == 1;
+  int32_t* to = a.hist + (int64_t)blockIdx.x * (n + 1);
+  for (int e = threadIdx.x; e < n; e += THREADS) {
+    int sum = 0;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      const int v = lds[w * n + e];
+      lds[w * n + e] = sum;
+      sum += v;
+    }
+    if (one)
+      total[e] = a.counts[e] = sum;
+    else
+      to[e] = sum;
+  }
+  int all = 0;
+#pragma unroll
+  for (int w = 0; w < WAVES; ++w) all += used[w];
+  if (threadIdx.x == 0) *(one ? a.counts + n + 1 : to + n) = all;
+  __syncthreads();
+  if (one) {
+    if (wave == 0) first_slots(total, n, first);
+    __syncthreads();
+    for (int e = threadIdx.x; e <= n; e += THREADS) a.offsets[e] = first[e];
+    if (threadIdx.x == 0) a.counts[n] = first[n];
+    for (int64_t i = first[n] + threadIdx.x; i < a.rows * a.top; i += THREADS) a.index[i] = -1;
+  }
+  // each wave its own rows' choices (which it has written)
+  for (int64_t i = r0 * a.top + lane; i < r1 * a.top; i += 64) {
+    const int e = a.expert[i];
+    if (e < 0) {
+      a.slot[i] = -1;
+      continue;
+    }
+    const int rank = a.slot[i] + lds[wave * n + e];
+    if (one) {
+      a.slot[i] = first[e] + rank;
+      a.index[first[e] + rank] = (int32_t)((uint32_t)i / (uint32_t)a.top);
+    } else {
+      a.slot[i] = rank;
+    }
+  }
+  if (!a.loss) return;
+  // the waves' probabilities, summed in their order
+  __syncthreads();
+  float* sums = (float*)lds + wave * n;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    float s = prob[v];
+    if constexpr (LPR == 16) {
+      s += __shfl_xor(s, 16);
+      s += __shfl_xor(s, 32);
+    }
+    const int c = R::column(v) + R::W * (lane % LPR);
+    if (lane < LPR && c < n) sums[c] = s;
+  }
+  __syncthreads();
+  auto sum_of = [&](int e) {
+    float s = 0.f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) s += ((const float*)lds)[w * n + e];
+    return s;
+  };
+  if (one)
+    write_loss<THREADS>(a, first, all, shared, sum_of);
+  else
+    for (int e = threadIdx.x; e < n; e += THREADS) a.prob[(int64_t)blockIdx.x * n + e] = sum_of(e);
+}
+
+// Eight experts (and, past the last, the count of rows) per workgroup, 128 threads each: the chunks'
+// counts become those of the chunks before, the totals go to counts, the probabilities' sums to mean.
+__global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
+  constexpr int SEGS = 128, PER = MAX_CHUNKS / SEGS;
+  __shared__ int seg[8][SEGS + 1];
+  __shared__ double seg_p[8][SEGS + 1];
+  const int k = threadIdx.x & 7, s = threadIdx.x >> 3, e = blockIdx.x * 8 + k;
+  const int64_t pitch = a.experts + 1;
+  const int per = (a.chunks + SEGS - 1) / SEGS, c0 = s * per;
+  const bool live = e <= a.experts, summed = e < a.experts && a.loss;
+  int v[PER], n = 0;
+  float f[PER];
+  double p = 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) v[i] = live && i < per && c0 + i < a.chunks ? a.hist[(c0 + i) * pitch + e] : 0;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) f[i] = summed && i < per && c0 + i < a.chunks ? a.prob[(int64_t)(c0 + i) * a.experts + e] : 0.f;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    n += v[i];
+    p += f[i];
+  }
+  seg[k][s] = n;
+  seg_p[k][s] = p;
+  __syncthreads();
+  // one wave per expert: two segments a lane
+  const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+  if (wave < 8) {
+    const int x = seg[wave][2 * lane], y = seg[wave][2 * lane + 1];
+    int sum = x + y;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int u = __shfl_up(sum, o);
+      if (lane >= o) sum += u;
+    }
+    double q = seg_p[wave][2 * lane] + seg_p[wave][2 * lane + 1];
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) q += __shfl_xor(q, o);
+    seg[wave][2 * lane] = sum - x - y;
+    seg[wave][2 * lane + 1] = sum - y;
+    const int mine = blockIdx.x * 8 + wave;
+    if (lane == 63 && mine <= a.experts) {
+      a.counts[mine == a.experts ? mine + 1 : mine] = sum;
+      if (mine < a.experts && a.loss) a.mean[mine] = q;
+    }
+  }
+  __syncthreads();
+  int before = seg[k][s];
+#pragma unroll
+  for (int i = 0; i < PER; ++i)
+    if (e < a.experts && i < per && c0 + i < a.chunks) {
+      a.hist[(c0 + i) * pitch + e] = before;
+      before += v[i];
+    }
+}
+
+__global__ __launch_bounds__(PLACERS) void route_place_kernel(RouteArgs a, int64_t chunk_rows) {
+  extern __shared__ int lds[];   // first slots [experts + 1], the chunk's next ones [experts]
+  __shared__ double shared[PLACERS / 64];
+  const int n = a.experts;
+  if (threadIdx.x < 64) first_slots(a.counts, n, lds);
+  __syncthreads();
+  const int made = lds[n];
+  int* next = lds + n + 1;
+  const int32_t* before = a.hist + (int64_t)blockIdx.x * (n + 1);
+  for (int e = threadIdx.x; e < n; e += PLACERS) next[e] = lds[e] + before[e];
+  __syncthreads();
+  const int64_t choices = a.rows * a.top, i0 = blockIdx.x * chunk_rows * a.top, i1 = min(i0 + chunk_rows * a.top, choices);
+  for (int64_t i = i0 + threadIdx.x; i < i1; i += PLACERS) {
+    const int e = a.expert[i];
+    if (e < 0) continue;   // (its slot is -1 already)
+    const int slot = next[e] + a.slot[i];
+    a.slot[i] = slot;
+    a.index[slot] = (int32_t)((uint32_t)i / (uint32_t)a.top);
+  }
+  for (int64_t i = max((int64_t)made, i0) + threadIdx.x; i < i1; i += PLACERS) a.index[i] = -1;
+  if (blockIdx.x != 0) return;
+  for (int e = threadIdx.x; e <= n; e += PLACERS) a.offsets[e] = lds[e];
+  if (threadIdx.x == 0) a.counts[n] = made;
+  if (a.loss) write_loss<PLACERS>(a, lds, a.counts[n + 1], shared, [&](int e) { return a.mean[e]; });
 }
 
 struct BackArgs {
@@ -346,11 +419,11 @@ struct BackArgs {
 };
 
 template <typename T, int LPR, int VPL>
-__global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(BackArgs a) {
+__global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArgs a) {
   using R = Row<LPR, VPL>;
   constexpr int ROWS = 64 / LPR;
   const int lane = threadIdx.x & 63, l = lane % LPR;
-  const int64_t chunk = blockIdx.x * WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t chunk = (int64_t)blockIdx.x * BACK_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t r0 = chunk * a.per, r1 = min(r0 + a.per, a.rows);
   float b[VPL];
   const float unit = a.dloss ? *a.dloss * (float)a.experts / ((float)max(a.counts[a.experts], 1) * (float)max(a.counts[a.experts + 1], 1)) : 0.f;
@@ -432,11 +505,14 @@ __global__ __launch_bounds__(64 * WAVES) void route_backward_kernel(BackArgs a) 
   }
 }
 
-// How many chunks the rows are dealt to: four row groups each at least, and as many as the card holds.
+// Waves of a workgroup of the first kernel: eight, four where their counts would take more LDS.
+int waves_of(int experts) { return experts <= 2048 ? 8 : 4; }
+
+// The rows of a wave and the number of chunks: four row groups of a wave at least.
 void deal(int64_t rows, int experts, int* chunks, int64_t* per) {
-  const int64_t most = std::max<int64_t>(512, std::min<int64_t>(2048, (1 << 20) / (experts + 1)));
-  *per = std::max<int64_t>(ceil_div(ceil_div(rows, most), 4) * 4, 16);
-  *chunks = (int)ceil_div(rows, *per);
+  const int waves = waves_of(experts);
+  *per = std::max<int64_t>(ceil_div(ceil_div(rows, (int64_t)MAX_CHUNKS * waves), 4) * 4, 16);
+  *chunks = (int)std::max<int64_t>(ceil_div(rows, *per * waves), 1);
 }
 
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
@@ -475,10 +551,14 @@ struct RouteLaunch {
 template <typename T, int LPR, int VPL>
 struct RouteRows {
   static kq_status go(const RouteLaunch& r) {
+    constexpr int WAVES = LPR * VPL <= 2048 ? 8 : 4;
     RouteArgs a = r.a;
     a.wide = a.experts % Row<LPR, VPL>::W == 0;
-    const unsigned grid = (unsigned)ceil_div(a.chunks, WAVES);
-    route_rows_kernel<T, LPR, VPL><<<dim3(grid), dim3(64 * WAVES), sizeof(int) * WAVES * (size_t)a.experts, r.s>>>(a);
+    const size_t lds = sizeof(int) * ((size_t)(WAVES + 2) * a.experts + 1);
+    const auto kernel = route_rows_kernel<T, LPR, VPL, WAVES>;
+    if (lds > 64 * 1024)
+      KQ_HIP(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
+    kernel<<<dim3((unsigned)a.chunks), dim3(64 * WAVES), lds, r.s>>>(a);
     KQ_LAUNCHED("route_rows_kernel");
     return KQ_OK;
   }
@@ -495,8 +575,8 @@ struct RouteBack {
     a.wide = a.experts % Row<LPR, VPL>::W == 0;
     const int64_t units = ceil_div(a.rows, 64 / LPR), waves = std::min<int64_t>(units, (int64_t)device_cu_count() * 32);
     a.per = ceil_div(units, waves) * (64 / LPR);
-    const unsigned grid = (unsigned)ceil_div(ceil_div(a.rows, a.per), WAVES);
-    route_backward_kernel<T, LPR, VPL><<<dim3(grid), dim3(64 * WAVES), 0, r.s>>>(a);
+    const unsigned grid = (unsigned)ceil_div(ceil_div(a.rows, a.per), BACK_WAVES);
+    route_backward_kernel<T, LPR, VPL><<<dim3(grid), dim3(64 * BACK_WAVES), 0, r.s>>>(a);
     KQ_LAUNCHED("route_backward_kernel");
     return KQ_OK;
   }
@@ -540,13 +620,11 @@ extern "C" kq_status kq_route(const void* logits, int type, int64_t rows, int ex
   a.hist = (int32_t*)ws;
   a.prob = (float*)((char*)ws + round16(sizeof(int32_t) * (size_t)a.chunks * (experts + 1)));
   a.mean = (double*)((char*)a.prob + round16(sizeof(float) * (size_t)a.chunks * experts));
-  if (rows > 0) KQ_TRY(by_width<RouteRows>(type, experts, RouteLaunch{a, s}));
-  route_scan_kernel<<<dim3((unsigned)ceil_div(experts + 1, 16)), dim3(1024), 0, s>>>(a);
+  KQ_TRY(by_width<RouteRows>(type, experts, RouteLaunch{a, s}));
+  if (a.chunks == 1) return KQ_OK;
+  route_scan_kernel<<<dim3((unsigned)ceil_div(experts + 1, 8)), dim3(1024), 0, s>>>(a);
   KQ_LAUNCHED("route_scan_kernel");
-  const size_t lds = sizeof(int) * ((size_t)(WAVES + 1) * experts + 1);
-  if (lds > 64 * 1024)
-    KQ_HIP(hipFuncSetAttribute((const void*)route_place_kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
-  route_place_kernel<<<dim3((unsigned)std::max<int64_t>(1, ceil_div(a.chunks, WAVES))), dim3(64 * WAVES), lds, s>>>(a);
+  route_place_kernel<<<dim3((unsigned)a.chunks), dim3(PLACERS), sizeof(int) * (2 * (size_t)experts + 1), s>>>(a, a.per * waves_of(experts));
   KQ_LAUNCHED("route_place_kernel");
   return KQ_OK;
 }
