@@ -39,14 +39,9 @@ struct RouteArgs {
 
 __device__ __forceinline__ float bf16_value(uint16_t v) { return __uint_as_float((unsigned)v << 16); }
 
-// exp(x) for x <= 0, infinities and NaN among them, to about an ulp: 2^(x log2 e) with what the
-// product loses put back.  Below -120 the result is zero in fp32 anyway (and -inf would give NaN).
-__device__ __forceinline__ float exp_of(float x) {
-  const float c = x < -120.f ? -120.f : x;
-  const float t = c * 1.44269502f, r = fmaf(c, 1.44269502f, -t) + c * 1.92596303e-8f;
-  const float e = __builtin_amdgcn_exp2f(t);
-  return fmaf(e, r * 0.693147182f, e);
-}
+// exp(x).  The product x log2 e rounds by 2^-24 of itself, a relative error of |x| 2^-24 in the result:
+// for the x <= 0 of a softmax largest where the result is least.
+__device__ __forceinline__ float exp_of(float x) { return __builtin_amdgcn_exp2f(1.44269504f * x); }
 
 // A row's values in registers: LPR lanes hold VPL each, in groups of W = min(VPL, 4) neighbours.
 // Value v of lane l is column (v / W) LPR W + l W + v % W, so columns ascend with v in a lane.
@@ -123,6 +118,56 @@ template <int LPR>
 __device__ __forceinline__ int row_min(int v) {
   return reduce_row<LPR>(v, [](int a, int b) { return min(a, b); });
 }
+template <int LPR>
+__device__ __forceinline__ int row_top(int v) {
+  return reduce_row<LPR>(v, [](int a, int b) { return max(a, b); });
+}
+
+// Keys of a row's values: whole numbers in the values' order, whose lowest bits make room for the
+// column, counted down, so that they are distinct and the lower of two columns comes first.
+// bf16 values keep all their bits; of fp32 values as many go as columns need, and two neighbours
+// in the order that agree in the rest have to be compared in full (ambiguous).
+constexpr int KEY_FINITE = (int)0x80800000, KEY_INFINITE = 0x7f800000;   // the lowest number's, infinity's
+__device__ __forceinline__ int key_of(float v, int low, int mask) {
+  const int u = __float_as_int(v);
+  return ((u ^ ((u >> 31) & 0x7fffffff)) & ~mask) | low;
+}
+
+// Sorts N keys, a power of two of them, in descending order: merges of odd and even places, of runs
+// of P, at distances Q = P, P / 2, .. 1.
+template <int P = 1, int Q = P, int N>
+__device__ __forceinline__ void sort_keys(int (&k)[N]) {
+  if constexpr (P < N) {
+#pragma unroll
+    for (int i = Q % P; i + Q < N; ++i)
+      if ((i - Q % P) % (2 * Q) < Q && i / (2 * P) == (i + Q) / (2 * P)) {
+        const int hi = max(k[i], k[i + Q]), lo = min(k[i], k[i + Q]);
+        k[i] = hi;
+        k[i + Q] = lo;
+      }
+    if constexpr (Q > 1)
+      sort_keys<P, Q / 2>(k);
+    else
+      sort_keys<2 * P>(k);
+  }
+}
+
+// The `count` largest keys of a row, key j to lane j: every lane's are sorted, and the one that holds
+// the largest gives it up.  DEPTH: at least count.
+template <int LPR, int DEPTH, int J = 0, int N>
+__device__ __forceinline__ void take_keys(int (&k)[N], int count, int& mine) {
+  if constexpr (J < DEPTH) {
+    if (J >= count) return;
+    const int best = row_top<LPR>(k[0]);
+    if (threadIdx.x % LPR == J) mine = best;
+    const bool gives = k[0] == best;
+    constexpr int LAST = N - 1, LEFT = DEPTH - 1 - J;   // (as many of a lane's as may still be taken)
+#pragma unroll
+    for (int i = 0; i < LAST && i < LEFT; ++i) k[i] = gives ? k[i + 1] : k[i];
+    if constexpr (LAST < LEFT) k[LAST] = gives ? INT32_MIN : k[LAST];
+    take_keys<LPR, DEPTH, J + 1>(k, count, mine);
+  }
+}
 
 // The rows [r0, r1), by one wave: weights, experts, and each choice's rank among the wave's at its
 // expert, in slot; hist (LDS, [experts], zero before) counts the choices; the rows' probabilities are
@@ -138,6 +183,8 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
     const bool in = row < r1;
     float x[VPL];
     load_row<T, LPR, VPL>((const T*)a.logits + (in ? row : r0) * a.ld, l, a.experts, a.wide, x);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v) x[v] += 0.f;   // (-0 becomes 0, which it equals)
     float m = x[0];
 #pragma unroll
     for (int v = 1; v < VPL; ++v) m = fmaxf(m, x[v]);
@@ -158,27 +205,58 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
       for (int v = 0; v < VPL; ++v) prob[v] += p[v] * inv;
     }
     used += __popcll(__ballot(in && l == 0 && (some || bad)));
-    // one choice after another: the first column of the largest value left
     float total = 0.f, mine = 0.f;
     int chosen = -1;
-    for (int j = 0; j < a.top; ++j) {
-      float best = x[0];
+    // bf16: the keys say it all; fp32: one choice more, to see that the last one is clear of it
+    constexpr bool WHOLE = sizeof(T) == 2;
+    const int count = a.top + (WHOLE ? 0 : 1);
+    bool clear = VPL <= 16 && count <= 16;
+    if constexpr (VPL <= 16) {
+      if (clear) {
+        constexpr int MASK = LPR * VPL - 1;
+        int k[VPL];
 #pragma unroll
-      for (int v = 1; v < VPL; ++v) best = fmaxf(best, x[v]);
-      best = row_max<LPR>(best);
-      int c = 0x7fffffff;
+        for (int v = 0; v < VPL; ++v) k[v] = key_of(x[v], (MASK - R::column(v)) - R::W * l, MASK);
+        sort_keys(k);
+        int key = INT32_MIN;
+        if (count <= 9)
+          take_keys<LPR, 9>(k, count, key);
+        else
+          take_keys<LPR, 16>(k, count, key);
+        const int before = moved<0x111>(key);   // (of the lane before)
+        const bool there = key >= KEY_FINITE;
+        if (!WHOLE) clear = !__any(l > 0 && l < count && there && ((key ^ before) & ~MASK) == 0);
+        if (l < a.top && there && !bad) {
+          chosen = MASK - (key & MASK);
+          const T v = ((const T*)a.logits + (in ? row : r0) * a.ld)[chosen];   // once more, whole
+          mine = exp_of((sizeof(T) == 4 ? (float)v : bf16_value((uint16_t)v)) - base);
+        }
+        total = row_sum<LPR>(mine);
+      }
+    }
+    if (!clear) {
+      // one choice after another: the first column of the largest value left
+      total = 0.f;
+      chosen = -1;
+      for (int j = 0; j < a.top; ++j) {
+        float best = x[0];
 #pragma unroll
-      for (int v = VPL - 1; v >= 0; --v) c = x[v] == best ? R::column(v) + R::W * l : c;
-      c = row_min<LPR>(c);
-      const int own = c - R::W * l;
+        for (int v = 1; v < VPL; ++v) best = fmaxf(best, x[v]);
+        best = row_max<LPR>(best);
+        int c = 0x7fffffff;
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) x[v] = own == R::column(v) ? -INFINITY : x[v];
-      const bool there = best > -INFINITY && !bad;
-      const float e = there ? exp_of(best - base) : 0.f;
-      total += e;
-      if (l == j) {
-        chosen = there ? c : -1;
-        mine = e;
+        for (int v = VPL - 1; v >= 0; --v) c = x[v] == best ? R::column(v) + R::W * l : c;
+        c = row_min<LPR>(c);
+        const int own = c - R::W * l;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) x[v] = own == R::column(v) ? -INFINITY : x[v];
+        const bool there = best > -INFINITY && !bad;
+        const float e = there ? exp_of(best - base) : 0.f;
+        total += e;
+        if (l == j) {
+          chosen = there ? c : -1;
+          mine = e;
+        }
       }
     }
     if (in && l < a.top) {

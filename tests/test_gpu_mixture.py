@@ -147,6 +147,32 @@ def _route_back_check(g, x, want, dw, dloss, normalize, kind):
     _within(_host(g), ref, c * size + _half(kind) * np.abs(ref) + 2.0 ** -126, "dlogits")
 
 
+@pytest.mark.parametrize("top", [1, 4, 8, 9, 15, 16])
+@pytest.mark.parametrize("experts", [16, 30, 64, 200, 256, 520, 1000])
+def test_route_of_close_logits(experts, top):
+    """Logits a few units in the last place apart, of either sign, zeros of both signs, numbers below the
+    normal ones, the lowest number beside closed experts: the order is that of the whole values."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(experts + top)
+    rows = 40
+    bits = np.float32(1.75).view(np.int32) + rng.integers(0, 40, (rows, experts)).astype(np.int32)
+    x = bits.view(np.float32).copy()
+    x[1::2] *= -1
+    x[4] = np.where(rng.random(experts) < 0.5, 0.0, -0.0)
+    x[5] = rng.integers(-3, 4, experts) * np.float32(2.0 ** -149)
+    x[6, ::2] = x[6, ::2] * 3
+    x[7] = np.where(rng.random(experts) < 0.7, -INF, np.finfo(np.float32).min)
+    x[8] = np.where(rng.random(experts) < 0.7, np.nextafter(np.finfo(np.float32).min, np.float32(0)), np.finfo(np.float32).min)
+    x[9] = rng.standard_normal(experts)
+    x[10, 1:] = -INF
+    x[11] = np.where(rng.random(experts) < 0.5, 3e38, np.nextafter(np.float32(3e38), np.float32(INF)))
+    x[12:20] = np.round(rng.standard_normal((8, experts)) * 2) / 2
+    r = Routes(rows, experts, top)
+    kq.kq_route(_dev(x), normalize=True, **r.dict())
+    _route_check(r, torch.from_numpy(x), top, True)
+
+
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
 @pytest.mark.parametrize("experts", [8, 60, 256, 700])
 def test_route_of_rows_without_a_softmax(experts, kind):
