@@ -181,8 +181,9 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
   for (int64_t t = r0; t < r1; t += ROWS) {
     const int64_t row = t + lane / LPR;
     const bool in = row < r1;
+    const T* from = (const T*)a.logits + (in ? row : r0) * a.ld;
     float x[VPL];
-    load_row<T, LPR, VPL>((const T*)a.logits + (in ? row : r0) * a.ld, l, a.experts, a.wide, x);
+    load_row<T, LPR, VPL>(from, l, a.experts, a.wide, x);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) x[v] += 0.f;   // (-0 becomes 0, which it equals)
     float m = x[0];
@@ -228,7 +229,7 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
         if (!WHOLE) clear = !__any(l > 0 && l < count && there && ((key ^ before) & ~MASK) == 0);
         if (l < a.top && there && !bad) {
           chosen = MASK - (key & MASK);
-          const T v = ((const T*)a.logits + (in ? row : r0) * a.ld)[chosen];   // once more, whole
+          const T v = from[chosen];   // once more, whole
           mine = exp_of((sizeof(T) == 4 ? (float)v : bf16_value((uint16_t)v)) - base);
         }
         total = row_sum<LPR>(mine);
@@ -236,6 +237,7 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
     }
     if (!clear) {
       // one choice after another: the first column of the largest value left
+      if constexpr (VPL <= 16) load_row<T, LPR, VPL>(from, l, a.experts, a.wide, x);   // (not held through the above)
       total = 0.f;
       chosen = -1;
       for (int j = 0; j < a.top; ++j) {
@@ -459,24 +461,57 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
 __global__ __launch_bounds__(PLACERS) void route_place_kernel(RouteArgs a, int64_t chunk_rows) {
   extern __shared__ int lds[];   // first slots [experts + 1], the chunk's next ones [experts]
   __shared__ double shared[PLACERS / 64];
-  const int n = a.experts;
-  if (threadIdx.x < 64) first_slots(a.counts, n, lds);
-  __syncthreads();
-  const int made = lds[n];
+  __shared__ int sums[PLACERS / 64];
+  const int n = a.experts, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   int* next = lds + n + 1;
   const int32_t* before = a.hist + (int64_t)blockIdx.x * (n + 1);
-  for (int e = threadIdx.x; e < n; e += PLACERS) next[e] = lds[e] + before[e];
-  __syncthreads();
   const int64_t choices = a.rows * a.top, i0 = blockIdx.x * chunk_rows * a.top, i1 = min(i0 + chunk_rows * a.top, choices);
-  for (int64_t i = i0 + threadIdx.x; i < i1; i += PLACERS) {
-    const int e = a.expert[i];
-    if (e < 0) continue;   // (its slot is -1 already)
-    const int slot = next[e] + a.slot[i];
+  // the first choices are on their way while the first slots are summed
+  constexpr int EARLY = 4;
+  int early_e[EARLY], early_r[EARLY];
+#pragma unroll
+  for (int k = 0; k < EARLY; ++k) {
+    const int64_t i = i0 + k * PLACERS + threadIdx.x;
+    early_e[k] = i < i1 ? a.expert[i] : -1;
+    early_r[k] = i < i1 ? a.slot[i] : 0;
+  }
+  int base = 0;
+  for (int e0 = 0; e0 < n; e0 += PLACERS) {
+    const int e = e0 + threadIdx.x, c = e < n ? a.counts[e] : 0, earlier = e < n ? before[e] : 0;
+    int sum = c;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(sum, o);
+      if (lane >= o) sum += v;
+    }
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    int first = base + sum - c;
+#pragma unroll
+    for (int w = 0; w < PLACERS / 64; ++w) {
+      if (w < wave) first += sums[w];
+      base += sums[w];
+    }
+    if (e < n) {
+      lds[e] = first;
+      next[e] = first + earlier;
+    }
+    __syncthreads();
+  }
+  const int made = base;
+  if (threadIdx.x == 0) lds[n] = made;
+  auto put = [&](int64_t i, int e, int rank) {
+    if (e < 0) return;   // (its slot is -1 already)
+    const int slot = next[e] + rank;
     a.slot[i] = slot;
     a.index[slot] = (int32_t)((uint32_t)i / (uint32_t)a.top);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < EARLY; ++k) put(i0 + k * PLACERS + threadIdx.x, early_e[k], early_r[k]);
+  for (int64_t i = i0 + EARLY * PLACERS + threadIdx.x; i < i1; i += PLACERS) put(i, a.expert[i], a.slot[i]);
   for (int64_t i = max((int64_t)made, i0) + threadIdx.x; i < i1; i += PLACERS) a.index[i] = -1;
   if (blockIdx.x != 0) return;
+  __syncthreads();
   for (int e = threadIdx.x; e <= n; e += PLACERS) a.offsets[e] = lds[e];
   if (threadIdx.x == 0) a.counts[n] = made;
   if (a.loss) write_loss<PLACERS>(a, lds, a.counts[n + 1], shared, [&](int e) { return a.mean[e]; });
