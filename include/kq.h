@@ -593,7 +593,7 @@ kq_status kq_mxfp4_experts_epilogue(const void* x, int x_type, int64_t rows, int
                                     size_t ws_bytes, void* stream);
 
 /*
- * kq_route_workspace -- workspace bytes of kq_route.
+ * kq_route_workspace -- workspace bytes of kq_route (none for few rows).
  */
 kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
 
@@ -620,7 +620,8 @@ kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
  *   offsets  device int32 [experts + 1]: each expert's first slot, then N
  *   counts   device int32 [experts + 2]: choices of each expert, then N, then R
  *   loss_opt device fp32 [1]: L, or NULL
- *   ws       device workspace, 16-byte aligned, ws_bytes >= kq_route_workspace(...)
+ *   ws       device workspace, 16-byte aligned, ws_bytes >= kq_route_workspace(...); may be NULL where
+ *            that is 0
  * Sizes: rows >= 0, rows * top < 2^31, 1 <= experts <= 4096, 1 <= top <= min(experts, 16).  Asynchronous
  * on `stream`; the same inputs give the same bits (no order depends on atomics).  The outputs must not
  * overlap each other or the inputs.

@@ -635,6 +635,20 @@ def _mx_same(device, *tensors) -> None:
             raise ValueError(f"tensors on devices {device} and {t.get_device()}")
 
 
+def _mx_buffer(t, name: str, n: int, dtype, device: int):
+    """The address of n contiguous entries on `device`, None for None: one pass over what has to hold."""
+    if t is None:
+        return None
+    try:
+        if t.dtype is dtype and t.get_device() == device and t.numel() == n and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        pass
+    _mx_vector(t, name, n, dtype)   # (says what does not)
+    _mx_same(device, t)
+    raise ValueError(f"{name}: not a buffer of {n} entries of {dtype} on device {device}")
+
+
 def _epilogue(bias, act, gated, residual, rows: int, out: int, experts):
     """A kq_epilogue for `rows` x `out` outputs (experts: of that many layers, None: of one)."""
     wide = out * (2 if gated else 1)
@@ -718,13 +732,16 @@ def kq_route(logits, weight, expert, slot, index, offsets, counts, loss=None, no
     if erows != rows:
         raise ValueError(f"expert must have {rows} rows")
     n, device = rows * top, logits.get_device()
-    if ws is None:
-        ws = _workspace(kq_route_workspace(rows, experts, top), logits.device, stream)
-    _mx_same(device, weight, expert, slot, index, offsets, counts, loss, ws)
-    st = _lib.kq_route(xp, xt, rows, experts, ld, top, 1 if normalize else 0, _mx_vector(weight, "weight", n, _mx_f32),
-                       _mx_vector(expert, "expert", n, _mx_i32), _mx_vector(slot, "slot", n, _mx_i32),
-                       _mx_vector(index, "index", n, _mx_i32), _mx_vector(offsets, "offsets", experts + 1, _mx_i32),
-                       _mx_vector(counts, "counts", experts + 2, _mx_i32), _mx_vector(loss, "loss", 1, _mx_f32), _mx_ptr(ws, "ws", _mx_u8), ws.numel(), _mx_here(device, stream))
+    stream_ptr = _mx_here(device, stream)
+    need = kq_route_workspace(rows, experts, top) if ws is None else 0
+    if need:
+        ws = _workspace(need, logits.device, stream)
+    st = _lib.kq_route(xp, xt, rows, experts, ld, top, 1 if normalize else 0, _mx_buffer(weight, "weight", n, _mx_f32, device),
+                       _mx_buffer(expert, "expert", n, _mx_i32, device), _mx_buffer(slot, "slot", n, _mx_i32, device),
+                       _mx_buffer(index, "index", n, _mx_i32, device), _mx_buffer(offsets, "offsets", experts + 1, _mx_i32, device),
+                       _mx_buffer(counts, "counts", experts + 2, _mx_i32, device), _mx_buffer(loss, "loss", 1, _mx_f32, device),
+                       None if ws is None else _mx_buffer(ws, "ws", ws.numel(), _mx_u8, device), 0 if ws is None else ws.numel(),
+                       stream_ptr)
     if st:
         _check(st, "kq_route")
 
@@ -743,11 +760,12 @@ def kq_route_backward(logits, dlogits, weight, expert, counts, dweight=None, dlo
     if erows != rows:
         raise ValueError(f"expert must have {rows} rows")
     n, device = rows * top, logits.get_device()
-    _mx_same(device, dlogits, weight, expert, counts, dweight, dloss)
+    _mx_same(device, dlogits)
     st = _lib.kq_route_backward(xp, xt, rows, experts, ld, top, 1 if normalize else 0,
-                                _mx_vector(weight, "weight", n, _mx_f32), _mx_vector(expert, "expert", n, _mx_i32),
-                                _mx_vector(counts, "counts", experts + 2, _mx_i32), _mx_vector(dweight, "dweight", n, _mx_f32),
-                                _mx_vector(dloss, "dloss", 1, _mx_f32), gp, ldd, _mx_here(device, stream))
+                                _mx_buffer(weight, "weight", n, _mx_f32, device), _mx_buffer(expert, "expert", n, _mx_i32, device),
+                                _mx_buffer(counts, "counts", experts + 2, _mx_i32, device),
+                                _mx_buffer(dweight, "dweight", n, _mx_f32, device), _mx_buffer(dloss, "dloss", 1, _mx_f32, device),
+                                gp, ldd, _mx_here(device, stream))
     if st:
         _check(st, "kq_route_backward")
 
@@ -769,9 +787,9 @@ def kq_combine(z, slot, y, weight=None, residual=None, stream=None) -> None:
         if rrows != rows or rcols != n:
             raise ValueError(f"residual must be {(rows, n)}")
     device = y.get_device()
-    _mx_same(device, z, slot, weight, residual)
-    st = _lib.kq_combine(zp, zt, slots, n, ldz, _mx_vector(slot, "slot", rows * top, _mx_i32),
-                         _mx_vector(weight, "weight", rows * top, _mx_f32), rows, top, rp, rt, ldr, yp, yt, ldy,
+    _mx_same(device, z, residual)
+    st = _lib.kq_combine(zp, zt, slots, n, ldz, _mx_buffer(slot, "slot", rows * top, _mx_i32, device),
+                         _mx_buffer(weight, "weight", rows * top, _mx_f32, device), rows, top, rp, rt, ldr, yp, yt, ldy,
                          _mx_here(device, stream))
     if st:
         _check(st, "kq_combine")
@@ -793,10 +811,11 @@ def kq_combine_backward(dy, z, slot, dz=None, weight=None, dweight=None, stream=
         if ot != zt or orows != slots or ocols != n:
             raise ValueError("dz must have the type and shape of z")
     device = dy.get_device()
-    _mx_same(device, z, slot, weight, dz, dweight)
+    _mx_same(device, z, dz)
     st = _lib.kq_combine_backward(gp, gt, rows, n, lddy, zp, zt, slots, ldz,
-                                  _mx_vector(slot, "slot", rows * top, _mx_i32), _mx_vector(weight, "weight", rows * top, _mx_f32),
-                                  top, op, ldo, _mx_vector(dweight, "dweight", rows * top, _mx_f32),
+                                  _mx_buffer(slot, "slot", rows * top, _mx_i32, device),
+                                  _mx_buffer(weight, "weight", rows * top, _mx_f32, device), top, op, ldo,
+                                  _mx_buffer(dweight, "dweight", rows * top, _mx_f32, device),
                                   _mx_here(device, stream))
     if st:
         _check(st, "kq_combine_backward")

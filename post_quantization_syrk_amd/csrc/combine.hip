@@ -1,6 +1,7 @@
 // The sum of the experts' rows back to the rows that they came from, and its gradients.
 #include "device_util.h"
 #include "kq_internal.h"
+#include "lanes.h"
 
 #include <algorithm>
 
@@ -98,57 +99,69 @@ struct BackArgs {
   float* dweight;
 };
 
-// A row per workgroup of WAVES, KB choices at a time.
-constexpr int KB = 8;
-template <typename D, typename Z, int WAVES>
+// A row per workgroup of WAVES, KB choices at a time: their reads go out together, each choice's
+// slot being the same for all lanes.
+template <typename D, typename Z, int WAVES, int KB>
 __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
   __shared__ float sums[WAVES][KB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
-    const D* dy = (const D*)a.dy + t * a.lddy;
-    for (int j0 = 0; j0 < a.top; j0 += KB) {
-      int s[KB];
-      float w[KB], dot[KB];
+  const int64_t t = blockIdx.x;
+  const D* dy = (const D*)a.dy + t * a.lddy;
+  for (int j0 = 0; j0 < a.top; j0 += KB) {
+    int s[KB];
+    float w[KB], dot[KB];
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
-        const int64_t at = t * a.top + min(j0 + j, a.top - 1);
-        const int k = a.slot[at];
-        s[j] = j0 + j < a.top && k >= 0 && k < a.slots ? k : -1;
-        w[j] = a.weight ? a.weight[at] : 1.f;
-        dot[j] = 0.f;
-      }
-      for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
-        const Pack<D> d = load(dy, c, a.n);
+    for (int j = 0; j < KB; ++j) {
+      const int64_t at = t * a.top + min(j0 + j, a.top - 1);
+      const int k = __builtin_amdgcn_readfirstlane(a.slot[at]);
+      s[j] = j0 + j < a.top && k >= 0 && k < a.slots ? k : -1;
+      w[j] = a.weight ? a.weight[at] : 1.f;
+      dot[j] = 0.f;
+    }
+    for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
+      const Pack<D> d = load(dy, c, a.n);
+      Pack<Z> z[KB];
+      if (a.dweight) {
 #pragma unroll
-        for (int j = 0; j < KB; ++j) {
-          if (s[j] < 0) continue;
-          if (a.dweight) {
-            const Pack<Z> z = load((const Z*)a.z + s[j] * a.ldz, c, a.n);
+        for (int j = 0; j < KB; ++j)
+          if (s[j] >= 0) z[j] = load((const Z*)a.z + s[j] * a.ldz, c, a.n);
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[j] += value(d.v[i]) * value(z.v[i]);
+        for (int j = 0; j < KB; ++j)
+          if (s[j] >= 0) {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) dot[j] += value(d.v[i]) * value(z[j].v[i]);
           }
-          if (a.dz) {
+      }
+      if (a.dz) {
+#pragma unroll
+        for (int j = 0; j < KB; ++j)
+          if (s[j] >= 0) {
             float v[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[i] = w[j] * value(d.v[i]);
             store((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
           }
-        }
       }
-      if (!a.dweight) continue;
+    }
+    if (!a.dweight) continue;
 #pragma unroll
-      for (int j = 0; j < KB; ++j) {
+    for (int j = 0; j < KB; ++j) dot[j] = reduce_lanes<64>(dot[j], [](float x, float y) { return x + y; });
+    if constexpr (WAVES > 1) {
 #pragma unroll
-        for (int o = 1; o < 64; o <<= 1) dot[j] += __shfl_xor(dot[j], o);
+      for (int j = 0; j < KB; ++j)
         if (lane == 0) sums[wave][j] = dot[j];
-      }
       __syncthreads();
       if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.top) {
         float v = 0.f;
+#pragma unroll
         for (int k = 0; k < WAVES; ++k) v += sums[k][threadIdx.x];
         a.dweight[t * a.top + j0 + threadIdx.x] = v;
       }
       __syncthreads();
+    } else {
+#pragma unroll
+      for (int j = 0; j < KB; ++j)
+        if (lane == j && j0 + j < a.top) a.dweight[t * a.top + j0 + j] = dot[j];
     }
   }
 }
@@ -179,15 +192,19 @@ kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
   return KQ_OK;
 }
 
-template <typename D, typename Z>
+template <typename D, typename Z, int KB>
 kq_status launch_backward(const BackArgs& a, hipStream_t s) {
   const dim3 grid((unsigned)a.rows);
   if (a.n <= 64 * VEC * 4)
-    combine_backward_kernel<D, Z, 1><<<grid, dim3(64), 0, s>>>(a);
+    combine_backward_kernel<D, Z, 1, KB><<<grid, dim3(64), 0, s>>>(a);
   else
-    combine_backward_kernel<D, Z, 4><<<grid, dim3(256), 0, s>>>(a);
+    combine_backward_kernel<D, Z, 4, KB><<<grid, dim3(256), 0, s>>>(a);
   KQ_LAUNCHED("combine_backward_kernel");
   return KQ_OK;
+}
+template <typename D, typename Z>
+kq_status launch_backward(const BackArgs& a, hipStream_t s) {
+  return a.top <= 2 ? launch_backward<D, Z, 2>(a, s) : a.top <= 4 ? launch_backward<D, Z, 4>(a, s) : launch_backward<D, Z, 8>(a, s);
 }
 
 }  // namespace

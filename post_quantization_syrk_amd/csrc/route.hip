@@ -8,6 +8,7 @@
 // first kernel does all of it.  Every order is that of the rows, so nothing depends on timing.
 #include "device_util.h"
 #include "kq_internal.h"
+#include "lanes.h"
 
 #include <algorithm>
 
@@ -82,45 +83,22 @@ __device__ __forceinline__ void load_row(const T* p, int l, int n, bool wide, fl
   }
 }
 
-// Over the LPR lanes (16 or 64) of a row, the result in all of them: rotations inside sixteen lanes,
-// which cost no more than the operation, then exchanges of sixteens and halves.
-template <int CTRL, typename V>
-__device__ __forceinline__ V moved(V v) {
-  return __builtin_bit_cast(V, __builtin_amdgcn_mov_dpp(__builtin_bit_cast(int, v), CTRL, 0xf, 0xf, true));
-}
-template <int LPR, typename V, typename F>
-__device__ __forceinline__ V reduce_row(V v, F f) {
-  v = f(v, moved<0x128>(v));
-  v = f(v, moved<0x124>(v));
-  v = f(v, moved<0x122>(v));
-  v = f(v, moved<0x121>(v));
-  if constexpr (LPR == 64) {
-    unsigned u = __builtin_bit_cast(unsigned, v);
-    const auto a = __builtin_amdgcn_permlane16_swap(u, u, false, false);
-    const unsigned a0 = a[0], a1 = a[1];
-    v = f(__builtin_bit_cast(V, a0), __builtin_bit_cast(V, a1));
-    u = __builtin_bit_cast(unsigned, v);
-    const auto b = __builtin_amdgcn_permlane32_swap(u, u, false, false);
-    const unsigned b0 = b[0], b1 = b[1];
-    v = f(__builtin_bit_cast(V, b0), __builtin_bit_cast(V, b1));
-  }
-  return v;
-}
+// Over the LPR lanes of a row, the result in all of them.
 template <int LPR>
 __device__ __forceinline__ float row_max(float v) {
-  return reduce_row<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
+  return reduce_lanes<LPR>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 template <int LPR>
 __device__ __forceinline__ float row_sum(float v) {
-  return reduce_row<LPR>(v, [](float a, float b) { return a + b; });
+  return reduce_lanes<LPR>(v, [](float a, float b) { return a + b; });
 }
 template <int LPR>
 __device__ __forceinline__ int row_min(int v) {
-  return reduce_row<LPR>(v, [](int a, int b) { return min(a, b); });
+  return reduce_lanes<LPR>(v, [](int a, int b) { return min(a, b); });
 }
 template <int LPR>
 __device__ __forceinline__ int row_top(int v) {
-  return reduce_row<LPR>(v, [](int a, int b) { return max(a, b); });
+  return reduce_lanes<LPR>(v, [](int a, int b) { return max(a, b); });
 }
 
 // Keys of a row's values: whole numbers in the values' order, whose lowest bits make room for the
@@ -706,7 +684,7 @@ extern "C" kq_status kq_route_workspace(int64_t rows, int experts, int top, size
   int chunks;
   int64_t per;
   deal(rows, experts, &chunks, &per);
-  *bytes = round16(sizeof(int32_t) * (size_t)chunks * (experts + 1)) + round16(sizeof(float) * (size_t)chunks * experts) + sizeof(double) * experts;
+  *bytes = chunks == 1 ? 0 : round16(sizeof(int32_t) * (size_t)chunks * (experts + 1)) + round16(sizeof(float) * (size_t)chunks * experts) + sizeof(double) * experts;
   return KQ_OK;
 }
 
@@ -723,14 +701,14 @@ extern "C" kq_status kq_route(const void* logits, int type, int64_t rows, int ex
     return fail(KQ_EINVAL, "%s: an output is not aligned to its type", fn);
   size_t need;
   KQ_TRY(kq_route_workspace(rows, experts, top, &need));
-  if (!ws || ws_bytes < need || ((uintptr_t)ws & 15)) return fail(KQ_EWORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
+  if (need > 0 && (!ws || ws_bytes < need || ((uintptr_t)ws & 15))) return fail(KQ_EWORKSPACE, "%s: needs %zu bytes of 16-byte aligned workspace", fn, need);
   hipStream_t s = as_stream(stream);
   RouteArgs a{};
   a.logits = logits; a.rows = rows; a.ld = ld; a.experts = experts; a.top = top; a.normalize = normalize;
   a.weight = weight; a.expert = expert; a.slot = slot; a.index = index; a.offsets = offsets; a.counts = counts;
   a.loss = loss_opt;
   deal(rows, experts, &a.chunks, &a.per);
-  a.hist = (int32_t*)ws;
+  a.hist = (int32_t*)ws;   // (one chunk has no use for it)
   a.prob = (float*)((char*)ws + round16(sizeof(int32_t) * (size_t)a.chunks * (experts + 1)));
   a.mean = (double*)((char*)a.prob + round16(sizeof(float) * (size_t)a.chunks * experts));
   KQ_TRY(by_width<RouteRows>(type, experts, RouteLaunch{a, s}));

@@ -713,8 +713,9 @@ def test_the_binding_refuses():
         kq.kq_route(x[:1].expand(8, 4), **r.dict())                       # rows that overlap
     with pytest.raises(ValueError):
         kq.kq_route(x.t().contiguous().t(), **r.dict())
+    many = Routes(5000, 4, 2)
     with pytest.raises(kq.KQError):
-        kq.kq_route(x, ws=torch.empty(16, dtype=torch.uint8, device="cuda"), **r.dict())
+        kq.kq_route(torch.randn(5000, 4, device="cuda"), ws=torch.empty(16, dtype=torch.uint8, device="cuda"), **many.dict())
     with pytest.raises(ValueError):
         kq.kq_route_backward(x, x.bfloat16(), r.weight, r.expert, r.counts)
     z, y = torch.randn(16, 12, device="cuda"), torch.empty(8, 12, device="cuda")

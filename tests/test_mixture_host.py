@@ -78,7 +78,7 @@ def test_combine_gradients_against_differences():
 
 
 def _route(**kw):
-    a = dict(x=P, type=kq.KQ_F32, rows=8, experts=4, ld=4, top=2, norm=0, w=P, e=P, s=P, i=P, o=P, c=P, loss=None,
+    a = dict(x=P, type=kq.KQ_F32, rows=8000, experts=4, ld=4, top=2, norm=0, w=P, e=P, s=P, i=P, o=P, c=P, loss=None,
              ws=P, bytes=1 << 20)
     a.update(kw)
     return kq.load_library().kq_route(*a.values(), None)
@@ -114,9 +114,9 @@ def test_route_backward_refuses(kw, status):
 
 
 def test_route_workspace():
-    assert kq.kq_route_workspace(0, 1, 1) > 0
+    assert kq.kq_route_workspace(0, 1, 1) == 0
     sizes = [kq.kq_route_workspace(r, 64, 2) for r in (1, 100, 10_000, 1 << 20, 1 << 29)]
-    assert sizes == sorted(sizes) and sizes[-1] < 1 << 25
+    assert sizes == sorted(sizes) and 0 < sizes[2] and sizes[-1] < 1 << 25
     for bad in ((-1, 4, 1), (4, 0, 1), (4, 4, 5), (1 << 30, 4, 2)):
         with pytest.raises(kq.KQError) as e:
             kq.kq_route_workspace(*bad)
