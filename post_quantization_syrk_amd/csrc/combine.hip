@@ -11,14 +11,26 @@ namespace {
 constexpr int VEC = 8;   // neighbouring columns of a lane
 constexpr int MAX_TOP = 64;
 
-// Eight values as they lie in memory, at any alignment of their type.
+// Eight neighbouring values, read and written 16 bytes at a time at any alignment of their type (as
+// single values the compiler would take them apart: 508 us where this takes XXX).
 template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Pack {
-  T v[VEC];
+struct __attribute__((packed, aligned(sizeof(T)))) Words {
+  u32x4 v[VEC * sizeof(T) / 16];
+};
+template <typename T>
+struct Pack {
+  u32x4 v[VEC * sizeof(T) / 16];
+  __device__ __forceinline__ float operator[](int i) const {
+    if constexpr (sizeof(T) == 4)
+      return __uint_as_float(v[i / 4][i % 4]);
+    else
+      return __uint_as_float(i & 1 ? v[0][i / 2] & 0xffff0000u : v[0][i / 2] << 16);
+  }
 };
 
-__device__ __forceinline__ float value(float v) { return v; }
-__device__ __forceinline__ float value(uint16_t v) { return __uint_as_float((unsigned)v << 16); }
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+__device__ __forceinline__ unsigned pair(float lo, float hi) { return __builtin_bit_cast(unsigned, bf16x2{(__bf16)lo, (__bf16)hi}); }
 __device__ __forceinline__ void put(float v, float& to) { to = v; }
 __device__ __forceinline__ void put(float v, uint16_t& to) { to = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
@@ -27,25 +39,36 @@ template <typename T>
 __device__ __forceinline__ Pack<T> load(const T* row, int64_t c, int64_t n) {
   Pack<T> k{};
   if (c + VEC <= n) {
-    k = *(const Pack<T>*)(row + c);
+    const Words<T> w = *(const Words<T>*)(row + c);
+#pragma unroll
+    for (int i = 0; i < (int)(VEC * sizeof(T) / 16); ++i) k.v[i] = w.v[i];
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      if (c + i < n) k.v[i] = row[c + i];
+      if (c + i < n) {
+        if constexpr (sizeof(T) == 4)
+          k.v[i / 4][i % 4] = __float_as_uint(row[c + i]);
+        else
+          k.v[0][i / 2] |= (unsigned)row[c + i] << (16 * (i & 1));
+      }
   }
   return k;
 }
 template <typename T>
 __device__ __forceinline__ void store(T* row, int64_t c, int64_t n, const float (&v)[VEC]) {
-  Pack<T> k;
-#pragma unroll
-  for (int i = 0; i < VEC; ++i) put(v[i], k.v[i]);
   if (c + VEC <= n) {
-    *(Pack<T>*)(row + c) = k;
+    Words<T> w;
+    if constexpr (sizeof(T) == 4) {
+      w.v[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
+      w.v[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
+    } else {
+      w.v[0] = u32x4{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
+    }
+    *(Words<T>*)(row + c) = w;
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
-      if (c + i < n) row[c + i] = k.v[i];
+      if (c + i < n) put(v[i], row[c + i]);
   }
 }
 
@@ -72,7 +95,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
     if (a.residual) {
       const Pack<R> r = load((const R*)a.residual + t * a.ldr, c, a.n);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] = value(r.v[i]);
+      for (int i = 0; i < VEC; ++i) acc[i] = r[i];
     }
     for (int j = 0; j < a.top; ++j) {
       const int s = a.slot[t * a.top + j];
@@ -80,7 +103,7 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
       Pack<Z> k{};
       if (s >= 0 && s < a.slots) k = load((const Z*)a.z + s * a.ldz, c, a.n);
 #pragma unroll
-      for (int i = 0; i < VEC; ++i) acc[i] += w * value(k.v[i]);
+      for (int i = 0; i < VEC; ++i) acc[i] += w * k[i];
     }
     store((Y*)a.y + t * a.ldy, c, a.n, acc);
   }
@@ -129,7 +152,7 @@ __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a
         for (int j = 0; j < KB; ++j)
           if (s[j] >= 0) {
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[j] += value(d.v[i]) * value(z[j].v[i]);
+            for (int i = 0; i < VEC; ++i) dot[j] += d[i] * z[j][i];
           }
       }
       if (a.dz) {
@@ -138,7 +161,7 @@ __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a
           if (s[j] >= 0) {
             float v[VEC];
 #pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = w[j] * value(d.v[i]);
+            for (int i = 0; i < VEC; ++i) v[i] = w[j] * d[i];
             store((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
           }
       }
