@@ -492,33 +492,30 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
         bias[k] = a.bias ? __int_as_float(read_lds((const int*)(bias_lds[turn & 1] + (wc * 32 + l32) * NT + k))) : 0.f;
       // Four rows of the lane's, rows 8 g + 4 q of m's: their values
       auto finish = [&](const f32x16 (&sums)[NT], int g, float (&v)[4 * W]) {
-        float s[NT][4];
+        float s[4 * W];   // the gate's, or all
 #pragma unroll
-        for (int k = 0; k < NT; ++k)
+        for (int i = 0; i < 4; ++i)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[k][i] = sums[k][4 * g + i] + bias[k];
-        activate(a.act, s[0]);
-        if constexpr (EPI == EPI_PLAIN && NT == 2) activate(a.act, s[NT - 1]);
+          for (int k = 0; k < W; ++k) s[i * W + k] = sums[k][4 * g + i] + bias[k];
+        activate(a.act, s);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           if constexpr (EPI == EPI_GATED) {
-            v[i] = NT == 2 ? s[0][i] * s[NT - 1][i] : s[0][i] * other_lane(sums[0][4 * g + i] + bias[0]);
+            const float other = sums[NT - 1][4 * g + i] + bias[NT - 1];
+            v[i] = s[i] * (NT == 2 ? other : other_lane(other));
           } else {
 #pragma unroll
-            for (int k = 0; k < W; ++k) v[i * W + k] = s[k][i];
+            for (int k = 0; k < W; ++k) v[i * W + k] = s[i * W + k];
           }
         }
       };
       if (!a.y_far && (W == 1 || t.n0 + BN <= a.N || a.N % NT == 0)) {
-        // Step k: rows 8 (k % 4) + 4 q .. + 3 of m = k / 4.  The four rows' offsets are the same in every
-        // step, from a base that moves on (64 offsets of their own would spill).
+        // Step k: rows 8 (k % 4) + 4 q .. + 3 of m = k / 4.
         const int r_size = a.r_bf16 ? 2 : 4, pitch = (int)a.ldy * size, r_pitch = (int)a.ldr * r_size;
-        uint8_t* y1 = (uint8_t*)a.y + ((int64_t)t.m0 * a.ldy + f0) * size;
-        const uint8_t* r1 = (const uint8_t*)a.residual + ((int64_t)t.m0 * a.ldr + f0) * r_size;
-        auto view = [&](const uint8_t* base, int bytes, int k) {
-          const int back = (8 * (k % 4) * MT + k / 4) * bytes;
-          return rsrc(base + back, rows < BM ? max(rows * bytes - back, 0) : OOB);
-        };
+        const __amdgpu_buffer_rsrc_t ry = rsrc((uint8_t*)a.y + ((int64_t)t.m0 * a.ldy + f0) * size, rows < BM ? rows * pitch : OOB);
+        const __amdgpu_buffer_rsrc_t rr = rsrc((const uint8_t*)a.residual + ((int64_t)t.m0 * a.ldr + f0) * r_size,
+                                               rows < BM ? rows * r_pitch : OOB);
+        auto row_of = [](int k, int i) { return (8 * (k % 4) + i) * MT + k / 4; };
         const int row0 = wr * 32 * MT + q * 4 * MT;
         const bool in = stores && f0 + col + W <= cols;
         const int at = in ? row0 * pitch + col * size : OOB;   // (masked, and so it is with rows added)
@@ -529,12 +526,11 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
         u32x16 raw{};
         auto fetch = [&](int k, auto words) {
           constexpr int D = decltype(words)::value;
-          const __amdgpu_buffer_rsrc_t rr = view(r1, r_pitch, k);
-          int lane_from = from;
+          int lane_from = from;   // (each step's offsets in their turn: all of them at once would spill)
           asm volatile("" : "+v"(lane_from));
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int off = lane_from + i * MT * r_pitch, to = D * (4 * k % (16 / D) + i);
+            const int off = lane_from + row_of(k, i) * r_pitch, to = D * (4 * k % (16 / D) + i);
             if constexpr (D == 2) {
               const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(rr, off, 0, 0);
               raw[to] = u[0];
@@ -545,11 +541,10 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
           }
         };
         auto fetch_half = [&](int k) {   // one bf16 value per row
-          const __amdgpu_buffer_rsrc_t rr = view(r1, r_pitch, k);
           int lane_from = from;
           asm volatile("" : "+v"(lane_from));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) raw[4 * (k % 4) + i] = __builtin_amdgcn_raw_buffer_load_b16(rr, lane_from + i * MT * r_pitch, 0, 0);
+          for (int i = 0; i < 4; ++i) raw[4 * (k % 4) + i] = __builtin_amdgcn_raw_buffer_load_b16(rr, lane_from + row_of(k, i) * r_pitch, 0, 0);
         };
         auto fetch_ahead = [&](int k, int first, int count) {   // steps k + first .. of this residual's distance
           if (W == 1 && a.r_bf16) {
@@ -588,7 +583,6 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
             }
             fetch_ahead(k, 4, 1);
           }
-          const __amdgpu_buffer_rsrc_t ry = view(y1, pitch, k);
           int lane_at = at;
           asm volatile("" : "+v"(lane_at));
           auto store = [&](auto put) {
@@ -597,7 +591,7 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
               float o[W];
 #pragma unroll
               for (int c = 0; c < W; ++c) o[c] = v[i * W + c];
-              put(lane_at + i * MT * pitch, o);
+              put(lane_at + row_of(k, i) * pitch, o);
             }
           };
           if (a.y_bf16)
