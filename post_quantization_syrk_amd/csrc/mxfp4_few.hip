@@ -210,9 +210,18 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
   const int count = (t.last - t.m0) * COLS;
   for (int o = threadIdx.x; o < count; o += 64 * WAVES) {
     const int r = o / COLS, c = o % COLS;
-    float v = 0.f;
+    float v = 0.f, u = 0.f;   // (gated: a pair, in one read)
 #pragma unroll
-    for (int w = 0; w < WAVES; ++w) v += lds[(w * BM + r) * LD + PAIR * c];
+    for (int w = 0; w < WAVES; ++w) {
+      const float* from = lds + (w * BM + r) * LD + PAIR * c;
+      if constexpr (EPI == EPI_GATED) {
+        const float2 both = *(const float2*)from;
+        v += both.x;
+        u += both.y;
+      } else {
+        v += *from;
+      }
+    }
     if (t.n0 + PAIR * c >= a.N) continue;
     if constexpr (EPI != EPI_NONE) {
       const float* bias = a.bias + (int64_t)t.e * a.N + w0 + c;
@@ -221,9 +230,6 @@ __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, Ro
       activate(a.act, half);
       v = half[0];
       if constexpr (EPI == EPI_GATED) {
-        float u = 0.f;
-#pragma unroll
-        for (int w = 0; w < WAVES; ++w) u += lds[(w * BM + r) * LD + 2 * c + 1];
         if (a.bias) u += bias[a.N >> 1];
         v *= u;
       }
@@ -296,23 +302,29 @@ bool mx_few_fused(const ProductArgs& p, const MxRows& x) {
 kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, bool fused, hipStream_t s) {
   RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block))};
   const int bm = fused || average_rows(p) <= 16 ? 16 : 32;
-  // Columns per workgroup: 64, so that its rows of x and its fixed costs serve more of the layer, or
-  // as few as leave a workgroup for five of eight compute units (16 rows, 4096 x 4096: 3.7 us
-  // with 16, 6.5 with 64; 11008 x 4096: 8.2 and 7.6; 28672 x 8192: 30 and 24).
-  const int64_t tm = even_tiles(p, bm);
-  const int64_t enough = device_cu_count() * 5 / 8;
-  const int nt = ceil_div(p.N, 64) * tm >= enough ? 4 : ceil_div(p.N, 32) * tm >= enough ? 2 : 1;
+  // Columns per workgroup, 16 to 64: more of them serve its rows of x and its fixed costs, which are worth
+  // about 16 columns; and what the busiest compute unit has to do counts (16 rows, 4096 x 4096: 3.7 us
+  // with 16, 6.5 with 64; 28672 x 8192: 30 and 24).
+  const int64_t tm = even_tiles(p, bm), cus = device_cu_count();
+  int nt = 1;
+  int64_t least = 0;
+  for (int k = bm == 32 ? 2 : 4; k > 0; --k) {
+    const int64_t cost = ceil_div(ceil_div(p.N, 16 * k) * tm, cus) * (16 * k + 16);
+    if (least == 0 || cost < least) {
+      least = cost;
+      nt = k;
+    }
+  }
   if (fused) {
     const bool f32 = x.type == KQ_F32, wide = wide_rows(x);
 #define KQ_FEW(NT, U)                                                                               \
   (f32 ? launch<8, 1, NT, U, float, true>(p, r, s)                                                   \
        : wide ? launch<8, 1, NT, U, uint16_t, true>(p, r, s) : launch<8, 1, NT, U, uint16_t, false>(p, r, s))
-    return nt == 4 ? KQ_FEW(4, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
+    return nt == 4 ? KQ_FEW(4, 1) : nt == 3 ? KQ_FEW(3, 1) : nt == 2 ? KQ_FEW(2, 2) : KQ_FEW(1, 2);
 #undef KQ_FEW
   }
-  // (32 rows never come with 64 columns: where mx_few takes them, such tiles are half as many as the
-  // compute units at most)
   if (bm == 32) return nt == 1 ? launch<8, 2, 1, 2, void>(p, r, s) : launch<8, 2, 2, 2, void>(p, r, s);
+  if (nt == 3) return launch<8, 1, 3, 1, void>(p, r, s);
   return nt == 4 ? launch<8, 1, 4, 1, void>(p, r, s) : nt == 2 ? launch<8, 1, 2, 2, void>(p, r, s) : launch<8, 1, 1, 2, void>(p, r, s);
 }
 
