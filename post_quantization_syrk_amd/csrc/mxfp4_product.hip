@@ -490,18 +490,21 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
 #pragma unroll
       for (int k = 0; k < NT; ++k)
         bias[k] = a.bias ? __int_as_float(read_lds((const int*)(bias_lds[turn & 1] + (wc * 32 + l32) * NT + k))) : 0.f;
-      // Four rows of the lane's, rows 8 g + 4 q of m's: their values
-      auto finish = [&](const f32x16 (&sums)[NT], int g, float (&v)[4 * W]) {
-        float s[4 * W];   // the gate's, or all
+      // The lane's sixteen rows of each m are finished R at a time: all of them in the smallest tiles, where
+      // every jump to code that no one has run yet shows (16 x 4096 to 2 x 11008, four at a time: XXX us,
+      // sixteen YYY), four in the largest, for want of registers.
+      constexpr int R = MT * NT == 1 ? 16 : 4, PARTS = 16 / R;
+      auto finish = [&](const f32x16 (&sums)[NT], int part, float (&v)[R * W]) {
+        float s[R * W];   // the gate's, or all
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int k = 0; k < W; ++k) s[i * W + k] = sums[k][4 * g + i] + bias[k];
+          for (int k = 0; k < W; ++k) s[i * W + k] = sums[k][R * part + i] + bias[k];
         activate(a.act, s);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
           if constexpr (EPI == EPI_GATED) {
-            const float other = sums[NT - 1][4 * g + i] + bias[NT - 1];
+            const float other = sums[NT - 1][R * part + i] + bias[NT - 1];
             v[i] = s[i] * (NT == 2 ? other : other_lane(other));
           } else {
 #pragma unroll
@@ -509,85 +512,82 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
           }
         }
       };
+      // Row i of step k, from the lane's first one of the tile.
+      auto row_of = [](int k, int i) {
+        const int j = R * (k % PARTS) + i;
+        return ((j >> 2) * 8 + (j & 3)) * MT + k / PARTS;
+      };
       if (!a.y_far && (W == 1 || t.n0 + BN <= a.N || a.N % NT == 0)) {
-        // Step k: rows 8 (k % 4) + 4 q .. + 3 of m = k / 4.
         const int r_size = a.r_bf16 ? 2 : 4, pitch = (int)a.ldy * size, r_pitch = (int)a.ldr * r_size;
         const __amdgpu_buffer_rsrc_t ry = rsrc((uint8_t*)a.y + ((int64_t)t.m0 * a.ldy + f0) * size, rows < BM ? rows * pitch : OOB);
         const __amdgpu_buffer_rsrc_t rr = rsrc((const uint8_t*)a.residual + ((int64_t)t.m0 * a.ldr + f0) * r_size,
                                                rows < BM ? rows * r_pitch : OOB);
-        auto row_of = [](int k, int i) { return (8 * (k % 4) + i) * MT + k / 4; };
         const int row0 = wr * 32 * MT + q * 4 * MT;
         const bool in = stores && f0 + col + W <= cols;
         const int at = in ? row0 * pitch + col * size : OOB;   // (masked, and so it is with rows added)
         const int from = in ? row0 * r_pitch + col * r_size : OOB;
-        // Residuals are read ahead, since a step is far shorter than a read takes: four steps of one dword
-        // (two bf16 values, or one value) per row, two steps of two.
-        constexpr int STEPS = 4 * MT;
+        // Residuals are read ahead, since a step is far shorter than a read takes: sixteen dwords, of one
+        // value, of two bf16 values, or two of them for two fp32 values.
+        constexpr int STEPS = PARTS * MT;
         u32x16 raw{};
-        auto fetch = [&](int k, auto words) {
-          constexpr int D = decltype(words)::value;
+        auto fetch = [&](int k, auto words) {   // words: dwords per row, 0: half of one
+          constexpr int D = decltype(words)::value > 1 ? 2 : 1, AHEAD = 16 / (R * D);
+          if (k >= STEPS) return;
           int lane_from = from;   // (each step's offsets in their turn: all of them at once would spill)
           asm volatile("" : "+v"(lane_from));
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int off = lane_from + row_of(k, i) * r_pitch, to = D * (4 * k % (16 / D) + i);
-            if constexpr (D == 2) {
+          for (int i = 0; i < R; ++i) {
+            const int off = lane_from + row_of(k, i) * r_pitch, to = D * (R * (k % AHEAD) + i);
+            if constexpr (decltype(words)::value == 2) {
               const u32x2 u = __builtin_amdgcn_raw_buffer_load_b64(rr, off, 0, 0);
               raw[to] = u[0];
               raw[to + 1] = u[1];
-            } else {
+            } else if constexpr (decltype(words)::value == 1) {
               raw[to] = __builtin_amdgcn_raw_buffer_load_b32(rr, off, 0, 0);
+            } else {
+              raw[to] = __builtin_amdgcn_raw_buffer_load_b16(rr, off, 0, 0);
             }
           }
         };
-        auto fetch_half = [&](int k) {   // one bf16 value per row
-          int lane_from = from;
-          asm volatile("" : "+v"(lane_from));
+        constexpr int NEAR = 16 / (R * W), FAR = 16 / R;   // steps ahead of two dwords (W = 2), of one
+        if (a.residual) {
+          if (a.r_bf16) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) raw[4 * (k % 4) + i] = __builtin_amdgcn_raw_buffer_load_b16(rr, lane_from + row_of(k, i) * r_pitch, 0, 0);
-        };
-        auto fetch_ahead = [&](int k, int first, int count) {   // steps k + first .. of this residual's distance
-          if (W == 1 && a.r_bf16) {
-#pragma unroll
-            for (int j = 0; j < count; ++j)
-              if (k + first + j < STEPS) fetch_half(k + first + j);
-          } else if (W == 1 || a.r_bf16) {
-#pragma unroll
-            for (int j = 0; j < count; ++j)
-              if (k + first + j < STEPS) fetch(k + first + j, std::integral_constant<int, 1>());
+            for (int k = 0; k < FAR; ++k) fetch(k, std::integral_constant<int, W == 1 ? 0 : 1>());
           } else {
 #pragma unroll
-            for (int j = 0; j < (count + 1) / 2; ++j)
-              if (k + first / 2 + j < STEPS) fetch(k + first / 2 + j, std::integral_constant<int, 2>());
+            for (int k = 0; k < NEAR; ++k) fetch(k, std::integral_constant<int, W>());
           }
-        };
-        if (a.residual) fetch_ahead(0, 0, 4);
+        }
         f32x16 sums[NT];
 #pragma unroll
         for (int k = 0; k < STEPS; ++k) {
-          if (k % 4 == 0) take(k / 4, sums);
+          if (k % PARTS == 0) take(k / PARTS, sums);
           __builtin_amdgcn_sched_barrier(0);
-          float v[4 * W];
-          finish(sums, k % 4, v);
+          float v[R * W];
+          finish(sums, k % PARTS, v);
           if (a.residual) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
+              const unsigned u = raw[R * (k % FAR) + i];
               if constexpr (W == 1) {
-                const unsigned u = raw[4 * (k % 4) + i];
                 v[i] += __uint_as_float(a.r_bf16 ? u << 16 : u);
               } else {
-                const unsigned u = raw[4 * (k % 4) + i], f0 = raw[8 * (k % 2) + 2 * i], f1 = raw[8 * (k % 2) + 2 * i + 1];
-                v[2 * i] += __uint_as_float(a.r_bf16 ? u << 16 : f0);
-                v[2 * i + 1] += __uint_as_float(a.r_bf16 ? u & 0xffff0000u : f1);
+                const unsigned u0 = raw[2 * (R * (k % NEAR) + i)], u1 = raw[2 * (R * (k % NEAR) + i) + 1];
+                v[2 * i] += __uint_as_float(a.r_bf16 ? u << 16 : u0);
+                v[2 * i + 1] += __uint_as_float(a.r_bf16 ? u & 0xffff0000u : u1);
               }
             }
-            fetch_ahead(k, 4, 1);
+            if (a.r_bf16)
+              fetch(k + FAR, std::integral_constant<int, W == 1 ? 0 : 1>());
+            else
+              fetch(k + NEAR, std::integral_constant<int, W>());
           }
           int lane_at = at;
           asm volatile("" : "+v"(lane_at));
           auto store = [&](auto put) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < R; ++i) {
               float o[W];
 #pragma unroll
               for (int c = 0; c < W; ++c) o[c] = v[i * W + c];
@@ -601,33 +601,30 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
         }
       } else {
         // a last column that ends inside a lane's, or rows too far apart for 32-bit offsets
+        f32x16 sums[NT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          f32x16 sums[NT];
-          take(m, sums);
+        for (int k = 0; k < PARTS * MT; ++k) {
+          if (k % PARTS == 0) take(k / PARTS, sums);
+          float v[R * W];
+          __builtin_amdgcn_sched_barrier(0);
+          finish(sums, k % PARTS, v);
+          int part = q;
+          asm volatile("" : "+v"(part));   // each step's addresses in their turn
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[4 * W];
-            __builtin_amdgcn_sched_barrier(0);
-            finish(sums, g, v);
-            int part = q;
-            asm volatile("" : "+v"(part));   // each step's addresses in their turn
+          for (int i = 0; i < R; ++i) {
+            const int r = wr * 32 * MT + part * 4 * MT + row_of(k, i);
+            const int64_t row = t.m0 + r;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int r = wr * 32 * MT + (8 * g + part * 4 + i) * MT + m;
-              const int64_t row = t.m0 + r;
-#pragma unroll
-              for (int k = 0; k < W; ++k) {
-                if (r >= rows || !stores || f0 + col + k >= cols) continue;
-                float o = v[i * W + k];
-                const int64_t from = row * a.ldr + f0 + col + k, at = row * a.ldy + f0 + col + k;
-                if (a.residual)
-                  o += a.r_bf16 ? __uint_as_float((unsigned)((const uint16_t*)a.residual)[from] << 16) : ((const float*)a.residual)[from];
-                if (a.y_bf16)
-                  ((uint16_t*)a.y)[at] = to_bf16(o);
-                else
-                  ((float*)a.y)[at] = o;
-              }
+            for (int c = 0; c < W; ++c) {
+              if (r >= rows || !stores || f0 + col + c >= cols) continue;
+              float o = v[i * W + c];
+              const int64_t from = row * a.ldr + f0 + col + c, at = row * a.ldy + f0 + col + c;
+              if (a.residual)
+                o += a.r_bf16 ? __uint_as_float((unsigned)((const uint16_t*)a.residual)[from] << 16) : ((const float*)a.residual)[from];
+              if (a.y_bf16)
+                ((uint16_t*)a.y)[at] = to_bf16(o);
+              else
+                ((float*)a.y)[at] = o;
             }
           }
         }
