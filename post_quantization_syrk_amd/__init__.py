@@ -477,11 +477,13 @@ def kq_mxfp4_empty(rows: int, n: int, experts: int | None = None, device="cuda")
 _mx_types = None   # tensor type -> KQ_*, and the types below, once torch is imported
 _mx_f32 = _mx_bf16 = _mx_u8 = _mx_i8 = _mx_i32 = None
 _mx_stream_of = _mx_device = None
+_mx_single = False   # one device: whatever is on a device is on that one
 
 
 def _mx_setup() -> None:
-    global _mx_types, _mx_f32, _mx_bf16, _mx_u8, _mx_i8, _mx_i32, _mx_stream_of, _mx_device
+    global _mx_types, _mx_f32, _mx_bf16, _mx_u8, _mx_i8, _mx_i32, _mx_stream_of, _mx_device, _mx_single
     torch = _torch()
+    _mx_single = torch.cuda.device_count() == 1
     _mx_f32, _mx_bf16, _mx_u8, _mx_i8, _mx_i32 = (torch.float32, torch.bfloat16, torch.uint8, torch.int8, torch.int32)
     _mx_stream_of, _mx_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
     _mx_types = {_mx_f32: KQ_F32, _mx_bf16: KQ_BF16}
@@ -630,6 +632,8 @@ def _mx_here(device, stream) -> int:
 
 
 def _mx_same(device, *tensors) -> None:
+    if _mx_single:
+        return   # (each has been found to be on a device)
     for t in tensors:
         if t is not None and t.get_device() != device:
             raise ValueError(f"tensors on devices {device} and {t.get_device()}")
