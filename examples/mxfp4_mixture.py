@@ -7,9 +7,11 @@ The block: every token goes through a shared layer and through `top` of the expe
 few large channels, as those of language models do.  Preparation, once: the Hessian factor of the
 activations (kq_accumulate_hessian), the input side of the incoherence processing
 (kq_biip_rotate, KQ_BIIP_IN_ONLY; the experts of one product share its rescale and signs, so their
-weights go through it as one matrix) and kq_mxfp4_quantize.  Serving, per call: one
-kq_mxfp4_linear and two kq_mxfp4_experts.  Prints each product's error against fp32 with and
-without the processing, and the time of a call.
+weights go through it as one matrix) and kq_mxfp4_quantize.  Serving, per call: kq_route, the
+gated product of kq_mxfp4_experts_epilogue, kq_mxfp4_experts, kq_mxfp4_linear for the shared layer
+and kq_combine.  Training the router beside the quantised layers, per call: kq_combine_backward
+and kq_route_backward, with the balance loss.  Prints the error against fp32 with and without the
+processing, and the times of both.
 """
 import argparse
 import os
@@ -54,6 +56,23 @@ class Layers:
         kq.kq_mxfp4_experts(x, index, offsets, self.codes, self.scales, y, d=self.d, sign=self.sign, had=self.had)
         return y
 
+    def gated(self, x, index, offsets):
+        """silu(first half) * second half of the experts' products, by slots."""
+        h = torch.empty((index.shape[0], self.out // 2), dtype=torch.bfloat16, device="cuda")
+        kq.kq_mxfp4_experts_epilogue(x, index, offsets, self.codes, self.scales, h, d=self.d, sign=self.sign, had=self.had,
+                                     act="silu", gated=True)
+        return h
+
+
+class Routes:
+    """What kq_route leaves for `rows` rows: kq_route(logits, **vars(routes))."""
+
+    def __init__(self, rows, experts, top):
+        whole = lambda *shape: torch.empty(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.weight, self.loss = torch.empty((rows, top), device="cuda"), torch.empty(1, device="cuda")
+        self.expert, self.slot, self.index = whole(rows, top), whole(rows, top), whole(rows * top)
+        self.offsets, self.counts = whole(experts + 1), whole(experts + 2)
+
 
 def route(x, router, top):
     """Slots sorted by expert: (token of each slot int32, first slot of each expert int32, weight)."""
@@ -78,12 +97,28 @@ class Mixture:
         index, offsets, _ = route(calibration, router, top)
         self.down = Layers(down, gated(self.up.experts(calibration, index, offsets)), processed)
 
+    def forward(self, x):
+        """The block's output in fp32, and what the router's gradient needs."""
+        logits = x.float() @ self.router
+        routes = Routes(x.shape[0], logits.shape[1], self.top)
+        kq.kq_route(logits, **vars(routes))
+        z = self.down.experts(self.up.gated(x, routes.index, routes.offsets), None, routes.offsets)
+        out = torch.empty((x.shape[0], self.down.out), device="cuda")
+        kq.kq_combine(z, routes.slot, out, weight=routes.weight, residual=self.shared.linear(x))
+        return out, (x, logits, routes, z)
+
     def __call__(self, x):
-        index, offsets, weight = route(x, self.router, self.top)
-        inner = gated(self.up.experts(x, index, offsets))
-        y = self.down.experts(inner, None, offsets)
-        out = self.shared.linear(x).float()
-        return out.index_add_(0, index, y.float() * weight[:, None])
+        return self.forward(x)[0]
+
+    def router_gradient(self, dout, kept, balance=0.01):
+        """The gradient of sum(dout * output) + balance * (the balance loss) by the router's weights,
+        the quantised layers being what they are."""
+        x, logits, routes, z = kept
+        dweight, dlogits = torch.empty_like(routes.weight), torch.empty_like(logits)
+        kq.kq_combine_backward(dout, z, routes.slot, weight=routes.weight, dweight=dweight)
+        kq.kq_route_backward(logits, dlogits, routes.weight, routes.expert, routes.counts, dweight=dweight,
+                             dloss=torch.full((1,), balance, device="cuda"))
+        return x.float().T @ dlogits
 
 
 def plain(x, shared, up, down, router, top):
@@ -122,18 +157,17 @@ def main():
         error = (block(x) - want).norm() / want.norm()
         print(f"{'processed' if processed else 'as it is':10s} error against fp32 {float(error):.4f}")
     for tokens in (1, a.tokens):
-        index, offsets, _ = route(x[:tokens], weights[3], a.top)
-        inner = gated(block.up.experts(x[:tokens], index, offsets))
-        begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
-        for turn in range(30):
-            if turn == 10:
-                begin.record()
-            block.shared.linear(x[:tokens])
-            block.up.experts(x[:tokens], index, offsets)
-            block.down.experts(inner, None, offsets)
-        end.record()
-        end.synchronize()
-        print(f"{tokens} token{'s' if tokens > 1 else ''}: the three products {begin.elapsed_time(end) / 20 * 1e3:.1f} us")
+        rows, dout = x[:tokens], torch.randn((tokens, a.width), device="cuda")
+        kept = block.forward(rows)[1]
+        for what, call in (("output", lambda: block(rows)), ("router's gradient", lambda: block.router_gradient(dout, kept))):
+            begin, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            for turn in range(30):
+                if turn == 10:
+                    begin.record()
+                call()
+            end.record()
+            end.synchronize()
+            print(f"{tokens} token{'s' if tokens > 1 else ''}: {what} {begin.elapsed_time(end) / 20 * 1e3:.1f} us")
 
 
 if __name__ == "__main__":

@@ -660,7 +660,7 @@ kq_status kq_route_backward(const void* logits, int type, int64_t rows, int expe
  *   weight   device fp32 [rows][top], or NULL for 1
  *   residual device, rows x n of residual_type, leading dim ldr >= n, or NULL for 0; it may be y itself
  *            (the same address, type and leading dim)
- *   y        device, rows x n of y_type, leading dim ldy >= n
+ *   y        device, rows x n of y_type, leading dim ldy >= n; must not overlap z
  * All aligned to their type.  Sizes: 0 <= rows, slots <= 2^30, rows * top < 2^31, 1 <= n <= 2^24,
  * 1 <= top <= 64.  Asynchronous on `stream`; the same inputs give the same bits.
  */
@@ -677,7 +677,8 @@ kq_status kq_combine(const void* z, int z_type, int64_t slots, int64_t n, int64_
  *   z        device, as given to kq_combine; read only for dweight (else it may be NULL)
  *   slot, weight  as given to kq_combine.  No slot may be named twice within [0, slots)
  *   dz_opt   device, slots x n of z_type, leading dim lddz >= n, or NULL.  Rows of slots that no choice
- *            names are left as they were.  May be z itself (the same address and leading dim)
+ *            names are left as they were.  May be z itself (the same address and leading dim), else it must
+ *            not overlap z, nor dy
  *   dweight_opt  device fp32 [rows][top], or NULL; 0 for a slot outside [0, slots)
  * Alignment, sizes and determinism as for kq_combine; sums in fp32.
  */

@@ -12,7 +12,7 @@ constexpr int VEC = 8;   // neighbouring columns of a lane
 constexpr int MAX_TOP = 64;
 
 // Eight neighbouring values, read and written 16 bytes at a time at any alignment of their type (as
-// single values the compiler would take them apart: 508 us where this takes XXX).
+// single values the compiler takes them apart: 32768 x 2048 x 6 backwards 525 us, as words 338).
 template <typename T>
 struct __attribute__((packed, aligned(sizeof(T)))) Words {
   u32x4 v[VEC * sizeof(T) / 16];

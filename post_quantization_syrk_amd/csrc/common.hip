@@ -73,7 +73,7 @@ kq_status fill_u32(uint32_t* p, int64_t n, uint32_t v, hipStream_t s) {
 
 }  // namespace kq
 
-extern "C" int kq_version(void) { return 300; /* 0.3.0: MXFP4 */ }
+extern "C" int kq_version(void) { return 400; /* 0.4.0: what surrounds a mixture's products */ }
 
 extern "C" const char* kq_last_error(void) { return kq::g_last_error; }
 

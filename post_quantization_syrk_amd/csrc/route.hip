@@ -105,7 +105,7 @@ __device__ __forceinline__ int row_top(int v) {
 // column, counted down, so that they are distinct and the lower of two columns comes first.
 // bf16 values keep all their bits; of fp32 values as many go as columns need, and two neighbours
 // in the order that agree in the rest have to be compared in full (ambiguous).
-constexpr int KEY_FINITE = (int)0x80800000, KEY_INFINITE = 0x7f800000;   // the lowest number's, infinity's
+constexpr int KEY_FINITE = (int)0x80800000;   // the lowest number's; only -inf (and NaN) lies below
 __device__ __forceinline__ int key_of(float v, int low, int mask) {
   const int u = __float_as_int(v);
   return ((u ^ ((u >> 31) & 0x7fffffff)) & ~mask) | low;

@@ -100,7 +100,8 @@ def _route_check(r, x, top, normalize, want=None):
 
 ROUTES = [(1, 1, 1), (1, 8, 2), (2, 64, 6), (3, 5, 5), (5, 15, 2), (7, 16, 16), (33, 17, 4), (64, 32, 1), (65, 33, 3), (200, 60, 4),
           (130, 64, 8), (100, 100, 2), (77, 128, 8), (500, 256, 8), (37, 300, 6), (20, 512, 10), (9, 1000, 16), (6, 2048, 3), (5, 4096, 16),
-          (5000, 8, 2), (2049, 64, 6), (4100, 3, 3)]
+          (5000, 8, 2), (2049, 64, 6), (4100, 3, 3), (150, 300, 6), (700, 256, 16), (1500, 250, 8),
+          (300, 2000, 4), (129, 1, 1), (128, 64, 6), (1100, 1024, 9)]
 
 
 @pytest.mark.parametrize("kind", ["f32", "bf16"])
@@ -678,6 +679,40 @@ def test_a_captured_mixture():
             assert torch.equal(a, b)
         for name, v in fresh[0].dict().items():
             assert torch.equal(v, getattr(held[0], name)), name
+
+
+@pytest.mark.parametrize("tokens", [1, 33, 300])
+def test_the_examples_router_gradient(tokens):
+    """The example's gradient against autograd in 64 bits on the experts' rows that it computed."""
+    torch = torch_cuda()
+    import examples.mxfp4_mixture as ex
+    torch.manual_seed(tokens)
+    x, *weights = ex.make(128 + tokens, 256, 160, 6, seed=tokens)
+    calibration, x = x[:128], x[128:]
+    want = ex.plain(x, *weights, 2)          # (first: processing the weights is done in place)
+    block = ex.Mixture(*weights, 2, calibration)
+    out, kept = block.forward(x)
+    dout = torch.randn_like(out)
+    got = block.router_gradient(dout, kept, balance=0.5)
+    _, logits, routes, z = kept
+    l64 = logits.double().requires_grad_()
+    p = torch.softmax(l64, 1)
+    chosen = routes.expert.long()
+    rows = z[routes.slot.long()].double()
+    counts = routes.counts[:6].double()
+    loss = 6 * (counts / counts.sum() * p.mean(0)).sum()
+    w = p.gather(1, chosen)
+    dl = torch.autograd.grad(((w[:, :, None] * rows).sum(1) * dout.double()).sum() + 0.5 * loss, l64)[0]
+    assert abs(float(routes.loss) - float(loss.detach())) <= (100 + 6 + 16 + tokens) * U * float(loss.detach())
+    # dweight is off by (n + 2) u sum |dy z|, the softmax by the module's bound, the product by (T + 2) u
+    mag = (rows.abs() * dout.double().abs()[:, None]).sum(2)
+    size = p.detach() * (w.detach() * mag).sum(1, keepdim=True) + 0.5 * p.detach()
+    size = size.scatter_add(1, chosen, w.detach() * mag)
+    xd = x.double()
+    # (torch's fp32 product adds T terms in an order of its own)
+    bound = xd.abs().T @ (size * (256 + 2 + 500) * U) + (tokens + 2) * U * (xd.abs().T @ dl.abs())
+    assert bool(((got.double() - xd.T @ dl).abs() <= bound).all())
+    assert float((out - want).norm() / want.norm()) < 0.25      # (as the block's own test has it)
 
 
 def test_routing_on_two_streams_at_once():
