@@ -23,7 +23,7 @@ struct RouteArgs {
   const void* logits;
   int64_t rows, ld;
   int experts, top;
-  bool normalize, wide;   // wide: rows that may be read four values at a time
+  bool normalize;
   float* weight;
   int32_t* expert;
   int32_t* slot;
@@ -52,34 +52,64 @@ struct Row {
   __device__ static constexpr int column(int v) { return v / W * (LPR * W) + v % W; }   // plus W l
 };
 
-template <typename T, int LPR, int VPL>
-__device__ __forceinline__ void load_row(const T* p, int l, int n, bool wide, float (&r)[VPL]) {
-  using R = Row<LPR, VPL>;
-  if (wide) {
+// W neighbouring values in one access, at any alignment of their type.
+template <typename T, int W>
+struct Group {
+  static constexpr int WORDS = W * (int)sizeof(T) / 4;
+  typedef unsigned words __attribute__((ext_vector_type(WORDS > 0 ? WORDS : 1)));
+  struct __attribute__((packed, aligned(sizeof(T)))) Memory { words v; };
+
+  __device__ static __forceinline__ float value(T v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return bf16_value(v);
+  }
+  __device__ static __forceinline__ T raw(float v) {
+    if constexpr (sizeof(T) == 4) return v;
+    else return __builtin_bit_cast(uint16_t, (__bf16)v);
+  }
+  // Columns c .. c + W - 1 of a row of n, -inf past its end.
+  __device__ static __forceinline__ void load(const T* p, int c, int n, float (&r)[W]) {
+    if (WORDS > 0 && c + W <= n) {
+      const words u = ((const Memory*)(p + c))->v;
 #pragma unroll
-    for (int g = 0; g < VPL / R::W; ++g) {
-      const int c = R::column(g * R::W) + R::W * l;
-      if constexpr (sizeof(T) == 4) {
-        struct __attribute__((packed, aligned(4))) Pack { float v[R::W]; };
-        Pack k{};
-        if (c < n) k = *(const Pack*)(p + c);
+      for (int i = 0; i < W; ++i) {
+        if constexpr (sizeof(T) == 4) r[i] = __uint_as_float(u[i]);
+        else r[i] = __uint_as_float(i & 1 ? u[i / 2] & 0xffff0000u : u[i / 2] << 16);
+      }
+    } else {
 #pragma unroll
-        for (int i = 0; i < R::W; ++i) r[g * R::W + i] = c < n ? k.v[i] : -INFINITY;
-      } else {
-        struct __attribute__((packed, aligned(2))) Pack { uint16_t v[R::W]; };
-        Pack k{};
-        if (c < n) k = *(const Pack*)(p + c);
-#pragma unroll
-        for (int i = 0; i < R::W; ++i) r[g * R::W + i] = c < n ? bf16_value(k.v[i]) : -INFINITY;
+      for (int i = 0; i < W; ++i) {
+        r[i] = -INFINITY;
+        if (c + i < n) r[i] = value(p[c + i]);
       }
     }
-  } else {
+  }
+  __device__ static __forceinline__ void store(T* p, int c, int n, const float (&r)[W]) {
+    if (WORDS > 0 && c + W <= n) {
+      words u{};
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) {
-      const int c = R::column(v) + R::W * l;
-      r[v] = -INFINITY;
-      if (c < n) r[v] = sizeof(T) == 4 ? ((const float*)p)[c] : bf16_value(((const uint16_t*)p)[c]);
+      for (int i = 0; i < W; ++i) {
+        if constexpr (sizeof(T) == 4) u[i] = __float_as_uint(r[i]);
+        else u[i / 2] |= (unsigned)raw(r[i]) << (16 * (i & 1));
+      }
+      ((Memory*)(p + c))->v = u;
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i)
+        if (c + i < n) p[c + i] = raw(r[i]);
     }
+  }
+};
+
+template <typename T, int LPR, int VPL>
+__device__ __forceinline__ void load_row(const T* p, int l, int n, float (&r)[VPL]) {
+  constexpr int W = Row<LPR, VPL>::W;
+#pragma unroll
+  for (int g = 0; g < VPL; g += W) {
+    float v[W];
+    Group<T, W>::load(p, Row<LPR, VPL>::column(g) + W * l, n, v);
+#pragma unroll
+    for (int i = 0; i < W; ++i) r[g + i] = v[i];
   }
 }
 
@@ -161,7 +191,7 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
     const bool in = row < r1;
     const T* from = (const T*)a.logits + (in ? row : r0) * a.ld;
     float x[VPL];
-    load_row<T, LPR, VPL>(from, l, a.experts, a.wide, x);
+    load_row<T, LPR, VPL>(from, l, a.experts, x);
 #pragma unroll
     for (int v = 0; v < VPL; ++v) x[v] += 0.f;   // (-0 becomes 0, which it equals)
     float m = x[0];
@@ -215,7 +245,7 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
     }
     if (!clear) {
       // one choice after another: the first column of the largest value left
-      if constexpr (VPL <= 16) load_row<T, LPR, VPL>(from, l, a.experts, a.wide, x);   // (not held through the above)
+      if constexpr (VPL <= 16) load_row<T, LPR, VPL>(from, l, a.experts, x);   // (not held through the above)
       total = 0.f;
       chosen = -1;
       for (int j = 0; j < a.top; ++j) {
@@ -549,7 +579,7 @@ struct BackArgs {
   const void* logits;
   int64_t rows, ld, ldd;
   int experts, top;
-  bool normalize, wide;
+  bool normalize;
   const float* weight;
   const int32_t* expert;
   const int32_t* counts;
@@ -578,7 +608,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArg
     const bool in = row < r1;
     const int64_t from = in ? row : r0;
     float x[VPL];
-    load_row<T, LPR, VPL>((const T*)a.logits + from * a.ld, l, a.experts, a.wide, x);
+    load_row<T, LPR, VPL>((const T*)a.logits + from * a.ld, l, a.experts, x);
     int chosen = -1;
     float w = 0.f, g = 0.f;
     if (l < a.top) {
@@ -623,25 +653,11 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArg
     if (!in) continue;
     T* to = (T*)a.dlogits + row * a.ldd;
 #pragma unroll
-    for (int g4 = 0; g4 < VPL / R::W; ++g4) {
-      const int c = R::column(g4 * R::W) + R::W * l;
-      if (a.wide) {
-        struct __attribute__((packed, aligned(sizeof(T)))) Pack { T v[R::W]; };
-        Pack k;
+    for (int v = 0; v < VPL; v += R::W) {
+      float out[R::W];
 #pragma unroll
-        for (int i = 0; i < R::W; ++i) {
-          if constexpr (sizeof(T) == 4) k.v[i] = x[g4 * R::W + i];
-          else k.v[i] = __builtin_bit_cast(uint16_t, (__bf16)x[g4 * R::W + i]);
-        }
-        if (c < a.experts) *(Pack*)(to + c) = k;
-      } else {
-#pragma unroll
-        for (int i = 0; i < R::W; ++i)
-          if (c + i < a.experts) {
-            if constexpr (sizeof(T) == 4) to[c + i] = x[g4 * R::W + i];
-            else to[c + i] = __builtin_bit_cast(uint16_t, (__bf16)x[g4 * R::W + i]);
-          }
-      }
+      for (int i = 0; i < R::W; ++i) out[i] = x[v + i];
+      Group<T, R::W>::store(to, R::column(v) + R::W * l, a.experts, out);
     }
   }
 }
@@ -699,7 +715,6 @@ struct RouteRows {
   static kq_status go(const RouteLaunch& r) {
     constexpr int WAVES = LPR * VPL <= 2048 ? 8 : 4;
     RouteArgs a = r.a;
-    a.wide = a.experts % Row<LPR, VPL>::W == 0;
     const size_t lds = sizeof(int) * ((size_t)(WAVES + 2) * a.experts + 1);
     const auto kernel = route_rows_kernel<T, LPR, VPL, WAVES>;
     if (lds > 64 * 1024)
@@ -718,7 +733,6 @@ template <typename T, int LPR, int VPL>
 struct RouteBack {
   static kq_status go(const BackLaunch& r) {
     BackArgs a = r.a;
-    a.wide = a.experts % Row<LPR, VPL>::W == 0;
     const int64_t units = ceil_div(a.rows, 64 / LPR), waves = std::min<int64_t>(units, (int64_t)device_cu_count() * 32);
     a.per = ceil_div(units, waves) * (64 / LPR);
     const unsigned grid = (unsigned)ceil_div(ceil_div(a.rows, a.per), BACK_WAVES);
