@@ -575,6 +575,12 @@ __global__ __launch_bounds__(PLACERS) void route_place_kernel(RouteArgs a, int64
   if (a.loss) write_loss<PLACERS>(a, lds, SCANNED ? a.counts[n + 1] : used, shared, [&](int e) { return a.mean[e]; });
 }
 
+// What the wave's lanes have written to LDS before is what they read after.
+__device__ __forceinline__ void wave_step() {
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+}
+
 struct BackArgs {
   const void* logits;
   int64_t rows, ld, ldd;
@@ -593,7 +599,13 @@ template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArgs a) {
   using R = Row<LPR, VPL>;
   constexpr int ROWS = 64 / LPR;
+  struct alignas(4 * R::W) Part { float v[R::W]; };
+  __shared__ __attribute__((aligned(16))) float parts[BACK_WAVES][ROWS][LPR * VPL];
   const int lane = threadIdx.x & 63, l = lane % LPR;
+  float* mine = parts[threadIdx.x >> 6][lane / LPR];
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) mine[v * LPR + l] = 0.f;
+  wave_step();
   const int64_t chunk = (int64_t)blockIdx.x * BACK_WAVES + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int64_t r0 = chunk * a.per, r1 = min(r0 + a.per, a.rows);
   float b[VPL];
@@ -644,11 +656,20 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArg
     const float extra = a.normalize ? w * (g - wg) : w * g;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) x[v] *= b[v] - back;
-    for (int j = 0; j < a.top; ++j) {
-      const int own = __shfl(chosen, lane / LPR * LPR + j) - R::W * l;
-      const float add = __shfl(extra, lane / LPR * LPR + j);
+    if (a.dweight) {
+      // the chosen columns' part goes to the lanes that hold them through LDS, which is zero else
+      const bool adds = l < a.top && chosen >= 0 && chosen < a.experts;
+      if (adds) mine[chosen] = extra;
+      wave_step();
 #pragma unroll
-      for (int v = 0; v < VPL; ++v) x[v] += own == R::column(v) ? add : 0.f;
+      for (int v = 0; v < VPL; v += R::W) {
+        const Part p = *(const Part*)(mine + R::column(v) + R::W * l);
+#pragma unroll
+        for (int i = 0; i < R::W; ++i) x[v + i] += p.v[i];
+      }
+      wave_step();
+      if (adds) mine[chosen] = 0.f;
+      wave_step();
     }
     if (!in) continue;
     T* to = (T*)a.dlogits + row * a.ldd;
