@@ -136,9 +136,9 @@ __device__ __forceinline__ int row_top(int v) {
 // bf16 values keep all their bits; of fp32 values as many go as columns need, and two neighbours
 // in the order that agree in the rest have to be compared in full (ambiguous).
 constexpr int KEY_FINITE = (int)0x80800000;   // the lowest number's; only -inf (and NaN) lies below
-__device__ __forceinline__ int key_of(float v, int low, int mask) {
+__device__ __forceinline__ int key_of(float v, int column, int low, int mask) {
   const int u = __float_as_int(v);
-  return ((u ^ ((u >> 31) & 0x7fffffff)) & ~mask) | low;
+  return (((u ^ ((u >> 31) & 0x7fffffff)) & ~mask) | low) ^ column;
 }
 
 // Sorts N keys, a power of two of them, in descending order: merges of odd and even places, of runs
@@ -223,15 +223,18 @@ __device__ __forceinline__ int route_chunk(const RouteArgs& a, int64_t r0, int64
     if constexpr (VPL <= 16) {
       if (clear) {
         constexpr int MASK = LPR * VPL - 1;
+        const int low = MASK - R::W * l;   // (column(v) has its bits among those of no lane)
         int k[VPL];
 #pragma unroll
-        for (int v = 0; v < VPL; ++v) k[v] = key_of(x[v], (MASK - R::column(v)) - R::W * l, MASK);
-        sort_keys(k);
+        for (int v = 0; v < VPL; ++v) k[v] = key_of(x[v], R::column(v), low, MASK);
         int key = INT32_MIN;
-        if (count <= 9)
+        if (count <= 9) {   // (sorted here, since what lies past the ninth is left out of it)
+          sort_keys(k);
           take_keys<LPR, 9>(k, count, key);
-        else
+        } else {
+          sort_keys(k);
           take_keys<LPR, 16>(k, count, key);
+        }
         const int before = moved<0x111>(key);   // (of the lane before)
         const bool there = key >= KEY_FINITE;
         if (!WHOLE) clear = !__any(l > 0 && l < count && there && ((key ^ before) & ~MASK) == 0);
