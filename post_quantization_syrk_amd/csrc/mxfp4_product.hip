@@ -490,10 +490,11 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
 #pragma unroll
       for (int k = 0; k < NT; ++k)
         bias[k] = a.bias ? __int_as_float(read_lds((const int*)(bias_lds[turn & 1] + (wc * 32 + l32) * NT + k))) : 0.f;
-      // The lane's sixteen rows of each m are finished R at a time: all of them in the smallest tiles, where
-      // every jump to code that no one has run yet shows (77 x 1000 to 4099 with
-      // everything, four at a time: 7.2 us, sixteen 6.8), four in the largest, for want of registers.
-      constexpr int R = MT * NT == 1 ? 16 : 4, PARTS = 16 / R;
+      // The lane's sixteen rows of each m are finished R at a time: as many as registers allow, since every
+      // jump to code that no one has run yet shows where a workgroup has a tile or two (77 x 1000 to 4099
+      // with everything, four at a time: 7.2 us, sixteen 6.8; 512 x 4096 to 8192 with bias in 128 x 128
+      // tiles, four: 17.1, eight 16.6).
+      constexpr int R = MT * NT == 1 ? 16 : MT == 2 ? 8 : 4, PARTS = 16 / R;
       auto finish = [&](const f32x16 (&sums)[NT], int part, float (&v)[R * W]) {
         float s[R * W];   // the gate's, or all
 #pragma unroll
