@@ -86,6 +86,10 @@ struct CombineArgs {
   int64_t chunks;   // lanes that share a row
 };
 
+// y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]]: a lane's eight columns of a row, one choice after
+// another, sums in registers.  Bound by HBM: 32768 x 2048, top 6, bf16, 224 us, 4.9 TB/s (a large copy:
+// 4.9); rows that begin inside a dword, 4099 x 4100, top 2, to fp32: 32 us with its inputs in the last
+// cache, 40 without.
 template <typename Z, typename Y, typename R>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t units = a.rows * a.chunks;
@@ -122,8 +126,10 @@ struct BackArgs {
   float* dweight;
 };
 
-// A row per workgroup of WAVES, KB choices at a time: their reads go out together, each choice's
-// slot being the same for all lanes.
+// dz[slot] = weight dy, dweight = <dy, z[slot]>: a row per workgroup of WAVES, KB choices at a time, whose
+// reads go out together, each choice's slot being the same for all lanes; dy is read once for all of
+// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 329 us, 5.3 TB/s.  One wave a row up to 2048 columns
+// (no barrier), four above.
 template <typename D, typename Z, int WAVES, int KB>
 __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
   __shared__ float sums[WAVES][KB];

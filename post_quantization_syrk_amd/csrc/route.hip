@@ -326,6 +326,12 @@ __device__ __forceinline__ void write_loss(const RouteArgs& a, const int* first,
   *a.loss = (float)(s * a.experts / ((double)max(first[a.experts], 1) * max(used, 1)));
 }
 
+// Softmax and choices of a chunk's rows: p_e = exp(l_e - m) / sum exp(l - m), each choice's rank.
+// Sixteen lanes a row, so that its reductions are lane rotations, which cost no more than the operation
+// (64 lanes past 256 experts).  Bound by the vector instructions: 131072 x 256 fp32, top 8, with the
+// loss, 51 us, VALU busy in four cycles of five, where the logits take 26 at 5.2 TB/s (choosing by eight
+// searches for the largest value: 79 us; with the next rows read ahead, which spills, 70); one row of
+// eight experts, all of routing in this launch, 4.0 us.
 template <typename T, int LPR, int VPL, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void route_rows_kernel(RouteArgs a) {
   using R = Row<LPR, VPL>;
@@ -414,7 +420,10 @@ __global__ __launch_bounds__(64 * WAVES) void route_rows_kernel(RouteArgs a) {
 }
 
 // Eight experts (and, past the last, the count of rows) per workgroup, 128 threads each: the chunks'
-// counts become those of the chunks before, the totals go to counts, the probabilities' sums to mean.
+// counts become those of the chunks before, the totals go to counts, the probabilities' sums (in 64
+// bits from here on) to mean.  Every thread's reads are out before it adds, so that one trip to memory
+// and one back are all there is: 1024 chunks of 256 experts 8.6 us, 17 workgroups that read one chunk
+// after another 28.
 __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
   constexpr int SEGS = 128, PER = MAX_CHUNKS / SEGS;
   __shared__ int seg[8][SEGS + 1];
@@ -469,6 +478,8 @@ __global__ __launch_bounds__(1024) void route_scan_kernel(RouteArgs a) {
     }
 }
 
+// Slots: an expert's first one, the choices of the chunks before, the rank in the chunk.  Latency, and
+// scattered writes of the index: 131072 rows of 8 choices 9.6 us, 4099 of 6 5.1 with the counts' sums.
 // SCANNED: the second kernel has been; else every workgroup adds up the chunks' counts itself.
 template <bool SCANNED>
 __global__ __launch_bounds__(PLACERS) void route_place_kernel(RouteArgs a, int64_t chunk_rows) {
@@ -598,6 +609,9 @@ struct BackArgs {
   int64_t per;
 };
 
+// The logits' gradient, dl_e = p_e (b_e - back) + [e chosen] extra, by the lanes that hold the row.
+// Bound by HBM: 131072 x 256 fp32, top 8, 52 us, 5.2 TB/s (each lane comparing its columns with every
+// choice: 61 us, and 48 for the bf16 that takes 38 so).
 template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArgs a) {
   using R = Row<LPR, VPL>;
