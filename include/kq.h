@@ -485,7 +485,7 @@ kq_status kq_mxfp4_quantize(const void* src, int src_type, int64_t rows, int64_t
                             uint8_t* scales, uint16_t* values_opt, int64_t ldv, void* stream);
 
 /*
- * kq_mxfp4_workspace -- workspace bytes of kq_mxfp4_linear and kq_mxfp4_experts for `rows` rows
+ * kq_mxfp4_workspace -- workspace bytes of kq_mxfp4_linear, kq_mxfp4_experts and their _epilogue forms for `rows` rows
  * of n activations: room for the quantised rows, rows * ceil(n / 128) * 68 (any rows not
  * quantised yet; quantised ones need none).
  */
@@ -593,7 +593,8 @@ kq_status kq_mxfp4_experts_epilogue(const void* x, int x_type, int64_t rows, int
                                     size_t ws_bytes, void* stream);
 
 /*
- * kq_route_workspace -- workspace bytes of kq_route (none for few rows).
+ * kq_route_workspace -- workspace bytes of kq_route (none for few rows); those for some rows serve any
+ * fewer, of as many experts.
  */
 kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
 

@@ -254,6 +254,7 @@ extern "C" kq_status kq_combine(const void* z, int z_type, int64_t slots, int64_
     if (!typed(residual_type)) return fail(KQ_EINVAL, "%s: residual of type %d", fn, residual_type);
     if (ldr < n) return fail(KQ_ESHAPE, "%s: ldr %lld < %lld", fn, (long long)ldr, (long long)n);
     if (off_type(residual, residual_type)) return fail(KQ_EINVAL, "%s: residual not aligned to its type", fn);
+    if (residual == y && rows > 0 && (residual_type != y_type || ldr != ldy)) return fail(KQ_EINVAL, "%s: in place, the residual has y's type and leading dim", fn);
   }
   if (rows == 0) return KQ_OK;
   const CombineArgs a{z, slots, n, ldz, slot, weight, rows, top, residual, ldr, y, ldy, ceil_div(n, VEC)};
@@ -278,6 +279,7 @@ extern "C" kq_status kq_combine_backward(const void* dy, int dy_type, int64_t ro
   if (dz_opt && lddz < n) return fail(KQ_ESHAPE, "%s: lddz %lld < %lld", fn, (long long)lddz, (long long)n);
   if (off_type(dy, dy_type) || off_type(z, z_type) || off_type(dz_opt, z_type) || ((uintptr_t)dweight_opt & 3))
     return fail(KQ_EINVAL, "%s: an argument is not aligned to its type", fn);
+  if (dz_opt && dz_opt == z && lddz != ldz) return fail(KQ_EINVAL, "%s: in place, lddz is ldz", fn);
   if (rows == 0 || (!dz_opt && !dweight_opt)) return KQ_OK;
   const BackArgs a{dy, rows, n, lddy, z, slots, ldz, slot, weight, top, dz_opt, lddz, dweight_opt};
   hipStream_t s = as_stream(stream);

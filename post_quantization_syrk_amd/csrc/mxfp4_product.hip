@@ -813,6 +813,8 @@ kq_status product(const char* fn, const MxRows& x, ProductArgs p, const kq_epilo
       if (ep->residual_type != KQ_F32 && ep->residual_type != KQ_BF16) return fail(KQ_EINVAL, "%s: residual of type %d", fn, ep->residual_type);
       if (ep->ldr < out) return fail(KQ_ESHAPE, "%s: ldr %lld < %lld", fn, (long long)ep->ldr, (long long)out);
       if ((uintptr_t)ep->residual & (ep->residual_type == KQ_F32 ? 3 : 1)) return fail(KQ_EINVAL, "%s: residual not aligned to its type", fn);
+      if (ep->residual == p.y && (ep->residual_type != y_type || ep->ldr != p.ldy))
+        return fail(KQ_EINVAL, "%s: in place, the residual has y's type and leading dim", fn);
       p.y_far |= ep->ldr > (1 << 20);
     }
     p.epi = ep->gated ? EPI_GATED : ep->act != KQ_ACT_NONE || ep->bias || ep->residual ? EPI_PLAIN : EPI_NONE;

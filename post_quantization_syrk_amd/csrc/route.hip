@@ -715,6 +715,12 @@ void deal(int64_t rows, int experts, int* chunks, int64_t* per) {
   *chunks = (int)std::max<int64_t>(ceil_div(rows, *per * waves), 1);
 }
 
+// The most chunks that deal() makes of up to so many rows (its own number does not always grow with them).
+int64_t most_chunks(int64_t rows, int experts) {
+  const int64_t waves = waves_of(experts);
+  return std::min(std::min<int64_t>(MAX_CHUNKS, ceil_div(rows, 4 * waves)), std::max<int64_t>(256, ceil_div(rows, 16 * waves)));
+}
+
 size_t round16(size_t n) { return (n + 15) / 16 * 16; }
 
 kq_status check_route(const char* fn, const void* logits, int type, int64_t rows, int experts, int64_t ld, int top, int normalize) {
@@ -791,7 +797,8 @@ extern "C" kq_status kq_route_workspace(int64_t rows, int experts, int top, size
   int chunks;
   int64_t per;
   deal(rows, experts, &chunks, &per);
-  *bytes = chunks == 1 ? 0 : round16(sizeof(int32_t) * (size_t)chunks * (experts + 1)) + round16(sizeof(float) * (size_t)chunks * experts) + sizeof(double) * experts;
+  const size_t most = (size_t)most_chunks(rows, experts);
+  *bytes = chunks == 1 ? 0 : round16(sizeof(int32_t) * most * (experts + 1)) + round16(sizeof(float) * most * experts) + sizeof(double) * experts;
   return KQ_OK;
 }
 
@@ -846,6 +853,7 @@ extern "C" kq_status kq_route_backward(const void* logits, int type, int64_t row
   if (((uintptr_t)weight | (uintptr_t)expert | (uintptr_t)counts | (uintptr_t)dweight_opt | (uintptr_t)dloss_opt) & 3 ||
       (uintptr_t)dlogits & (type == KQ_F32 ? 3 : 1))
     return fail(KQ_EINVAL, "%s: an argument is not aligned to its type", fn);
+  if (dlogits == logits && ldd != ld) return fail(KQ_EINVAL, "%s: in place, ldd is ld", fn);
   if (rows == 0) return KQ_OK;
   BackArgs a{};
   a.logits = logits; a.rows = rows; a.ld = ld; a.ldd = ldd; a.experts = experts; a.top = top; a.normalize = normalize;

@@ -735,6 +735,52 @@ def test_routing_on_two_streams_at_once():
             assert torch.equal(v, getattr(b, name)), name
 
 
+@pytest.mark.parametrize("rows", [1, 40, 500])
+def test_epilogues_and_sums_on_given_streams(rows):
+    """Calls on two streams with the workspaces that the binding allocates: the bits of a call by itself."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(rows)
+    n, out = 1024, 200
+    wc, ws, _ = _layer(rng, 2 * out, n)
+    slot = _dev(_choices(rng, rows, 3, 3 * rows, False))
+    inputs = [_rows(rng, rows, n, "bf16").cuda() for _ in range(6)]
+    z = [torch.randn(3 * rows, out, device="cuda") for _ in inputs]
+
+    def call(x, z, stream=None):
+        y, s = _empty((rows, out), "bf16"), _empty((rows, out), "f32")
+        dz, dw = torch.empty_like(z), torch.empty(rows, 3, device="cuda")
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        kq.kq_mxfp4_linear_epilogue(x, wc, ws, y, act="gelu", gated=True, had=n, stream=stream)
+        kq.kq_combine(z, slot, s, residual=y, stream=stream)
+        kq.kq_combine_backward(s, z, slot, dz, dweight=dw, stream=stream)
+        return y, s, dz, dw
+
+    want = [call(x, v) for x, v in zip(inputs, z)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [call(x, v, streams[k % 2]) for k, (x, v) in enumerate(zip(inputs, z))]
+    torch.cuda.synchronize()
+    for a, b in zip(want, got):
+        assert all(torch.equal(u, v) for u, v in zip(a, b))
+
+
+def test_routing_with_a_larger_workspace():
+    """One workspace for the largest batch serves all smaller ones."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(6)
+    ws = torch.full((kq.kq_route_workspace(131_200, 16, 2),), 255, dtype=torch.uint8, device="cuda")
+    for rows in (131_200, 131_072, 33_000, 4000, 70, 3):
+        x = _logits(rng, rows, 16, "f32", False).cuda()
+        r, own = Routes(rows, 16, 2), Routes(rows, 16, 2)
+        kq.kq_route(x, ws=ws, **r.dict())
+        kq.kq_route(x, **own.dict())
+        for name, v in r.dict().items():
+            assert torch.equal(v, getattr(own, name)), name
+
+
 def test_the_binding_refuses():
     torch = torch_cuda()
     kq = _kq()

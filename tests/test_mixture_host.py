@@ -108,7 +108,7 @@ def _route_back(**kw):
 
 @pytest.mark.parametrize("kw,status", ROUTE + [
     (dict(g=None), kq.KQ_EINVAL), (dict(g=TWO), kq.KQ_EINVAL), (dict(dw=TWO), kq.KQ_EINVAL),
-    (dict(dl=TWO), kq.KQ_EINVAL), (dict(ldd=3), kq.KQ_ESHAPE)])
+    (dict(dl=TWO), kq.KQ_EINVAL), (dict(ldd=3), kq.KQ_ESHAPE), (dict(ldd=5), kq.KQ_EINVAL)])
 def test_route_backward_refuses(kw, status):
     assert _route_back(**kw) == status
 
@@ -117,6 +117,9 @@ def test_route_workspace():
     assert kq.kq_route_workspace(0, 1, 1) == 0
     sizes = [kq.kq_route_workspace(r, 64, 2) for r in (1, 100, 10_000, 1 << 20, 1 << 29)]
     assert sizes == sorted(sizes) and 0 < sizes[2] and sizes[-1] < 1 << 25
+    for experts in (1, 64, 256, 3000):      # what serves some rows serves fewer
+        sizes = [kq.kq_route_workspace(r, experts, 1) for r in sorted({*range(1, 2000, 7), *range(2000, 300_000, 997), 131_072, 131_200})]
+        assert sizes == sorted(sizes)
     for bad in ((-1, 4, 1), (4, 0, 1), (4, 4, 5), (1 << 30, 4, 2)):
         with pytest.raises(kq.KQError) as e:
             kq.kq_route_workspace(*bad)
@@ -138,7 +141,8 @@ COMBINE = [(dict(z=None), kq.KQ_EINVAL), (dict(z=ODD), kq.KQ_EINVAL), (dict(zt=2
 
 @pytest.mark.parametrize("kw,status", COMBINE + [
     (dict(y=None), kq.KQ_EINVAL), (dict(y=TWO), kq.KQ_EINVAL), (dict(yt=3), kq.KQ_EINVAL), (dict(ldy=15), kq.KQ_ESHAPE),
-    (dict(r=P, rt=2, ldr=16), kq.KQ_EINVAL), (dict(r=P, ldr=15), kq.KQ_ESHAPE), (dict(r=TWO, ldr=16), kq.KQ_EINVAL)])
+    (dict(r=P, rt=2, ldr=16), kq.KQ_EINVAL), (dict(r=P, ldr=15), kq.KQ_ESHAPE), (dict(r=TWO, ldr=16), kq.KQ_EINVAL),
+    (dict(r=P, rt=1, ldr=16), kq.KQ_EINVAL), (dict(r=P, ldr=17), kq.KQ_EINVAL)])
 def test_combine_refuses(kw, status):
     assert _combine(**kw) == status
 
@@ -151,7 +155,7 @@ def _combine_back(**kw):
 
 @pytest.mark.parametrize("kw,status", COMBINE + [
     (dict(dy=None), kq.KQ_EINVAL), (dict(dy=TWO), kq.KQ_EINVAL), (dict(dyt=2), kq.KQ_EINVAL), (dict(lddy=15), kq.KQ_ESHAPE),
-    (dict(dz=ODD), kq.KQ_EINVAL), (dict(lddz=15), kq.KQ_ESHAPE), (dict(dw=TWO), kq.KQ_EINVAL)])
+    (dict(dz=ODD), kq.KQ_EINVAL), (dict(lddz=15), kq.KQ_ESHAPE), (dict(dw=TWO), kq.KQ_EINVAL), (dict(lddz=17), kq.KQ_EINVAL)])
 def test_combine_backward_refuses(kw, status):
     assert _combine_back(**kw) == status
 
@@ -183,6 +187,7 @@ def _product(experts=None, ep=None, **kw):
     (dict(ep=dict(gated=2)), kq.KQ_EINVAL), (dict(ep=dict(bias=TWO)), kq.KQ_EINVAL),
     (dict(ep=dict(residual=P, residual_type=2, ldr=16)), kq.KQ_EINVAL), (dict(ep=dict(residual=P, ldr=15)), kq.KQ_ESHAPE),
     (dict(ep=dict(residual=TWO, ldr=16)), kq.KQ_EINVAL), (dict(ep=dict(residual=ODD, residual_type=1, ldr=16)), kq.KQ_EINVAL),
+    (dict(ep=dict(residual=P, residual_type=1, ldr=16)), kq.KQ_EINVAL), (dict(ep=dict(residual=P, ldr=17)), kq.KQ_EINVAL),
     (dict(ep=dict(gated=1), out=(1 << 23) + 1, ldy=1 << 24), kq.KQ_ESHAPE),
     (dict(ep=dict(gated=1), out=1 << 20, ldy=1 << 20, n=1 << 16, ldx=1 << 16, bytes=1 << 40), kq.KQ_ESHAPE),
     (dict(x=None), kq.KQ_EINVAL), (dict(wc=None), kq.KQ_EINVAL), (dict(y=None), kq.KQ_EINVAL), (dict(ldy=15), kq.KQ_ESHAPE),
