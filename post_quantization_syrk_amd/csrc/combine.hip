@@ -12,14 +12,12 @@ constexpr int VEC = 8;   // neighbouring columns of a lane
 constexpr int MAX_TOP = 64;
 
 // Eight neighbouring values, read and written 16 bytes at a time at any alignment of their type (as
-// single values the compiler takes them apart: 32768 x 2048 x 6 backwards 525 us, as words 338).
-template <typename T>
-struct __attribute__((packed, aligned(sizeof(T)))) Words {
-  u32x4 v[VEC * sizeof(T) / 16];
-};
+// single values the compiler takes them apart: 32768 x 2048 x 6 backwards 525 us, so 338).
+typedef u32x4 u32x4_any __attribute__((aligned(2)));
 template <typename T>
 struct Pack {
-  u32x4 v[VEC * sizeof(T) / 16];
+  static constexpr int WORDS = VEC * (int)sizeof(T) / 16;
+  u32x4 v[WORDS];
   __device__ __forceinline__ float operator[](int i) const {
     if constexpr (sizeof(T) == 4)
       return __uint_as_float(v[i / 4][i % 4]);
@@ -34,14 +32,15 @@ __device__ __forceinline__ unsigned pair(float lo, float hi) { return __builtin_
 __device__ __forceinline__ void put(float v, float& to) { to = v; }
 __device__ __forceinline__ void put(float v, uint16_t& to) { to = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Columns c .. c + 7 of a row of n (zeros past its end).
-template <typename T>
+// Columns c .. c + 7 of a row of n (zeros past its end).  STREAM: past the caches, which hold nothing
+// of calls this large for whoever comes next.
+template <bool STREAM, typename T>
 __device__ __forceinline__ Pack<T> load(const T* row, int64_t c, int64_t n) {
   Pack<T> k{};
   if (c + VEC <= n) {
-    const Words<T> w = *(const Words<T>*)(row + c);
+    const u32x4_any* from = (const u32x4_any*)(row + c);
 #pragma unroll
-    for (int i = 0; i < (int)(VEC * sizeof(T) / 16); ++i) k.v[i] = w.v[i];
+    for (int i = 0; i < Pack<T>::WORDS; ++i) k.v[i] = STREAM ? __builtin_nontemporal_load(from + i) : from[i];
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -54,17 +53,24 @@ __device__ __forceinline__ Pack<T> load(const T* row, int64_t c, int64_t n) {
   }
   return k;
 }
-template <typename T>
+template <bool STREAM, typename T>
 __device__ __forceinline__ void store(T* row, int64_t c, int64_t n, const float (&v)[VEC]) {
   if (c + VEC <= n) {
-    Words<T> w;
+    Pack<T> w;
     if constexpr (sizeof(T) == 4) {
       w.v[0] = u32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])};
       w.v[1] = u32x4{__float_as_uint(v[4]), __float_as_uint(v[5]), __float_as_uint(v[6]), __float_as_uint(v[7])};
     } else {
       w.v[0] = u32x4{pair(v[0], v[1]), pair(v[2], v[3]), pair(v[4], v[5]), pair(v[6], v[7])};
     }
-    *(Words<T>*)(row + c) = w;
+    u32x4_any* to = (u32x4_any*)(row + c);
+#pragma unroll
+    for (int i = 0; i < Pack<T>::WORDS; ++i) {
+      if constexpr (STREAM)
+        __builtin_nontemporal_store(w.v[i], to + i);
+      else
+        to[i] = w.v[i];
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < VEC; ++i)
@@ -87,17 +93,17 @@ struct CombineArgs {
 };
 
 // y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]]: a lane's eight columns of a row, one choice after
-// another, sums in registers.  Bound by HBM: 32768 x 2048, top 6, bf16, 224 us, 4.9 TB/s (a large copy:
+// another, sums in registers.  Bound by HBM: 32768 x 2048, top 6, bf16, 185 us, 5.8 TB/s (a large copy:
 // 4.9); rows that begin inside a dword, 4099 x 4100, top 2, to fp32: 32 us with its inputs in the last
 // cache, 40 without.
-template <typename Z, typename Y, typename R>
+template <typename Z, typename Y, typename R, bool STREAM>
 __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
   const int64_t units = a.rows * a.chunks;
   for (int64_t u = (int64_t)blockIdx.x * 256 + threadIdx.x; u < units; u += (int64_t)gridDim.x * 256) {
     const int64_t t = u / a.chunks, c = (u - t * a.chunks) * VEC;
     float acc[VEC] = {};
     if (a.residual) {
-      const Pack<R> r = load((const R*)a.residual + t * a.ldr, c, a.n);
+      const Pack<R> r = load<STREAM>((const R*)a.residual + t * a.ldr, c, a.n);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] = r[i];
     }
@@ -105,11 +111,11 @@ __global__ __launch_bounds__(256) void combine_kernel(CombineArgs a) {
       const int s = a.slot[t * a.top + j];
       const float w = a.weight ? a.weight[t * a.top + j] : 1.f;
       Pack<Z> k{};
-      if (s >= 0 && s < a.slots) k = load((const Z*)a.z + s * a.ldz, c, a.n);
+      if (s >= 0 && s < a.slots) k = load<STREAM>((const Z*)a.z + s * a.ldz, c, a.n);
 #pragma unroll
       for (int i = 0; i < VEC; ++i) acc[i] += w * k[i];
     }
-    store((Y*)a.y + t * a.ldy, c, a.n, acc);
+    store<STREAM>((Y*)a.y + t * a.ldy, c, a.n, acc);
   }
 }
 
@@ -128,9 +134,9 @@ struct BackArgs {
 
 // dz[slot] = weight dy, dweight = <dy, z[slot]>: a row per workgroup of WAVES, KB choices at a time, whose
 // reads go out together, each choice's slot being the same for all lanes; dy is read once for all of
-// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 329 us, 5.3 TB/s.  One wave a row up to 2048 columns
+// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 341 us, 5.1 TB/s.  One wave a row up to 2048 columns
 // (no barrier), four above.
-template <typename D, typename Z, int WAVES, int KB>
+template <typename D, typename Z, int WAVES, int KB, bool STREAM>
 __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
   __shared__ float sums[WAVES][KB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
@@ -148,12 +154,12 @@ __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a
       dot[j] = 0.f;
     }
     for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
-      const Pack<D> d = load(dy, c, a.n);
+      const Pack<D> d = load<STREAM>(dy, c, a.n);
       Pack<Z> z[KB];
       if (a.dweight) {
 #pragma unroll
         for (int j = 0; j < KB; ++j)
-          if (s[j] >= 0) z[j] = load((const Z*)a.z + s[j] * a.ldz, c, a.n);
+          if (s[j] >= 0) z[j] = load<STREAM>((const Z*)a.z + s[j] * a.ldz, c, a.n);
 #pragma unroll
         for (int j = 0; j < KB; ++j)
           if (s[j] >= 0) {
@@ -168,7 +174,7 @@ __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a
             float v[VEC];
 #pragma unroll
             for (int i = 0; i < VEC; ++i) v[i] = w[j] * d[i];
-            store((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
+            store<STREAM>((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
           }
       }
     }
@@ -213,21 +219,26 @@ kq_status check_choices(const char* fn, int z_type, int64_t slots, int64_t n, in
   return KQ_OK;
 }
 
+// Whether the rows of z are more than the last cache (256 MB) holds: then nothing is kept in it
+// (32768 x 2048, top 6, bf16 with both gradients, 805 MB of z: 517 to 524 us, through the caches 553; 4099 x
+// 4100, top 2, 67 MB: 40 to 42 us either way, and what is written may be read next).
+bool streams(int64_t rows, int64_t top, int64_t n, size_t size) { return rows * top * n * (int64_t)size > ((int64_t)256 << 20); }
+
 template <typename Z, typename Y, typename R>
 kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
   const int64_t blocks = std::min<int64_t>(ceil_div(a.rows * a.chunks, 256), 1 << 30);
-  combine_kernel<Z, Y, R><<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
+  const auto kernel = streams(a.rows, a.top, a.n, sizeof(Z)) ? combine_kernel<Z, Y, R, true> : combine_kernel<Z, Y, R, false>;
+  kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
   KQ_LAUNCHED("combine_kernel");
   return KQ_OK;
 }
 
 template <typename D, typename Z, int KB>
 kq_status launch_backward(const BackArgs& a, hipStream_t s) {
-  const dim3 grid((unsigned)a.rows);
-  if (a.n <= 64 * VEC * 4)
-    combine_backward_kernel<D, Z, 1, KB><<<grid, dim3(64), 0, s>>>(a);
-  else
-    combine_backward_kernel<D, Z, 4, KB><<<grid, dim3(256), 0, s>>>(a);
+  const bool stream = streams(a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 4;
+  const auto kernel = wide ? (stream ? combine_backward_kernel<D, Z, 4, KB, true> : combine_backward_kernel<D, Z, 4, KB, false>)
+                           : (stream ? combine_backward_kernel<D, Z, 1, KB, true> : combine_backward_kernel<D, Z, 1, KB, false>);
+  kernel<<<dim3((unsigned)a.rows), dim3(wide ? 256 : 64), 0, s>>>(a);
   KQ_LAUNCHED("combine_backward_kernel");
   return KQ_OK;
 }
