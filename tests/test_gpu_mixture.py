@@ -18,7 +18,8 @@ import pytest
 import oracle.mixture as ox
 import oracle.mxfp4 as om
 from tests.gpu_util import announce, torch_cuda
-from tests.test_gpu_mxfp4 import PATHS, _dev, _empty, _experts_ref, _forced, _layer, _processing, _rows, _sorted_slots
+from tests.test_gpu_mxfp4 import (PATHS, _dev, _empty, _experts_ref, _forced, _layer, _processing, _random_codes, _rows, _sorted_slots,
+                                  _values)
 
 pytestmark = pytest.mark.gpu
 
@@ -464,6 +465,69 @@ def test_epilogue_keeps_what_is_not_finite_in_its_place(rows):
     assert torch.equal(y[:, 9], torch.full_like(other[:, 9], 1e30) * other[:, 9])
 
 
+def test_epilogue_of_rows_past_32_bits():
+    """Quantised rows of more than 4 GiB, read through an index: the bits of the same rows side by side."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(11)
+    rows, n, out, slots = 1_060_000, 8192, 70, 300
+    codes, scales = _random_codes(rows, n)
+    index = rng.integers(0, rows, slots).astype(np.int32)
+    index[[0, 1, slots - 1]] = [rows - 1, 0, rows - 2]
+    offsets = np.int32([0, 3, slots])
+    picked = torch.from_numpy(index).long().cuda()
+    xq = _values(codes, scales, index)
+    for act, gated, biased, rk in (("silu", True, True, "f32"), ("gelu", False, True, "bf16")):
+        wide = out * (1 + gated)
+        wc, ws, wv = _layer(rng, wide, n, 2)
+        bias, res = rng.standard_normal((2, wide)).astype(np.float32), _residual(rng, slots, out, rk)
+        rest = dict(bias=_dev(bias), act=act, gated=gated, residual=res.cuda(), n=n)
+        y, near = _empty((slots, out), "f32"), _empty((slots, out), "f32")
+        kq.kq_mxfp4_experts_epilogue(codes, _dev(index), _dev(offsets), wc, ws, y, x_scales=scales, **rest)
+        with _forced(dict(KQ_TESTING_MX_FEW=0, KQ_TESTING_MX_TILE=256)):
+            kq.kq_mxfp4_experts_epilogue(codes[picked], None, _dev(offsets), wc, ws, near, x_scales=scales[:, picked].contiguous(), **rest)
+        assert torch.equal(y, near)
+        s, mag = _experts_ref(xq, None, offsets, wv, slots, slots)
+        per = bias[np.searchsorted(offsets, np.arange(slots), side="right") - 1]
+        want, bound = _finish(s, (n + 2) * U * mag, per, act, gated, _host(res), "f32")
+        _within(_host(y), want, bound)
+
+
+def test_epilogue_of_an_output_past_32_bits():
+    """More than 4 GiB of output, which is its own residual."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(12)
+    rows, n, out = 1_000_003, 128, 2200
+    codes, scales = _random_codes(rows, n)
+    wc, ws, wv = _layer(rng, out, n)
+    bias = rng.standard_normal(out).astype(np.float32)
+    y = torch.empty((rows, out), dtype=torch.bfloat16, device="cuda")
+    y.copy_((torch.arange(rows, device="cuda") % 251)[:, None].expand(rows, out))
+    kq.kq_mxfp4_linear_epilogue(codes, wc, ws, y, x_scales=scales, n=n, bias=_dev(bias), act="gelu_tanh", residual=y)
+    some = np.concatenate([[0, 1, rows - 1, rows - 2, rows - 3], rng.integers(0, rows, 200)])
+    xq = _values(codes, scales, some)
+    want, bound = _finish(xq @ wv.T, (n + 2) * U * (np.abs(xq) @ np.abs(wv.T)), bias, "gelu_tanh", False, (some % 251)[:, None], "bf16")
+    _within(_host(y[torch.from_numpy(some).cuda()]), want, bound)
+
+
+@pytest.mark.parametrize("slots", [40, 600])
+def test_epilogue_of_layers_past_32_bits(slots):
+    """Gated layers that lie more than 4 GiB behind the first, from the sums of the call without an epilogue."""
+    torch = torch_cuda()
+    kq = _kq()
+    n, out, experts = 8192, 2048, 260
+    wc, ws = _random_codes(2 * out, n, experts)
+    x, xs = _random_codes(slots, n)
+    offsets = np.zeros(experts + 1, np.int32)
+    offsets[2:] = slots // 2
+    offsets[-1] = slots
+    sums, y = _empty((slots, 2 * out), "f32"), _empty((slots, out), "f32")
+    kq.kq_mxfp4_experts(x, None, _dev(offsets), wc, ws, sums, x_scales=xs, n=n)
+    kq.kq_mxfp4_experts_epilogue(x, None, _dev(offsets), wc, ws, y, x_scales=xs, n=n, act="relu", gated=True)
+    assert torch.equal(y, torch.relu(sums[:, :out]) * sums[:, out:])
+
+
 # ---- the experts' rows together ----
 
 def _choices(rng, rows, top, slots, dropped):
@@ -582,6 +646,33 @@ def test_combine_past_32_bits():
     assert torch.equal(z[slot.view(-1).long()].view(3, 2, n), y.to(torch.bfloat16)[:, None].expand(3, 2, n))
     want = (rows.double() * y.double()[:, None]).sum(2)
     assert bool(((dw - want).abs() <= (n + 2) * U * (rows.double() * y.double()[:, None]).abs().sum(2)).all())
+
+
+@pytest.mark.parametrize("zk,n,top", [("bf16", 4101, 4), ("f32", 2052, 4), ("bf16", 1500, 11)])
+def test_combine_of_more_than_the_last_cache(zk, n, top):
+    """Rows that go past the caches: the bits of the same rows in calls that do not."""
+    announce(f"combine 8200 rows of {n} {zk} top {top}")
+    torch = torch_cuda()
+    kq = _kq()
+    rows, size = 8200, 2 if zk == "bf16" else 4
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    assert rows * top * n * size > 256 << 20
+    z = torch.randn(rows * top, n + 3, generator=gen, device="cuda").to(_dtype(zk))[:, :n]
+    slot = torch.randperm(rows * top, generator=gen, device="cuda").int().view(rows, top)
+    slot[5, 1], slot[8199, 0] = -1, rows * top
+    w = torch.randn(rows, top, generator=gen, device="cuda")
+    res = torch.randn(rows, n, generator=gen, device="cuda").to(torch.bfloat16)
+
+    def call(parts):
+        y, dz, dw = _empty((rows, n), "bf16"), torch.full((rows * top, n), 5.0, dtype=z.dtype, device="cuda"), torch.empty(rows, top, device="cuda")
+        for k in range(parts):
+            a = slice(k * rows // parts, (k + 1) * rows // parts)
+            kq.kq_combine(z, slot[a], y[a], weight=w[a], residual=res[a])
+            kq.kq_combine_backward(res[a], z, slot[a], dz, weight=w[a], dweight=dw[a])
+        return y, dz, dw
+
+    for a, b in zip(call(1), call(4)):
+        assert torch.equal(a, b)
 
 
 # ---- a mixture, as it is used ----
