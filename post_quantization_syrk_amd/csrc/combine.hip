@@ -140,63 +140,64 @@ template <typename D, typename Z, int WAVES, int KB, bool STREAM>
 __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
   __shared__ float sums[WAVES][KB];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int64_t t = blockIdx.x;
-  const D* dy = (const D*)a.dy + t * a.lddy;
-  for (int j0 = 0; j0 < a.top; j0 += KB) {
-    int s[KB];
-    float w[KB], dot[KB];
+  for (int64_t t = blockIdx.x; t < a.rows; t += gridDim.x) {
+    const D* dy = (const D*)a.dy + t * a.lddy;
+    for (int j0 = 0; j0 < a.top; j0 += KB) {
+      int s[KB];
+      float w[KB], dot[KB];
 #pragma unroll
-    for (int j = 0; j < KB; ++j) {
-      const int64_t at = t * a.top + min(j0 + j, a.top - 1);
-      const int k = __builtin_amdgcn_readfirstlane(a.slot[at]);
-      s[j] = j0 + j < a.top && k >= 0 && k < a.slots ? k : -1;
-      w[j] = a.weight ? a.weight[at] : 1.f;
-      dot[j] = 0.f;
-    }
-    for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
-      const Pack<D> d = load<STREAM>(dy, c, a.n);
-      Pack<Z> z[KB];
-      if (a.dweight) {
+      for (int j = 0; j < KB; ++j) {
+        const int64_t at = t * a.top + min(j0 + j, a.top - 1);
+        const int k = __builtin_amdgcn_readfirstlane(a.slot[at]);
+        s[j] = j0 + j < a.top && k >= 0 && k < a.slots ? k : -1;
+        w[j] = a.weight ? a.weight[at] : 1.f;
+        dot[j] = 0.f;
+      }
+      for (int64_t c = threadIdx.x * VEC; c < a.n; c += 64 * WAVES * VEC) {
+        const Pack<D> d = load<STREAM>(dy, c, a.n);
+        Pack<Z> z[KB];
+        if (a.dweight) {
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (s[j] >= 0) z[j] = load<STREAM>((const Z*)a.z + s[j] * a.ldz, c, a.n);
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (s[j] >= 0) {
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) dot[j] += d[i] * z[j][i];
+            }
+        }
+        if (a.dz) {
+#pragma unroll
+          for (int j = 0; j < KB; ++j)
+            if (s[j] >= 0) {
+              float v[VEC];
+#pragma unroll
+              for (int i = 0; i < VEC; ++i) v[i] = w[j] * d[i];
+              store<STREAM>((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
+            }
+        }
+      }
+      if (!a.dweight) continue;
+#pragma unroll
+      for (int j = 0; j < KB; ++j) dot[j] = reduce_lanes<64>(dot[j], [](float x, float y) { return x + y; });
+      if constexpr (WAVES > 1) {
 #pragma unroll
         for (int j = 0; j < KB; ++j)
-          if (s[j] >= 0) z[j] = load<STREAM>((const Z*)a.z + s[j] * a.ldz, c, a.n);
+          if (lane == 0) sums[wave][j] = dot[j];
+        __syncthreads();
+        if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.top) {
+          float v = 0.f;
+#pragma unroll
+          for (int k = 0; k < WAVES; ++k) v += sums[k][threadIdx.x];
+          a.dweight[t * a.top + j0 + threadIdx.x] = v;
+        }
+        __syncthreads();
+      } else {
 #pragma unroll
         for (int j = 0; j < KB; ++j)
-          if (s[j] >= 0) {
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) dot[j] += d[i] * z[j][i];
-          }
+          if (lane == j && j0 + j < a.top) a.dweight[t * a.top + j0 + j] = dot[j];
       }
-      if (a.dz) {
-#pragma unroll
-        for (int j = 0; j < KB; ++j)
-          if (s[j] >= 0) {
-            float v[VEC];
-#pragma unroll
-            for (int i = 0; i < VEC; ++i) v[i] = w[j] * d[i];
-            store<STREAM>((Z*)a.dz + s[j] * a.lddz, c, a.n, v);
-          }
-      }
-    }
-    if (!a.dweight) continue;
-#pragma unroll
-    for (int j = 0; j < KB; ++j) dot[j] = reduce_lanes<64>(dot[j], [](float x, float y) { return x + y; });
-    if constexpr (WAVES > 1) {
-#pragma unroll
-      for (int j = 0; j < KB; ++j)
-        if (lane == 0) sums[wave][j] = dot[j];
-      __syncthreads();
-      if (threadIdx.x < KB && j0 + (int)threadIdx.x < a.top) {
-        float v = 0.f;
-#pragma unroll
-        for (int k = 0; k < WAVES; ++k) v += sums[k][threadIdx.x];
-        a.dweight[t * a.top + j0 + threadIdx.x] = v;
-      }
-      __syncthreads();
-    } else {
-#pragma unroll
-      for (int j = 0; j < KB; ++j)
-        if (lane == j && j0 + j < a.top) a.dweight[t * a.top + j0 + j] = dot[j];
     }
   }
 }
@@ -224,9 +225,13 @@ kq_status check_choices(const char* fn, int z_type, int64_t slots, int64_t n, in
 // 4100, top 2, 67 MB: 40 to 42 us either way, and what is written may be read next).
 bool streams(int64_t rows, int64_t top, int64_t n, size_t size) { return rows * top * n * (int64_t)size > ((int64_t)256 << 20); }
 
+// Workgroups of a launch: a grid of 2^32 threads or more in a dimension is cut to its low bits, without an
+// error, so more rows than this are taken in turns.
+constexpr int64_t MAX_GROUPS = 1 << 20;
+
 template <typename Z, typename Y, typename R>
 kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
-  const int64_t blocks = std::min<int64_t>(ceil_div(a.rows * a.chunks, 256), 1 << 30);
+  const int64_t blocks = std::min(ceil_div(a.rows * a.chunks, 256), MAX_GROUPS);
   const auto kernel = streams(a.rows, a.top, a.n, sizeof(Z)) ? combine_kernel<Z, Y, R, true> : combine_kernel<Z, Y, R, false>;
   kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
   KQ_LAUNCHED("combine_kernel");
@@ -238,7 +243,7 @@ kq_status launch_backward(const BackArgs& a, hipStream_t s) {
   const bool stream = streams(a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 4;
   const auto kernel = wide ? (stream ? combine_backward_kernel<D, Z, 4, KB, true> : combine_backward_kernel<D, Z, 4, KB, false>)
                            : (stream ? combine_backward_kernel<D, Z, 1, KB, true> : combine_backward_kernel<D, Z, 1, KB, false>);
-  kernel<<<dim3((unsigned)a.rows), dim3(wide ? 256 : 64), 0, s>>>(a);
+  kernel<<<dim3((unsigned)std::min(a.rows, MAX_GROUPS)), dim3(wide ? 256 : 64), 0, s>>>(a);
   KQ_LAUNCHED("combine_backward_kernel");
   return KQ_OK;
 }
