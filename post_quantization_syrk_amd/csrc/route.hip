@@ -761,7 +761,7 @@ struct RouteRows {
     RouteArgs a = r.a;
     const size_t lds = sizeof(int) * ((size_t)(WAVES + 2) * a.experts + 1);
     const auto kernel = route_rows_kernel<T, LPR, VPL, WAVES>;
-    if (lds > 64 * 1024)
+    if (lds > 64 * 1024 - 256)   // (beside it `used` and `shared`, up to 96 bytes)
       KQ_HIP(hipFuncSetAttribute((const void*)kernel, hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds));
     kernel<<<dim3((unsigned)a.chunks), dim3(64 * WAVES), lds, r.s>>>(a);
     KQ_LAUNCHED("route_rows_kernel");

@@ -4,9 +4,11 @@ sizes next to a limit of the launch, gradients over many rows of each lane layou
 Results are exact where nothing is rounded (one choice, no weights: a row of z or dy itself, and products of
 two bf16 values, which fp32 holds); the other bounds are those of test_gpu_mixture.py.
 """
+import numpy as np
 import pytest
 
 from tests.gpu_util import announce, torch_cuda
+from tests.test_gpu_mixture import Routes, _dev, _logits, _route_back_check, _route_check
 
 pytestmark = pytest.mark.gpu
 
@@ -72,3 +74,22 @@ def test_combine_of_more_columns_than_threads():
     want = table[pattern.long()]
     for at in range(0, rows, 1 << 24):
         assert bool((y[at:at + (1 << 24)].view(-1, 1 << 16, n) == want).all()), at
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", [1635, 1636, 1637, 1638, 1639])
+def test_route_next_to_64_kb_of_counts(experts, kind):
+    """Experts whose counts take about 64 KB of LDS, with what the kernel holds beside them or without."""
+    announce(f"route 70 x {experts} {kind}")
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(experts)
+    for rows in (70, 6):
+        x = _logits(rng, rows, experts, kind, True)
+        r = Routes(rows, experts, 5)
+        kq.kq_route(x.cuda(), normalize=True, **r.dict())
+        want = _route_check(r, x, 5, True)
+        dw, dloss = rng.standard_normal((rows, 5)).astype(np.float32), np.float32(2.0)
+        g = torch.full((rows, experts), 7.0, dtype=x.dtype, device="cuda")
+        kq.kq_route_backward(x.cuda(), g, r.weight, r.expert, r.counts, dweight=_dev(dw), dloss=_dev(dloss.reshape(1)), normalize=True)
+        _route_back_check(g, x, want, dw, dloss, True, kind)
