@@ -8,7 +8,7 @@ import numpy as np
 import pytest
 
 from tests.gpu_util import announce, torch_cuda
-from tests.test_gpu_mixture import Routes, _dev, _logits, _route_back_check, _route_check
+from tests.test_gpu_mixture import INF, U, Routes, _dev, _half, _logits, _route_back_check, _route_check
 
 pytestmark = pytest.mark.gpu
 
@@ -93,3 +93,54 @@ def test_route_next_to_64_kb_of_counts(experts, kind):
         g = torch.full((rows, experts), 7.0, dtype=x.dtype, device="cuda")
         kq.kq_route_backward(x.cuda(), g, r.weight, r.expert, r.counts, dweight=_dev(dw), dloss=_dev(dloss.reshape(1)), normalize=True)
         _route_back_check(g, x, want, dw, dloss, True, kind)
+
+
+# (rows so many that every wave of the gradient's kernel has several groups of them, and no whole number; a
+# case for each number of lanes a row and of values a lane)
+MANY = [(70_001, 8, 2), (50_003, 30, 9), (99_998, 60, 4), (40_007, 100, 16), (131_075, 256, 8), (20_005, 300, 6), (17_001, 1000, 9),
+        (9_001, 2000, 3), (12_291, 4000, 16)]
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("normalize", [False, True])
+@pytest.mark.parametrize("rows,experts,top", MANY)
+def test_route_gradient_of_many_rows(rows, experts, top, normalize, kind):
+    """Against the formula in 64 bits on the device, with the choices that kq_route made."""
+    announce(f"route gradient {rows}x{experts} top {top} {kind} normalize {normalize}")
+    torch = torch_cuda()
+    kq = _kq()
+    gen = torch.Generator(device="cuda").manual_seed(rows + normalize)
+    x = 2 * torch.randn(rows, experts, generator=gen, device="cuda") + torch.randn(experts, generator=gen, device="cuda")
+    x[torch.rand(rows, experts, generator=gen, device="cuda") < 0.2] = -INF
+    x[torch.rand(rows, generator=gen, device="cuda") < 0.05] = -INF
+    x = x.to(torch.bfloat16 if kind == "bf16" else torch.float32)
+    dw, dloss = torch.randn(rows, top, generator=gen, device="cuda"), torch.full((1,), 0.3 * rows, device="cuda")
+    r = Routes(rows, experts, top)
+    kq.kq_route(x, normalize=normalize, **r.dict())
+    g = torch.full_like(x, 7.0)
+    kq.kq_route_backward(x, g, r.weight, r.expert, r.counts, dweight=dw, dloss=dloss, normalize=normalize)
+
+    v = x.double()
+    most = v.amax(1, keepdim=True)
+    there = v > -INF
+    far = torch.where(there, most - v, 0.0).max()
+    e = torch.where(there, torch.exp(v - torch.where(most > -INF, most, 0.0)), 0.0)
+    total = e.sum(1, keepdim=True)
+    p = e / torch.where(total > 0, total, 1.0)
+    chosen = r.expert >= 0
+    at = r.expert.clamp(min=0).long()
+    w = torch.where(chosen, e.gather(1, at), 0.0)
+    under = w.sum(1, keepdim=True) if normalize else total
+    w = w / torch.where(under > 0, under, 1.0)
+    dw64 = torch.where(chosen, dw.double(), 0.0)
+    made, used = max(int(r.counts[experts]), 1), max(int(r.counts[experts + 1]), 1)
+    b = float(dloss) * experts * r.counts[:experts].double() / (float(made) * used)
+    wg = (w * dw64).sum(1, keepdim=True)
+    want = p * (b - (p * b).sum(1, keepdim=True) - (0.0 if normalize else wg))
+    want.scatter_add_(1, at, w * (dw64 - wg) if normalize else w * dw64)      # (missing choices add zero)
+    size_of = (w * dw64).abs()
+    size = p * (b + (p * b).sum(1, keepdim=True) + size_of.sum(1, keepdim=True))
+    size.scatter_add_(1, at, size_of + w * size_of.sum(1, keepdim=True))
+    bound = (4 * far + 2 * experts + 2 * top + 64) * U * size + _half(kind) * want.abs() + 2.0 ** -126
+    over = (g.double() - want).abs() - bound
+    assert bool((over <= 0).all()), float(over.max())
