@@ -611,7 +611,7 @@ struct BackArgs {
 
 // The logits' gradient, dl_e = p_e (b_e - back) + [e chosen] extra, by the lanes that hold the row.
 // Bound by HBM: 131072 x 256 fp32, top 8, 52 us, 5.2 TB/s (each lane comparing its columns with every
-// choice: 61 us, and 48 for the bf16 that takes 38 so).
+// choice: 61 us, and 48 for the bf16 that takes 32 so).
 template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArgs a) {
   using R = Row<LPR, VPL>;
@@ -661,7 +661,8 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArg
       sum += x[v];
     }
     sum = row_sum<LPR>(sum);
-    const float inv = sum == 0.f ? 0.f : 1.f / sum;   // (no logit above -inf: every p is 0)
+    const bool none = sum == 0.f;   // (no logit above -inf)
+    const float inv = 1.f / sum;
 #pragma unroll
     for (int v = 0; v < VPL; ++v) {
       x[v] *= inv;
@@ -672,7 +673,7 @@ __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArg
     const float back = a.normalize ? dot : dot + wg;
     const float extra = a.normalize ? w * (g - wg) : w * g;
 #pragma unroll
-    for (int v = 0; v < VPL; ++v) x[v] *= b[v] - back;
+    for (int v = 0; v < VPL; ++v) x[v] = none ? 0.f : x[v] * (b[v] - back);   // (zero beside a dloss of inf or NaN too)
     if (a.dweight) {
       // the chosen columns' part goes to the lanes that hold them through LDS, which is zero else
       const bool adds = l < a.top && chosen >= 0 && chosen < a.experts;

@@ -144,3 +144,31 @@ def test_route_gradient_of_many_rows(rows, experts, top, normalize, kind):
     bound = (4 * far + 2 * experts + 2 * top + 64) * U * size + _half(kind) * want.abs() + 2.0 ** -126
     over = (g.double() - want).abs() - bound
     assert bool((over <= 0).all()), float(over.max())
+
+
+@pytest.mark.parametrize("kind", ["f32", "bf16"])
+@pytest.mark.parametrize("dloss", [INF, -INF, np.nan])
+@pytest.mark.parametrize("experts", [7, 64, 256, 900])
+def test_route_gradient_of_padding_beside_a_loss_that_is_not_finite(experts, dloss, kind):
+    """Rows without a logit above -inf get zeros whatever comes back from the loss; choices that are missing
+    take nothing from their weights' gradients."""
+    torch = torch_cuda()
+    kq = _kq()
+    rng = np.random.default_rng(experts)
+    x = _logits(rng, 60, experts, kind, False).cuda()
+    padding = [0, 5, 17, 58, 59]
+    x[padding] = -INF
+    x[30, 1:] = -INF                       # (one choice of its three)
+    dw = torch.ones(60, 3, device="cuda")
+    dw[padding], dw[30, 1:] = np.nan, np.nan
+    for normalize in (False, True):
+        r = Routes(60, experts, 3)
+        kq.kq_route(x, normalize=normalize, **r.dict())
+        g = torch.full_like(x, 7.0)
+        kq.kq_route_backward(x, g, r.weight, r.expert, r.counts, dweight=dw, normalize=normalize,
+                             dloss=torch.full((1,), dloss, device="cuda"))
+        assert not g[padding].any()
+        rest = [t for t in range(60) if t not in padding]
+        assert not torch.isfinite(g[rest]).all(1).any()
+        kq.kq_route_backward(x, g, r.weight, r.expert, r.counts, dweight=dw, normalize=normalize)
+        assert torch.isfinite(g).all() and not g[padding].any()
