@@ -32,8 +32,8 @@ __device__ __forceinline__ unsigned pair(float lo, float hi) { return __builtin_
 __device__ __forceinline__ void put(float v, float& to) { to = v; }
 __device__ __forceinline__ void put(float v, uint16_t& to) { to = __builtin_bit_cast(uint16_t, (__bf16)v); }
 
-// Columns c .. c + 7 of a row of n (zeros past its end).  STREAM: past the caches, which hold nothing
-// of calls this large for whoever comes next.
+// Columns c .. c + 7 of a row of n (zeros past its end).  STREAM: past the caches
+// (streams() below).
 template <bool STREAM, typename T>
 __device__ __forceinline__ Pack<T> load(const T* row, int64_t c, int64_t n) {
   Pack<T> k{};
@@ -220,10 +220,14 @@ kq_status check_choices(const char* fn, int z_type, int64_t slots, int64_t n, in
   return KQ_OK;
 }
 
-// Whether the rows of z are more than the last cache (256 MB) holds: then nothing is kept in it
-// (32768 x 2048, top 6, bf16 with both gradients, 805 MB of z: 517 to 524 us, through the caches 553; 4099 x
-// 4100, top 2, 67 MB: 40 to 42 us either way, and what is written may be read next).
-bool streams(int64_t rows, int64_t top, int64_t n, size_t size) { return rows * top * n * (int64_t)size > ((int64_t)256 << 20); }
+// Whether the rows of z that a call can name are more than the last cache (256 MB) holds: then nothing is kept
+// in it, y included.  32768 x 2048, top 6, bf16, 805 MB of z: the sum 190 us, through the caches 211; with a
+// pass that reads y after it 233 and 262, and 239 with y alone through the caches; both gradients 353 and 358.
+// z of 4096 rows there, 17 MB, each named by 48 choices: 172 us past the caches, 131 through them.  4099 x
+// 4100, top 2, 67 MB of z: 40 to 42 us either way.
+bool streams(int64_t slots, int64_t rows, int64_t top, int64_t n, size_t size) {
+  return std::min(slots, rows * top) * n * (int64_t)size > ((int64_t)256 << 20);
+}
 
 // Workgroups of a launch: a grid of 2^32 threads or more in a dimension is cut to its low bits, without an
 // error, so more rows than this are taken in turns.
@@ -232,7 +236,7 @@ constexpr int64_t MAX_GROUPS = 1 << 20;
 template <typename Z, typename Y, typename R>
 kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
   const int64_t blocks = std::min(ceil_div(a.rows * a.chunks, 256), MAX_GROUPS);
-  const auto kernel = streams(a.rows, a.top, a.n, sizeof(Z)) ? combine_kernel<Z, Y, R, true> : combine_kernel<Z, Y, R, false>;
+  const auto kernel = streams(a.slots, a.rows, a.top, a.n, sizeof(Z)) ? combine_kernel<Z, Y, R, true> : combine_kernel<Z, Y, R, false>;
   kernel<<<dim3((unsigned)blocks), dim3(256), 0, s>>>(a);
   KQ_LAUNCHED("combine_kernel");
   return KQ_OK;
@@ -240,7 +244,7 @@ kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
 
 template <typename D, typename Z, int KB>
 kq_status launch_backward(const BackArgs& a, hipStream_t s) {
-  const bool stream = streams(a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 4;
+  const bool stream = streams(a.slots, a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 4;
   const auto kernel = wide ? (stream ? combine_backward_kernel<D, Z, 4, KB, true> : combine_backward_kernel<D, Z, 4, KB, false>)
                            : (stream ? combine_backward_kernel<D, Z, 1, KB, true> : combine_backward_kernel<D, Z, 1, KB, false>);
   kernel<<<dim3((unsigned)std::min(a.rows, MAX_GROUPS)), dim3(wide ? 256 : 64), 0, s>>>(a);

@@ -172,3 +172,26 @@ def test_route_gradient_of_padding_beside_a_loss_that_is_not_finite(experts, dlo
         assert not torch.isfinite(g[rest]).all(1).any()
         kq.kq_route_backward(x, g, r.weight, r.expert, r.counts, dweight=dw, normalize=normalize)
         assert torch.isfinite(g).all() and not g[padding].any()
+
+
+@pytest.mark.parametrize("zk,yk,rows,n,top,slots", [("bf16", "bf16", 16384, 2048, 6, 300), ("f32", "bf16", 9000, 4099, 8, 1), ("bf16", "f32", 70_000, 1025, 2, 140_001)])
+def test_combine_of_slots_that_many_rows_name(zk, yk, rows, n, top, slots):
+    """Few rows of z behind many choices, and more slots than choices: the sums in the order of the choices."""
+    announce(f"combine {rows}x{n} top {top} of {slots} slots {zk} {yk}")
+    torch = torch_cuda()
+    kq = _kq()
+    gen = torch.Generator(device="cuda").manual_seed(n)
+    kind = {"bf16": torch.bfloat16, "f32": torch.float32}
+    z = torch.randn(slots, n, generator=gen, device="cuda").to(kind[zk])
+    slot = torch.randint(-1, slots + 1, (rows, top), generator=gen, device="cuda", dtype=torch.int32)    # (either end: none)
+    weight = torch.randn(rows, top, generator=gen, device="cuda")
+    y = torch.full((rows, n), 7.0, dtype=kind[yk], device="cuda")
+    kq.kq_combine(z, slot, y, weight=weight)
+    want, size = torch.zeros(rows, n, dtype=torch.float64, device="cuda"), torch.zeros(rows, n, dtype=torch.float64, device="cuda")
+    for j in range(top):
+        there = (slot[:, j] >= 0) & (slot[:, j] < slots)
+        term = z[slot[:, j].clamp(0, slots - 1).long()].double() * torch.where(there, weight[:, j].double(), 0.0)[:, None]
+        want += term
+        size += term.abs()
+    bound = (top + 2) * U * size
+    assert bool(((y.double() - want).abs() <= bound * (1 + _half(yk)) + _half(yk) * want.abs() + 2.0 ** -126).all())
