@@ -134,8 +134,9 @@ struct BackArgs {
 
 // dz[slot] = weight dy, dweight = <dy, z[slot]>: a row per workgroup of WAVES, KB choices at a time, whose
 // reads go out together, each choice's slot being the same for all lanes; dy is read once for all of
-// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 341 us, 5.1 TB/s.  One wave a row up to 2048 columns
-// (no barrier), four above.
+// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 325 us, 5.4 TB/s.  One wave a row up to 1536 columns, which it
+// takes in three passes and without a barrier, four above (bf16, top 8: 16384 rows of 1024 121 us, with four
+// waves 130, of 1536 173 and 171, of 2048 247 and 229; 64 rows of 2048 10 and 6, of 16384 60 and 20).
 template <typename D, typename Z, int WAVES, int KB, bool STREAM>
 __global__ __launch_bounds__(64 * WAVES) void combine_backward_kernel(BackArgs a) {
   __shared__ float sums[WAVES][KB];
@@ -244,7 +245,7 @@ kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
 
 template <typename D, typename Z, int KB>
 kq_status launch_backward(const BackArgs& a, hipStream_t s) {
-  const bool stream = streams(a.slots, a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 4;
+  const bool stream = streams(a.slots, a.rows, a.top, a.n, sizeof(Z)), wide = a.n > 64 * VEC * 3;
   const auto kernel = wide ? (stream ? combine_backward_kernel<D, Z, 4, KB, true> : combine_backward_kernel<D, Z, 4, KB, false>)
                            : (stream ? combine_backward_kernel<D, Z, 1, KB, true> : combine_backward_kernel<D, Z, 1, KB, false>);
   kernel<<<dim3((unsigned)std::min(a.rows, MAX_GROUPS)), dim3(wide ? 256 : 64), 0, s>>>(a);
