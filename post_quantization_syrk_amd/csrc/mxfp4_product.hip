@@ -429,8 +429,10 @@ __global__ __launch_bounds__(128 * WC, WC == 4 || EPI != EPI_NONE ? 2 : 1) void 
       const int r = min(64 * (wave % MT) + lane, nt.last - 1 - nt.m0);
       copy_lds<4>(rsrc(a.index + nt.m0, (int)ALL), 4 * r, (uint8_t*)(next_index + 64 * (wave % MT)));
     }
-    // The tile's bias, by column, behind the next one's in time: waves may still read the last
-    // tile's.  Older than every copy of this tile's last stage, it has landed when that one's have.
+    // The tile's bias, by column; in two places by turns, since waves may still read the last tile's.
+    // Each stage issues COPIES after its wait, so RING - 1 stages' are newer than the bias when a round's last
+    // stage waits, and that wait leaves NEWER = (RING - 2) COPIES outstanding: the bias has landed, and the barrier
+    // behind the wait shows it to every wave, with one round as with several.
     if (EPI != EPI_NONE && a.bias) {
       const int c = 64 * (wave % (BN / 64));
       copy_lds<4>(rsrc(a.bias + (int64_t)t.e * a.N + first_row<EPI>(t.n0), (int)ALL),
