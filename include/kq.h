@@ -609,7 +609,7 @@ kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
  *   normalize = 1   exp(l[c_j] - m) / sum_i exp(l[c_i] - m)
  * A slot is given to every choice, sorted by expert, then by row, then by j.  The balance loss is
  *   L = experts sum_e f_e P_e,  f_e = count_e / N,  P_e = sum_t p[t, e] / R
- * over the N choices and the R rows that have a logit above -inf (0 if there are none): 1 where the
+ * over the N choices and the R rows that are not -inf throughout (0 if there are none): 1 where the
  * experts are equally busy or equally probable.  A row with a NaN or +inf has no softmax: its choices
  * are missing, and its weights and the loss are NaN.
  *
@@ -624,8 +624,8 @@ kq_status kq_route_workspace(int64_t rows, int experts, int top, size_t* bytes);
  *   ws       device workspace, 16-byte aligned, ws_bytes >= kq_route_workspace(...); may be NULL where
  *            that is 0
  * Sizes: rows >= 0, rows * top < 2^31, 1 <= experts <= 4096, 1 <= top <= min(experts, 16).  Asynchronous
- * on `stream`; the same inputs give the same bits (no order depends on atomics).  The outputs must not
- * overlap each other or the inputs.
+ * on `stream`; the same inputs give the same bits (no order depends on atomics), but the last bits of a row's
+ * weights may depend on the rows around it.  The outputs must not overlap each other or the inputs.
  */
 kq_status kq_route(const void* logits, int type, int64_t rows, int experts, int64_t ld, int top, int normalize,
                    float* weight, int32_t* expert, int32_t* slot, int32_t* index, int32_t* offsets,
@@ -657,10 +657,11 @@ kq_status kq_route_backward(const void* logits, int type, int64_t rows, int expe
  *   y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]],   in fp32, j ascending, rounded once to y_type.
  *
  *   z        device, slots x n of z_type (KQ_F32 or KQ_BF16), leading dim ldz >= n
- *   slot     device int32 [rows][top]; one outside [0, slots) stands for a row of zeros
+ *   slot     device int32 [rows][top]; one outside [0, slots) stands for a row of zeros, whose product with a
+ *            weight of infinity or NaN is NaN as that with a zero of z is (kq_route's NaN weights reach y)
  *   weight   device fp32 [rows][top], or NULL for 1
  *   residual device, rows x n of residual_type, leading dim ldr >= n, or NULL for 0; it may be y itself
- *            (the same address, type and leading dim)
+ *            (the same address, type and leading dim), else it must not overlap y
  *   y        device, rows x n of y_type, leading dim ldy >= n; must not overlap z
  * All aligned to their type.  Sizes: 0 <= rows, slots <= 2^30, rows * top < 2^31, 1 <= n <= 2^24,
  * 1 <= top <= 64.  Asynchronous on `stream`; the same inputs give the same bits.
