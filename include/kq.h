@@ -168,7 +168,8 @@ kq_status kq_sensitivity_async(const float* HX, int64_t n_in, int64_t ldx, const
  *   alpha            rescale exponent (0.25 for weight-only KronQ)
  *   mode             KQ_BIIP_*
  *   d_in, d_out      device fp32 outputs, lengths in / out (1 where not rescaled)
- * Sizes: 1 <= in, out; in and out must be multiples of 4.
+ * Sizes: 1 <= in, out; in and out must be multiples of 4.  A matrix whose rows are transformed has fewer than
+ * 2^34 entries in blocks of 4, 2^35 in blocks of 8 or 2048, 2^36 in others (KQ_ESHAPE before any launch).
  */
 kq_status kq_biip_rotate(const float* W_src, float* W_dst, int64_t out, int64_t in,
                          const float* HX_src, float* HX_dst, const float* HG_src, float* HG_dst,

@@ -230,10 +230,6 @@ bool streams(int64_t slots, int64_t rows, int64_t top, int64_t n, size_t size) {
   return std::min(slots, rows * top) * n * (int64_t)size > ((int64_t)256 << 20);
 }
 
-// Workgroups of a launch: a grid of 2^32 threads or more in a dimension is cut to its low bits, without an
-// error, so more rows than this are taken in turns.
-constexpr int64_t MAX_GROUPS = 1 << 20;
-
 template <typename Z, typename Y, typename R>
 kq_status launch_combine(const CombineArgs& a, hipStream_t s) {
   const int64_t blocks = std::min(ceil_div(a.rows * a.chunks, 256), MAX_GROUPS);

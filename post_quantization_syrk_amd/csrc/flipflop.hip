@@ -263,39 +263,41 @@ __global__ __launch_bounds__(256) void qform_kernel(QArgs a) {
 // bf16(a - bf16(a)) (round to nearest even; the remainder is exact in fp32); one workgroup per
 // token, 8 channels per thread and step.
 __global__ __launch_bounds__(256) void ff_scale_kernel(const uint16_t* __restrict__ S, int64_t lds,
-                                                       int k, const float* __restrict__ part,
+                                                       int64_t T, int k, const float* __restrict__ part,
                                                        int np, float c, uint16_t* __restrict__ out,
                                                        int64_t ldo) {
-  const int64_t t = blockIdx.x;
   __shared__ float sf;
-  if (threadIdx.x < 64) {
-    float w = 0.f;
-    for (int p = threadIdx.x; p < np; p += 64) w += part[t * np + p];
+  for (int64_t t = blockIdx.x; t < T; t += gridDim.x) {
+    if (threadIdx.x < 64) {
+      float w = 0.f;
+      for (int p = threadIdx.x; p < np; p += 64) w += part[t * np + p];
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) w += __shfl_xor(w, o);
-    if (threadIdx.x == 0) sf = c * w;
-  }
-  __syncthreads();
-  const float f = sf;
-  for (int i = 8 * threadIdx.x; i < k; i += 8 * 256) {
-    const u32x4 v = *(const u32x4*)(S + t * lds + i);
-    u32x4 oh, ol;
-#pragma unroll
-    for (int h = 0; h < 4; ++h) {
-      unsigned rh = 0, rl = 0;
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const float x = __uint_as_float(((v[h] >> (16 * e)) & 0xffffu) << 16) * f;
-        const unsigned hi = bf16_rne(x);
-        const unsigned lo = bf16_rne(x - __uint_as_float(hi << 16));
-        rh |= hi << (16 * e);
-        rl |= lo << (16 * e);
-      }
-      oh[h] = rh;
-      ol[h] = rl;
+      for (int o = 32; o > 0; o >>= 1) w += __shfl_xor(w, o);
+      if (threadIdx.x == 0) sf = c * w;
     }
-    *(u32x4*)(out + t * ldo + i) = oh;
-    *(u32x4*)(out + t * ldo + k + i) = ol;
+    __syncthreads();
+    const float f = sf;
+    for (int i = 8 * threadIdx.x; i < k; i += 8 * 256) {
+      const u32x4 v = *(const u32x4*)(S + t * lds + i);
+      u32x4 oh, ol;
+#pragma unroll
+      for (int h = 0; h < 4; ++h) {
+        unsigned rh = 0, rl = 0;
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float x = __uint_as_float(((v[h] >> (16 * e)) & 0xffffu) << 16) * f;
+          const unsigned hi = bf16_rne(x);
+          const unsigned lo = bf16_rne(x - __uint_as_float(hi << 16));
+          rh |= hi << (16 * e);
+          rl |= lo << (16 * e);
+        }
+        oh[h] = rh;
+        ol[h] = rl;
+      }
+      *(u32x4*)(out + t * ldo + i) = oh;
+      *(u32x4*)(out + t * ldo + k + i) = ol;
+    }
+    __syncthreads();   // (sf is the next token's from here on)
   }
 }
 
@@ -331,8 +333,8 @@ __global__ __launch_bounds__(256) void to_bf16_pair_kernel(const float* __restri
 }
 
 __global__ void identity_kernel(float* __restrict__ M, int64_t k) {
-  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (i < k * k) M[i] = (i / k == i % k) ? 1.f : 0.f;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < k * k; i += (int64_t)gridDim.x * 256)
+    M[i] = (i / k == i % k) ? 1.f : 0.f;
 }
 
 struct Workspace {
@@ -437,7 +439,7 @@ kq_status half_step(const float* M, const uint16_t* S2, int64_t ld2, int64_t k2,
   KQ_TRY(pt.mark(s));
   const int np = 2 * (int)((k2 + QT - 1) / QT);
   const float c = (float)(1.0 / ((double)T * (double)k2));
-  ff_scale_kernel<<<dim3((unsigned)T), dim3(256), 0, s>>>(S1, ld1, (int)k1, w.part, np, c, w.Ss, w.ldS);
+  ff_scale_kernel<<<dim3((unsigned)std::min(T, MAX_GROUPS)), dim3(256), 0, s>>>(S1, ld1, T, (int)k1, w.part, np, c, w.Ss, w.ldS);
   KQ_LAUNCHED("ff_scale_kernel");
   KQ_TRY(pt.mark(s));
   KQ_TRY(gram_lower(w.Ss, w.ldS, S1, ld1, T, k1, out, k1, false, false, s));
@@ -501,7 +503,7 @@ extern "C" kq_status kq_flipflop(const uint16_t* X, int64_t ldx, const uint16_t*
   layout(T, n, m, (char*)ws, &w);
   hipStream_t s = as_stream(stream);
   KQ_HIP(hipMemsetAsync(w.flag, 0, sizeof(int), s));
-  identity_kernel<<<dim3((unsigned)ceil_div(m * m, 256)), dim3(256), 0, s>>>(B, m);
+  identity_kernel<<<dim3((unsigned)std::min(ceil_div(m * m, 256), MAX_GROUPS)), dim3(256), 0, s>>>(B, m);
   KQ_LAUNCHED("identity_kernel");
   PhaseTimer pt;
   pt.on = phase_ms != nullptr;

@@ -30,6 +30,8 @@
 
 #include <math.h>
 
+#include <algorithm>
+
 namespace kq {
 namespace {
 
@@ -572,16 +574,16 @@ __global__ __launch_bounds__(NT) void row_fwht8192_kernel(const float* __restric
 __global__ __launch_bounds__(NT) void scale_kernel(const float* __restrict__ src,
                                                    float* __restrict__ dst, int64_t rows,
                                                    int64_t n, Scale rs, Scale cs) {
-  const int64_t i4 = ((int64_t)blockIdx.x * NT + threadIdx.x) * 4;
-  if (i4 >= rows * n) return;
-  const int64_t r = i4 / n, c = i4 % n;
-  const float a = scale_at(rs, r);
-  float4 q = *(const float4*)(src + i4);
-  q.x *= a * scale_at(cs, c);
-  q.y *= a * scale_at(cs, c + 1);
-  q.z *= a * scale_at(cs, c + 2);
-  q.w *= a * scale_at(cs, c + 3);
-  *(float4*)(dst + i4) = q;
+  for (int64_t i4 = ((int64_t)blockIdx.x * NT + threadIdx.x) * 4; i4 < rows * n; i4 += (int64_t)gridDim.x * NT * 4) {
+    const int64_t r = i4 / n, c = i4 % n;
+    const float a = scale_at(rs, r);
+    float4 q = *(const float4*)(src + i4);
+    q.x *= a * scale_at(cs, c);
+    q.y *= a * scale_at(cs, c + 1);
+    q.z *= a * scale_at(cs, c + 2);
+    q.w *= a * scale_at(cs, c + 3);
+    *(float4*)(dst + i4) = q;
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -777,7 +779,7 @@ kq_status row_transform(const float* src, float* dst, int64_t rows, int64_t n, i
                         Scale rs, Scale cs, hipStream_t s) {
   if (b <= 1) {
     const int64_t tot4 = rows * n / 4;
-    scale_kernel<<<dim3((unsigned)ceil_div(tot4, NT)), dim3(NT), 0, s>>>(src, dst, rows, n, rs, cs);
+    scale_kernel<<<dim3((unsigned)std::min(ceil_div(tot4, NT), MAX_GROUPS)), dim3(NT), 0, s>>>(src, dst, rows, n, rs, cs);
     KQ_LAUNCHED("scale_kernel");
     return KQ_OK;
   }
@@ -876,6 +878,15 @@ extern "C" kq_status kq_biip_rotate(const float* W_src, float* W_dst, int64_t ou
   if (do_out && !valid_block(out, bout))
     return fail(KQ_ESHAPE, "kq_biip_rotate: output Hadamard block %lld does not tile out=%lld",
                 (long long)bout, (long long)out);
+  // a row transform takes a thread for 4 to 16 values (row_transform), of which a launch has less than 2^32
+  auto too_many = [](int64_t rows, int64_t n, int64_t b) {
+    const int64_t values = b <= 16 ? b : b == 2048 ? 8 : 16;
+    return b > 1 && rows * n / values > ((int64_t)1 << 32) - NT;
+  };
+  if (do_in && (too_many(out, in, bin) || too_many(in, in, bin)))
+    return fail(KQ_ESHAPE, "kq_biip_rotate: %lld x %lld in blocks of %lld", (long long)out, (long long)in, (long long)bin);
+  if (do_out && too_many(out, out, bout))
+    return fail(KQ_ESHAPE, "kq_biip_rotate: %lld x %lld in blocks of %lld", (long long)out, (long long)out, (long long)bout);
   hipStream_t s = as_stream(stream);
 
   // 1. rescale vectors (norms of the original W, diagonals of the raw factors)

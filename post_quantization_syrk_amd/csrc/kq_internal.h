@@ -18,6 +18,10 @@ inline hipStream_t as_stream(void* s) { return reinterpret_cast<hipStream_t>(s);
 
 inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Workgroups of a launch that grows with the data.  A grid of 2^32 threads or more in a dimension is cut to its
+// low bits, without an error, so its kernel takes what lies behind in turns.
+constexpr int64_t MAX_GROUPS = 1 << 20;
+
 inline bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 
 // Number of compute units of the current device (cached per device).
