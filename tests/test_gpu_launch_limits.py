@@ -66,3 +66,31 @@ def test_scaling_of_more_weights_than_threads():
     want = base * sign.float()
     for at in range(0, out, 1 << 18):
         assert bool((W[at:at + (1 << 18)].view(-1, 4, n) == want).all()), at
+
+
+def test_reordered_columns_of_more_than_65535_rows():
+    """act_order with 70000 output channels through the path of rows too long for LDS, where rows lie along
+    the grid's second dimension: the bits of the path through LDS."""
+    announce("gptq act_order 70000 x 256")
+    torch = torch_cuda()
+    kq = _kq()
+    out, n = 70_000, 256
+    gen = torch.Generator(device="cuda").manual_seed(7)
+    W0 = torch.randn(out, n, generator=gen, device="cuda")
+    X = torch.randn(2000, n, generator=gen, device="cuda") * torch.rand(n, generator=gen, device="cuda")
+    H = X.T @ X + torch.eye(n, device="cuda")
+    p = kq.make_params(4, n, 128, 0.01, act_order=1)
+    ws = torch.empty(kq.kq_quantize_layer_workspace(p, out, n, False), dtype=torch.uint8, device="cuda")
+
+    def run():
+        W, codes = W0.clone(), torch.empty((out, n), dtype=torch.uint8, device="cuda")
+        packed = torch.empty((out, n * 4 // 32), dtype=torch.int32, device="cuda")
+        scales, zeros = torch.empty((out, 1), device="cuda"), torch.empty((out, 1), dtype=torch.uint8, device="cuda")
+        kq.kq_quantize_layer(p, W, H.clone(), None, packed, scales, zeros, ws, codes=codes)
+        return W, codes, packed, scales, zeros
+
+    want = run()
+    with kq.testing_select(kq.KQ_TESTING_ROW_LDS_BYTES, 0):
+        got = run()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
