@@ -305,13 +305,14 @@ kq_status mx_few_product(const ProductArgs& p, const MxRows& x, int64_t block, b
   RowArgs r{x.x, x.ld, x.n, x.d, x.sign, (int)block, (float)(1.0 / sqrt((double)block))};
   const int bm = fused || average_rows(p) <= 16 ? 16 : 32;
   // Columns per workgroup, 16 to 64: more of them serve its rows of x and its fixed costs, which are worth
-  // about 16 columns; and what the busiest compute unit has to do counts (16 rows, 4096 x 4096: 3.7 us
-  // with 16, 6.5 with 64; 28672 x 8192: 30 and 24).
-  const int64_t tm = even_tiles(p, bm), cus = device_cu_count();
+  // about 16 columns, and 48 where it quantises the rows too; and what the busiest compute unit has to do
+  // counts (16 rows, 4096 x 4096: 3.7 us with 16, 6.5 with 64; 28672 x 8192: 30 and 24; 6 experts of 4096 x 1024
+  // for a token each, quantised here: 11.9, with 32 9.0, with 64 7.0).
+  const int64_t tm = even_tiles(p, bm), cus = device_cu_count(), fixed = fused ? 48 : 16;
   int nt = 1;
   int64_t least = 0;
   for (int k = bm == 32 ? 2 : 4; k > 0; --k) {
-    const int64_t cost = ceil_div(ceil_div(p.N, 16 * k) * tm, cus) * (16 * k + 16);
+    const int64_t cost = ceil_div(ceil_div(p.N, 16 * k) * tm, cus) * (16 * k + fixed);
     if (least == 0 || cost < least) {
       least = cost;
       nt = k;
