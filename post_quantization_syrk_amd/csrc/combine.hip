@@ -93,7 +93,7 @@ struct CombineArgs {
 };
 
 // y[t] = residual[t] + sum_j weight[t, j] z[slot[t, j]]: a lane's eight columns of a row, one choice after
-// another, sums in registers.  Bound by HBM: 32768 x 2048, top 6, bf16, 185 us, 5.8 TB/s (a large copy:
+// another, sums in registers.  Bound by HBM: 32768 x 2048, top 6, bf16, 183 us, 5.9 TB/s (a large copy:
 // 4.9); rows that begin inside a dword, 4099 x 4100, top 2, to fp32: 32 us with its inputs in the last
 // cache, 40 without.
 template <typename Z, typename Y, typename R, bool STREAM>
@@ -134,7 +134,7 @@ struct BackArgs {
 
 // dz[slot] = weight dy, dweight = <dy, z[slot]>: a row per workgroup of WAVES, KB choices at a time, whose
 // reads go out together, each choice's slot being the same for all lanes; dy is read once for all of
-// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 325 us, 5.4 TB/s.  One wave a row up to 1536 columns, which it
+// them.  Bound by HBM: 32768 x 2048, top 6, bf16, 322 us, 5.4 TB/s.  One wave a row up to 1536 columns, which it
 // takes in three passes and without a barrier, four above (bf16, top 8: 16384 rows of 1024 121 us, with four
 // waves 130, of 1536 173 and 171, of 2048 247 and 229; 64 rows of 2048 10 and 6, of 16384 60 and 20).
 template <typename D, typename Z, int WAVES, int KB, bool STREAM>

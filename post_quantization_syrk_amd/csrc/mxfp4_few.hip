@@ -72,10 +72,10 @@ __device__ __forceinline__ void quantize_rows(const ProductArgs& a, const RowArg
 // instruction, so its two loads are neighbours, a row's line is read whole, and both blocks'
 // scales lie in one dword.
 // Bound by the layer's bytes and, at these sizes, by the latency of the loads before the first
-// product (16 rows, 11008 x 4096: 24 MB, 7.7 us; 2 experts of it for one token: 48 MB, 15.3 us with
+// product (16 rows, 11008 x 4096: 24 MB, 6.8 us; 2 experts of it for one token: 48 MB, 14.8 us with
 // the token's rotation).
 // EPI: as for the tiles; a gated layer's pair lies in two neighbouring sums of a lane (one token, 4096 to
-// 2 x 11008 with silu: 14.3 us; to 22016 plain: 14.0).
+// 2 x 11008 with silu: 14.6 us; to 22016 plain: 14.0).
 // T: void for quantised activations, else their type, quantised here (MT = 1).
 template <int WAVES, int MT, int NT, int U, bool EXPERTS, typename T, bool WIDE, int EPI>
 __global__ __launch_bounds__(64 * WAVES, 4) void mx_few_kernel(ProductArgs a, RowArgs x) {
@@ -295,8 +295,8 @@ bool mx_few(const ProductArgs& p) {
 }
 
 // One token or two: each workgroup quantises them for itself, while its part of the layer is on
-// the way (one token, 4096 x 4096: 7.5 us, and by a kernel of its own 4.5 + 3.7 and a launch; through
-// two of eight experts of 11008 x 4096: 15.3, and 4.2 + 13.8).
+// the way (one token, 4096 x 4096: 7.5 us, and by a kernel of its own 8.2; through two of eight experts of
+// 11008 x 4096: 14.8 and 17.7; 6 experts of 4096 x 1024 10.2 and 12.2; but 16 rows, 28672 x 512: 14.1 and 10.2).
 bool mx_few_fused(const ProductArgs& p, const MxRows& x) {
   return x.rows > 0 && p.slots <= 16 && p.slots * x.n <= testing_value(KQ_TESTING_MX_FUSED, 8192);
 }

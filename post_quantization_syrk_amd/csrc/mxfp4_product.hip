@@ -149,8 +149,9 @@ __device__ __forceinline__ float other_lane(float v) {
 // since four of 128 x 128, which read a third less from LDS, are 2 % slower.  2048 x 11008 x 4096 with
 // 128 x 128 tiles: 55 us, 3.3 PF; with 256 x 256, on half as many workgroups, 71.
 // EPI: what is done with the sums before they are stored (mxfp4_tiles.h).  A gated silu over 16384 x 4096
-// to 2 x 11008 takes 741 us where the plain product, which stores twice as much, takes 720 to 815; bias and
-// a bf16 residual over 2048 x 11008 to 4096 57 us, plain 52.
+// to 2 x 11008 takes 740 to 837 us where the plain product, which stores twice as much, takes 720 to 893 (MFMA
+// 51 % busy at 1.74 to 1.83 GHz: not power, but what a tile costs beside its products); bias and a bf16
+// residual over 2048 x 11008 to 4096 58 to 63 us, plain 52 to 55.
 // RING: stages in LDS; four where a tile is small (256 x 10496 x 2914: 14 us, with two and more
 // workgroups side by side 21).
 template <int MT, int NT, int WC, int RING, int ROWS, int EPI>

@@ -87,7 +87,9 @@ __device__ __forceinline__ float sigmoid_times(float v, float u) {
 }
 // v Phi(v), Phi the normal distribution: with a = |v|, Phi(-a) = 2^-(a^2 log2(e) / 2 + r(a)), where r
 // grows slowly, from 1 at 0 to 3.9 at 6.  The polynomial is r's, fitted over [0, 6] for the least
-// error of v Phi(v) relative to v (2.3 roundings); past 6, where Phi(-a) < 2^-29, r(6) serves.
+// error of v Phi(v) relative to v (2.4 roundings); past 6, where Phi(-a) < 2^-29, r(6) serves.  Relative
+// to the result, which vanishes there, the error grows to 3e-5 at -3, 1e-3 at -4, 2e-2 at -5 and 0.2 at -6;
+// that of 1 + erf in fp32 to 1e-5, 5e-4, 5e-2 and 1.
 __device__ __forceinline__ float gelu(float v) {
   const float a = fabsf(v), t = fminf(a, 6.f);
   float r = fmaf(-8.4700869e-06f, t, 5.3903324e-05f);

@@ -329,9 +329,9 @@ __device__ __forceinline__ void write_loss(const RouteArgs& a, const int* first,
 // Softmax and choices of a chunk's rows: p_e = exp(l_e - m) / sum exp(l - m), each choice's rank.
 // Sixteen lanes a row, so that its reductions are lane rotations, which cost no more than the operation
 // (64 lanes past 256 experts).  Bound by the vector instructions: 131072 x 256 fp32, top 8, with the
-// loss, 51 us, VALU busy in four cycles of five, where the logits take 26 at 5.2 TB/s (choosing by eight
-// searches for the largest value: 79 us; with the next rows read ahead, which spills, 70); one row of
-// eight experts, all of routing in this launch, 4.0 us.
+// loss, 51 us (59 with the logits from memory), VALU busy in four cycles of five, where the logits take 26 at
+// 5.2 TB/s (choosing by eight searches for the largest value: 79 us; with the next rows read ahead, which
+// spills, 70); one row of eight experts, all of routing in this launch, 4.1 us.
 template <typename T, int LPR, int VPL, int WAVES>
 __global__ __launch_bounds__(64 * WAVES) void route_rows_kernel(RouteArgs a) {
   using R = Row<LPR, VPL>;
@@ -610,7 +610,7 @@ struct BackArgs {
 };
 
 // The logits' gradient, dl_e = p_e (b_e - back) + [e chosen] extra, by the lanes that hold the row.
-// Bound by HBM: 131072 x 256 fp32, top 8, 52 us, 5.2 TB/s (each lane comparing its columns with every
+// Bound by HBM: 131072 x 256 fp32, top 8, 55 us, 5.1 TB/s (each lane comparing its columns with every
 // choice: 61 us, and 48 for the bf16 that takes 32 so).
 template <typename T, int LPR, int VPL>
 __global__ __launch_bounds__(64 * BACK_WAVES) void route_backward_kernel(BackArgs a) {
